@@ -22,7 +22,9 @@ EXPORTS = (
     "qlora_launch_count", "qlora_profile_enable", "qlora_profile_reset", "qlora_profile_read",
     "qlora_profile_kinds", "qlora_profile_read_each",
     "qlora_forward_noalloc", "qlora_merge", "qlora_selftest_wait_timeout", "nf4_dequantize_dtype",
-    "nf4_codebook", "fp4_codebook",
+    "nf4_codebook", "fp4_codebook", "int8_quantize", "int8_dequantize", "int8_matmul",
+    "int8_matmul_backward_workspace_size", "int8_matmul_backward",
+    "qlora_backward_int8_workspace_size", "qlora_backward_int8",
 )
 
 
@@ -40,6 +42,17 @@ class NF4WeightC(ctypes.Structure):
         ("absmax_code", ctypes.c_void_p),
         ("dq_step", ctypes.c_void_p),
         ("dq_mean", ctypes.c_void_p),
+    ]
+
+
+class Int8RowsC(ctypes.Structure):
+    """Mirror of int8_rows_t."""
+    _fields_ = [
+        ("rows", ctypes.c_int64),
+        ("cols", ctypes.c_int64),
+        ("ld", ctypes.c_int64),
+        ("codes", ctypes.c_void_p),
+        ("scales", ctypes.c_void_p),
     ]
 
 
@@ -106,6 +119,22 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.nf4_codebook.argtypes = [ctypes.c_double, P]
     lib.fp4_codebook.restype = ctypes.c_int
     lib.fp4_codebook.argtypes = [P]
+    R = ctypes.POINTER(Int8RowsC)
+    lib.int8_quantize.restype = ctypes.c_int
+    lib.int8_quantize.argtypes = [P, i32, i64, R, P, P]
+    lib.int8_dequantize.restype = ctypes.c_int
+    lib.int8_dequantize.argtypes = [R, i32, P, P]
+    lib.int8_matmul.restype = ctypes.c_int
+    lib.int8_matmul.argtypes = [P, i32, i64, R, R, P, P, i32, P, P]
+    lib.int8_matmul_backward_workspace_size.restype = sz
+    lib.int8_matmul_backward_workspace_size.argtypes = [i64, R]
+    lib.int8_matmul_backward.restype = ctypes.c_int
+    lib.int8_matmul_backward.argtypes = [P, i32, i64, R, P, P, sz, P, P]
+    lib.qlora_backward_int8_workspace_size.restype = sz
+    lib.qlora_backward_int8_workspace_size.argtypes = [i64, W, i32, i32]
+    lib.qlora_backward_int8.restype = ctypes.c_int
+    lib.qlora_backward_int8.argtypes = [R, P, i64, W, P, P, P, i32, ctypes.c_float, i32, P, P, P, P, P,
+                                        sz, P, P]
     _lib = lib
     return lib
 

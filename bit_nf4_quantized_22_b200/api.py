@@ -11,6 +11,7 @@ import ctypes
 from dataclasses import dataclass
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from . import _lib
 from .codebook import nf4_codebook
@@ -95,6 +96,50 @@ class NF4Weight:
             if t is not None:
                 n += t.numel() * t.element_size()
         return n
+
+
+@dataclass
+class Int8Rows:
+    """A matrix in 8-bit rows: row m stands for codes[m] * scales[m].  The rows are
+    tokens for an activation, output channels for a weight Wt:[Dout, Din]."""
+    codes: torch.Tensor    # int8 [rows, cols], unit column stride, row stride a multiple of 16
+    scales: torch.Tensor   # fp32 [rows]
+
+    @staticmethod
+    def empty(rows: int, cols: int, device="cuda") -> "Int8Rows":
+        ld = (cols + 15) // 16 * 16
+        codes = torch.empty(rows, ld, dtype=torch.int8, device=device)[:, :cols]
+        return Int8Rows(codes, torch.empty(rows, dtype=torch.float32, device=device))
+
+    @property
+    def rows(self) -> int:
+        return self.codes.shape[0]
+
+    @property
+    def cols(self) -> int:
+        return self.codes.shape[1]
+
+    @property
+    def device(self) -> torch.device:
+        return self.codes.device
+
+    @property
+    def nbytes(self) -> int:
+        return self.codes.numel() + 4 * self.scales.numel()
+
+    def c_struct(self) -> _lib.Int8RowsC:
+        c, s = self.codes, self.scales
+        if c.dtype != torch.int8 or c.dim() != 2 or s.dtype != torch.float32 or s.dim() != 1:
+            raise TypeError("Int8Rows: codes int8 [rows, cols] and scales fp32 [rows] are needed")
+        if not c.is_cuda or s.device != c.device:
+            raise TypeError("Int8Rows: codes and scales must be CUDA tensors of one device")
+        rows, cols = c.shape
+        if s.shape[0] != rows or not s.is_contiguous():
+            raise ValueError("Int8Rows: one scale a row, contiguous")
+        ld = c.stride(0) if rows > 1 else (max(cols, 1) + 15) // 16 * 16
+        if cols < 1 or (cols > 1 and c.stride(1) != 1) or ld < cols or ld % 16 or c.data_ptr() % 16:
+            raise ValueError("Int8Rows: codes need a unit column stride, and 16-byte aligned rows")
+        return _lib.Int8RowsC(rows, cols, ld, c.data_ptr(), s.data_ptr())
 
 
 def load():
@@ -197,12 +242,16 @@ def forward(x: torch.Tensor, q: NF4Weight, A: torch.Tensor, B: torch.Tensor, alp
     return y, T
 
 
-def backward(x: torch.Tensor | None, dy: torch.Tensor, q: NF4Weight, A: torch.Tensor,
+def backward(x: torch.Tensor | Int8Rows | None, dy: torch.Tensor, q: NF4Weight, A: torch.Tensor,
              B: torch.Tensor, alpha: float, pool_group: int = 1, T: torch.Tensor | None = None,
              need_dx: bool = True, need_dA: bool = True, need_dB: bool = True,
              codebook: torch.Tensor | None = None, workspace: torch.Tensor | None = None,
              status: torch.Tensor | None = None):
-    """Returns (dX bf16 [M, Din] | None, dA fp32 | None, dB fp32 | None); W4 gets none."""
+    """Returns (dX bf16 [M, Din] | None, dA fp32 | None, dB fp32 | None); W4 gets none.
+    `x` may be the layer's input in 8 bits, int8_quantize(x) (qlora_backward_int8)."""
+    if isinstance(x, Int8Rows):
+        return _backward_int8(x, dy, q, A, B, alpha, pool_group, T, need_dx, need_dA, need_dB,
+                              codebook, workspace, status)
     _need(dy, q.compute_dtype, "dy", 2)
     _need(A, q.compute_dtype, "A", 2)
     _need(B, q.compute_dtype, "B", 2)
@@ -219,6 +268,151 @@ def backward(x: torch.Tensor | None, dy: torch.Tensor, q: NF4Weight, A: torch.Te
                                _ptr(dA), _ptr(dB), _ptr(ws), nbytes, _ptr(status), _stream())
     _lib.check(rc, "qlora_backward")
     return dX, dA, dB
+
+
+def _backward_int8(x: Int8Rows, dy, q: NF4Weight, A, B, alpha, pool_group, T, need_dx, need_dA, need_dB,
+                   codebook, workspace, status):
+    _need(dy, q.compute_dtype, "dy", 2)
+    _need(A, q.compute_dtype, "A", 2)
+    _need(B, q.compute_dtype, "B", 2)
+    M, r = dy.shape[0], A.shape[1]
+    dev = _one_device(dy, x, A, B, T, workspace, status, q.packed)
+    if tuple(dy.shape) != (x.rows, q.rows) or x.cols != q.cols:
+        raise ValueError(f"dy [{x.rows}, {q.rows}] and x [{M}, {q.cols}] are needed")
+    if pool_group not in (1, 64) or tuple(A.shape) != (q.cols // pool_group, r) or tuple(B.shape) != (r, q.rows):
+        raise ValueError("A [Din/pool_group, r] and B [r, Dout] are needed")
+    if T is not None:
+        _need(T, torch.float32, "T", 2)
+        if tuple(T.shape) != (M, r):
+            raise ValueError(f"T [{M}, {r}] is needed")
+    with torch.cuda.device(dev):
+        new = torch.empty if M else torch.zeros      # no token: the adapter gradients are zero
+        dX = torch.empty(M, q.cols, dtype=q.compute_dtype, device=dev) if need_dx else None
+        dA = new(A.shape[0], r, dtype=torch.float32, device=dev) if need_dA else None
+        dB = new(r, q.rows, dtype=torch.float32, device=dev) if need_dB else None
+        qc, xc = q.c_struct(), x.c_struct()
+        need = int(load().qlora_backward_int8_workspace_size(M, ctypes.byref(qc), r, pool_group))
+        ws, nbytes = _workspace(need, dev, workspace)
+        rc = load().qlora_backward_int8(ctypes.byref(xc), _ptr(dy), M, ctypes.byref(qc), _cb_host(codebook),
+                                        _ptr(A), _ptr(B), r, float(alpha), pool_group, _ptr(T), _ptr(dX),
+                                        _ptr(dA), _ptr(dB), _ptr(ws), nbytes, _ptr(status), _stream())
+        _lib.check(rc, "qlora_backward_int8")
+    return dX, dA, dB
+
+
+def _one_device(*tensors) -> torch.device:
+    dev = tensors[0].device
+    for t in tensors[1:]:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors of one device are needed: {dev} and {t.device} were given")
+    return dev
+
+
+def int8_quantize(x: torch.Tensor, out: Int8Rows | None = None,
+                  status: torch.Tensor | None = None) -> Int8Rows:
+    """The rows of x (bf16, fp16 or fp32 [rows, cols], unit column stride) in 8 bits,
+    one scale a row: a token's activation, or an output channel of a weight Wt."""
+    if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPE_CODES or x.dim() != 2 or not x.is_cuda:
+        raise TypeError("x: expected a 2-D bf16, fp16 or fp32 CUDA tensor")
+    rows, cols, ldx = _row_stride(x, "x")
+    q = out if out is not None else Int8Rows.empty(rows, cols, x.device)
+    if (q.rows, q.cols) != (rows, cols):
+        raise ValueError(f"out: [{rows}, {cols}] is needed")
+    with torch.cuda.device(_one_device(x, q, status)):
+        qc = q.c_struct()
+        rc = load().int8_quantize(_ptr(x), _DTYPE_CODES[x.dtype], ldx, ctypes.byref(qc), _ptr(status),
+                                  _stream())
+        _lib.check(rc, "int8_quantize")
+    return q
+
+
+def _row_stride(x: torch.Tensor, name: str):
+    rows, cols = x.shape
+    ldx = x.stride(0) if rows > 1 else max(cols, 1)
+    if cols < 1 or (cols > 1 and x.stride(1) != 1) or ldx < cols:
+        raise ValueError(f"{name}: at least one column, a unit column stride and rows that do not overlap are needed")
+    return rows, cols, ldx
+
+
+def int8_dequantize(q: Int8Rows, dtype: torch.dtype = torch.bfloat16,
+                    out: torch.Tensor | None = None) -> torch.Tensor:
+    """The values codes * scales [rows, cols] in bf16, fp16 or fp32."""
+    if dtype not in _DTYPE_CODES:
+        raise TypeError(f"dtype: one of {list(_DTYPE_CODES)}")
+    out = out if out is not None else torch.empty(q.rows, q.cols, dtype=dtype, device=q.device)
+    _need(out, dtype, "out", 2)
+    if tuple(out.shape) != (q.rows, q.cols):
+        raise ValueError(f"out: [{q.rows}, {q.cols}] is needed")
+    with torch.cuda.device(_one_device(out, q)):
+        qc = q.c_struct()
+        _lib.check(load().int8_dequantize(ctypes.byref(qc), _DTYPE_CODES[dtype], _ptr(out), _stream()),
+                   "int8_dequantize")
+    return out
+
+
+def int8_matmul(x: torch.Tensor | Int8Rows, w: Int8Rows, bias: torch.Tensor | None = None,
+                dtype: torch.dtype | None = None, out: torch.Tensor | None = None,
+                x8_out: Int8Rows | None = None, status: torch.Tensor | None = None) -> torch.Tensor:
+    """y = x W^T (+ bias) with both operands in 8 bits: x [M, K] is a tensor (bf16, fp16 or
+    fp32), quantized row by row in the call, or 8-bit rows already; w the weight's [N, K] rows
+    (int8_quantize of an nn.Linear weight or of merge()'s).  y [M, N] has `dtype`: x's by
+    default, bf16 for 8-bit rows.  `x8_out` receives a tensor x's rows, to be kept as the
+    checkpoint of backward()."""
+    given = isinstance(x, Int8Rows)
+    if not given and (not isinstance(x, torch.Tensor) or x.dtype not in _DTYPE_CODES or x.dim() != 2
+                      or not x.is_cuda):
+        raise TypeError("x: expected Int8Rows or a 2-D bf16, fp16 or fp32 CUDA tensor")
+    if dtype is None:
+        dtype = out.dtype if out is not None else (torch.bfloat16 if given else x.dtype)
+    if dtype not in _DTYPE_CODES:
+        raise TypeError(f"dtype: one of {list(_DTYPE_CODES)}")
+    if given and x8_out is not None:
+        raise ValueError("x8_out: only for a tensor x")
+    M, K, ldx = (x.rows, x.cols, 0) if given else _row_stride(x, "x")
+    if K != w.cols:
+        raise ValueError(f"x has {K} columns, w {w.cols}")
+    x8 = x if given else (x8_out if x8_out is not None else Int8Rows.empty(M, K, x.device))
+    if (x8.rows, x8.cols) != (M, K):
+        raise ValueError(f"x8_out: [{M}, {K}] is needed")
+    y = out if out is not None else torch.empty(M, w.rows, dtype=dtype, device=x.device)
+    _need(y, dtype, "out", 2)
+    if tuple(y.shape) != (M, w.rows):
+        raise ValueError(f"out: [{M}, {w.rows}] is needed")
+    if bias is not None:
+        _need(bias, dtype, "bias", 1)
+        if bias.shape[0] != w.rows:
+            raise ValueError(f"bias: [{w.rows}] is needed")
+    with torch.cuda.device(_one_device(x, w, x8, y, bias, status)):
+        xc, wc = x8.c_struct(), w.c_struct()
+        rc = load().int8_matmul(None if given else _ptr(x), 0 if given else _DTYPE_CODES[x.dtype], ldx,
+                                ctypes.byref(xc), ctypes.byref(wc), _ptr(bias), _ptr(y),
+                                _DTYPE_CODES[dtype], _ptr(status), _stream())
+        _lib.check(rc, "int8_matmul")
+    return y
+
+
+def int8_matmul_backward(dy: torch.Tensor, w: Int8Rows, out: torch.Tensor | None = None,
+                         workspace: torch.Tensor | None = None,
+                         status: torch.Tensor | None = None) -> torch.Tensor:
+    """dX = dy dequant(w) [M, K] (bf16 or fp16): int8_matmul's gradient for its tokens."""
+    if not isinstance(dy, torch.Tensor) or dy.dtype not in (torch.bfloat16, torch.float16):
+        raise TypeError("dy: expected a 2-D bf16 or fp16 tensor")
+    _need(dy, dy.dtype, "dy", 2)
+    M = dy.shape[0]
+    if dy.shape[1] != w.rows:
+        raise ValueError(f"dy has {dy.shape[1]} columns, w {w.rows} rows")
+    dX = out if out is not None else torch.empty(M, w.cols, dtype=dy.dtype, device=dy.device)
+    _need(dX, dy.dtype, "out", 2)
+    if tuple(dX.shape) != (M, w.cols):
+        raise ValueError(f"out: [{M}, {w.cols}] is needed")
+    with torch.cuda.device(_one_device(dy, w, dX, workspace, status)):
+        wc = w.c_struct()
+        need = int(load().int8_matmul_backward_workspace_size(M, ctypes.byref(wc)))
+        ws, nbytes = _workspace(need, dy.device, workspace)
+        rc = load().int8_matmul_backward(_ptr(dy), _DTYPE_CODES[dy.dtype], M, ctypes.byref(wc), _ptr(dX),
+                                         _ptr(ws), nbytes, _ptr(status), _stream())
+        _lib.check(rc, "int8_matmul_backward")
+    return dX
 
 
 def forward_noalloc(x: torch.Tensor, q: NF4Weight, A: torch.Tensor, B: torch.Tensor,
@@ -259,3 +453,46 @@ class QLoRALinearFn(torch.autograd.Function):
                               need_dB=ctx.needs_input_grad[2])
         return (dX, None if dA is None else dA.to(A.dtype), None if dB is None else dB.to(B.dtype),
                 None, None, None)
+
+
+class QLoRALinear8BitInputFn(torch.autograd.Function):
+    """QLoRALinearFn with the input kept in 8 bits between forward and backward.  `x8` is
+    int8_quantize(x), made here when None; layers that read the same x share one."""
+
+    @staticmethod
+    def forward(ctx, x, A, B, q: NF4Weight, alpha: float, pool_group: int = 1,
+                x8: Int8Rows | None = None):
+        y, T = forward(x, q, A, B, alpha, pool_group)
+        x8 = int8_quantize(x) if x8 is None else x8
+        if (x8.rows, x8.cols) != tuple(x.shape):
+            raise ValueError("x8: int8_quantize(x) is needed")
+        ctx.save_for_backward(x8.codes, x8.scales, A, B, T)
+        ctx.q, ctx.alpha, ctx.pool = q, alpha, pool_group
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        codes, scales, A, B, T = ctx.saved_tensors
+        dX, dA, dB = backward(Int8Rows(codes, scales), dy.contiguous(), ctx.q, A, B, ctx.alpha, ctx.pool, T=T,
+                              need_dx=ctx.needs_input_grad[0], need_dA=ctx.needs_input_grad[1],
+                              need_dB=ctx.needs_input_grad[2])
+        return (dX, None if dA is None else dA.to(A.dtype), None if dB is None else dB.to(B.dtype),
+                None, None, None, None)
+
+
+class Int8LinearFn(torch.autograd.Function):
+    """int8_matmul of a bf16 or fp16 x with a gradient for x (straight through its rounding);
+    none for the frozen weight and bias."""
+
+    @staticmethod
+    def forward(ctx, x, w: Int8Rows, bias=None):
+        if x.dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError("x: expected bf16 or fp16")
+        ctx.w = w
+        return int8_matmul(x, w, bias)
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        return int8_matmul_backward(dy.contiguous(), ctx.w), None, None

@@ -5,6 +5,7 @@
 #include <unordered_map>
 
 #include "common.cuh"
+#include "int8_gemm.cuh"
 
 namespace qlora {
 // quantize.cu
@@ -240,6 +241,9 @@ struct FwdWs {
 struct BwdWs {
     uint16_t *Apad, *ph, *pl, *sG, *Gsplit, *Tsplit, *Aext;
     float *G32, *Gpart, *T32, *Tpart, *dApart, *dBpart, *gemv_part;
+    // input in 8 bits, not pooled: the digits of s_m G's columns and of A's
+    int8_t *Gdig, *Adig;
+    float *Gstep, *Astep;
 };
 
 size_t layout_fwd(const Dims &d, bool have_tsave, void *base, FwdWs *w) {
@@ -262,19 +266,30 @@ size_t layout_fwd(const Dims &d, bool have_tsave, void *base, FwdWs *w) {
     return b.off;
 }
 
-size_t layout_bwd(const Dims &d, bool have_tsaved, bool want_dx, bool want_da, bool want_db,
+// x8: the layer's input is 8-bit rows; without pooling its products (dA, T)
+// are integer ones, which need digits instead of hi/lo halves and partials.
+size_t layout_bwd(const Dims &d, bool have_tsaved, bool want_dx, bool want_da, bool want_db, bool x8,
                   void *base, BwdWs *w) {
     Bump b(base);
     BwdWs x{};
+    const bool digits = x8 && d.g == 1;
     x.G32 = b.take<float>(d.M * d.r);
     x.Gpart = b.take<float>(prod_partial_floats(prod_G(d, 0, 0)));
-    if (want_da) x.Gsplit = b.take<uint16_t>(d.M * 2 * d.rp);
+    if (want_da && !digits) x.Gsplit = b.take<uint16_t>(d.M * 2 * d.rp);
+    if (want_da && digits) {
+        x.Gdig = b.take<int8_t>(3 * d.rp * round_up(d.M, 16));
+        x.Gstep = b.take<float>(d.rp);
+    }
     if (d.g > 1 && (want_da || (want_db && !have_tsaved))) {
         x.ph = b.take<uint16_t>(d.M * d.Dap);
         x.pl = b.take<uint16_t>(d.M * d.Dap);
     }
     if (want_db) {
-        if (!have_tsaved) {
+        if (!have_tsaved && digits) {
+            x.Adig = b.take<int8_t>(3 * d.rp * round_up(d.Da, 16));
+            x.Astep = b.take<float>(d.rp);
+            x.T32 = b.take<float>(d.M * d.r);
+        } else if (!have_tsaved) {
             x.Apad = b.take<uint16_t>(d.Da * d.rp);
             x.T32 = b.take<float>(d.M * d.r);
             x.Tpart = b.take<float>(prod_partial_floats(prod_T(d, 0, 0, 0, 0)));
@@ -282,7 +297,7 @@ size_t layout_bwd(const Dims &d, bool have_tsaved, bool want_dx, bool want_da, b
         x.Tsplit = b.take<uint16_t>(d.M * 2 * d.rp);
         x.dBpart = b.take<float>(prod_partial_floats(prod_dB(d, 0, 0)));
     }
-    if (want_da) x.dApart = b.take<float>(prod_partial_floats(prod_dA(d, 0, 0, 0, 0)));
+    if (want_da && !digits) x.dApart = b.take<float>(prod_partial_floats(prod_dA(d, 0, 0, 0, 0)));
     if (want_dx) {
         if (d.small) {
             x.gemv_part = b.take<float>(gemv_bwd_partial_bytes((int)d.M, d.Din, d.Dout) / 4 + 1);
@@ -337,6 +352,74 @@ int run_adapter_down(const Dims &d, const uint16_t *X, const uint16_t *A, uint16
         return QLORA_ECUDA;
     return launch_reduce(Tpart, plan.splits, d.M, plan.Qp, 0, d.r, 1.f, T32, d.r, 1, s, sT, d.rp64,
                          nullptr, 0, st, d.f16);
+}
+
+// ---------------------------------------------------------------- 8-bit rows
+// The integer products sum up to 131072 terms of 127 * 128 in 32 bits.
+constexpr int64_t kInt8MaxTerms = 131072;
+
+int check_rows8(const int8_rows_t *q) {
+    if (!q || q->rows < 0 || q->rows > (int64_t)0x7fffffff || q->cols < 1 || q->cols > (int64_t)0x7fffffff)
+        return QLORA_EINVAL;
+    if (q->ld < q->cols || q->ld % 16 != 0) return QLORA_EINVAL;
+    if (q->rows == 0) return QLORA_OK;
+    if (!q->codes || !aligned16(q->codes) || !q->scales) return QLORA_EINVAL;
+    return QLORA_OK;
+}
+
+bool known_dtype(int32_t dt) {
+    return dt == QLORA_DTYPE_BF16 || dt == QLORA_DTYPE_FP16 || dt == QLORA_DTYPE_FP32;
+}
+
+// A pointer to values of a dtype has that dtype's own alignment.
+bool aligned_to(const void *p, int32_t dt) {
+    return (reinterpret_cast<uintptr_t>(p) & (dt == QLORA_DTYPE_FP32 ? 3u : 1u)) == 0;
+}
+
+// dA = s u^T G from codes c and scales of the tokens: column j of (scale_m G[m][j]) in digits, then
+// dA[k][j] = s step_j sum_m c[m][k] digits.
+int run_dA_int8(const Dims &d, const int8_rows_t &x, const float *G, int8_t *dig, float *step, float s, float *dA,
+                uint32_t *status, cudaStream_t st) {
+    const int64_t ld = round_up(d.M, 16);
+    RC(launch_int8_col_digits(G, QLORA_DTYPE_FP32, d.M, d.r, x.scales, dig, ld, d.rp, step, st));
+    Int8Product g{};
+    g.a = x.codes, g.lda = x.ld, g.a_mn = 1;
+    g.b = dig, g.ldb = ld, g.plane_rows = d.rp, g.planes = 3;
+    g.P = d.Din, g.Q = d.r, g.R = d.M;
+    g.qscale = step, g.mul = s;
+    g.out = dA, g.ldo = d.r, g.q_inner = 1, g.dtype = QLORA_DTYPE_FP32;
+    return launch_int8_tall(g, status, st);
+}
+
+// T[m][j] = scale_m step_j sum_k c[m][k] (digits of A's column j)
+int run_T_int8(const Dims &d, const int8_rows_t &x, const uint16_t *A, int8_t *dig, float *step, float *T,
+               uint32_t *status, cudaStream_t st) {
+    const int64_t ld = round_up(d.Da, 16);
+    RC(launch_int8_col_digits(A, d.f16 ? QLORA_DTYPE_FP16 : QLORA_DTYPE_BF16, d.Da, d.r, nullptr, dig, ld, d.rp,
+                              step, st));
+    Int8Product g{};
+    g.a = x.codes, g.lda = x.ld;
+    g.b = dig, g.ldb = ld, g.plane_rows = d.rp, g.planes = 3;
+    g.P = d.M, g.Q = d.r, g.R = d.Din;
+    g.qscale = step, g.pscale = x.scales, g.mul = 1.f;
+    g.out = T, g.ldo = d.r, g.q_inner = 1, g.dtype = QLORA_DTYPE_FP32;
+    return launch_int8_tall(g, status, st);
+}
+
+// Scratch of int8_matmul_backward: the digit planes of dY times the channel scales, a step a token.
+struct GradWs {
+    int8_t *planes;
+    float *steps;
+    int64_t ld;
+};
+size_t layout_grad8(int64_t M, const int8_rows_t &w, void *base, GradWs *out) {
+    Bump b(base);
+    GradWs x{};
+    x.ld = round_up(w.rows, 16);
+    x.planes = b.take<int8_t>(2 * M * x.ld);
+    x.steps = b.take<float>(M);
+    if (out) *out = x;
+    return b.off;
 }
 
 int run_pool(const Dims &d, const uint16_t *X, uint16_t *ph, uint16_t *pl, cudaStream_t st) {
@@ -418,7 +501,7 @@ size_t qlora_workspace_size(int64_t M, const nf4_weight_t *q, int32_t r, int32_t
     if (M == 0) return 0;
     const Dims d = make_dims(M, q, r, pool_group);
     if (which == 0) return layout_fwd(d, false, nullptr, nullptr);
-    return layout_bwd(d, false, true, true, true, nullptr, nullptr);
+    return layout_bwd(d, false, true, true, true, false, nullptr, nullptr);
 }
 
 int qlora_forward(const uint16_t *X, int64_t M, const nf4_weight_t *q, const float codebook[16],
@@ -472,22 +555,23 @@ static cudaStream_t side_stream() {
     return s;
 }
 
-int qlora_backward(const uint16_t *X, const uint16_t *dY, int64_t M, const nf4_weight_t *q,
-                   const float codebook[16], const uint16_t *A, const uint16_t *B, int32_t r,
-                   float alpha, int32_t pool_group, const float *T_saved, uint16_t *dX, float *dA,
-                   float *dB, void *workspace, size_t ws_bytes, uint32_t *d_status, void *stream) {
+// qlora_backward, and qlora_backward_int8 with the input as 8-bit rows (X8, then X is NULL).
+static int backward_impl(const uint16_t *X, const int8_rows_t *X8, const uint16_t *dY, int64_t M,
+                         const nf4_weight_t *q, const float codebook[16], const uint16_t *A, const uint16_t *B,
+                         int32_t r, float alpha, int32_t pool_group, const float *T_saved, uint16_t *dX, float *dA,
+                         float *dB, void *workspace, size_t ws_bytes, uint32_t *d_status, void *stream) {
     RC(check_layer_args(M, q, codebook, r, alpha, pool_group, nullptr));
     if (M == 0) return QLORA_OK;
     if (!dY || !A || !B) return QLORA_EINVAL;
     const bool want_dx = dX != nullptr, want_da = dA != nullptr, want_db = dB != nullptr;
-    if ((want_da || (want_db && !T_saved)) && !X) return QLORA_EINVAL;
+    if ((want_da || (want_db && !T_saved)) && !X && !X8) return QLORA_EINVAL;
     if (!aligned16(dY) || !aligned16(B) || (X && !aligned16(X)) || (dX && !aligned16(dX)))
         return QLORA_EINVAL;
     const Dims d = make_dims(M, q, r, pool_group);
-    const size_t need = layout_bwd(d, T_saved != nullptr, want_dx, want_da, want_db, nullptr, nullptr);
+    const size_t need = layout_bwd(d, T_saved != nullptr, want_dx, want_da, want_db, X8 != nullptr, nullptr, nullptr);
     if (need > ws_bytes || (need > 0 && !workspace)) return QLORA_EWORKSPACE;
     BwdWs w;
-    layout_bwd(d, T_saved != nullptr, want_dx, want_da, want_db, workspace, &w);
+    layout_bwd(d, T_saved != nullptr, want_dx, want_da, want_db, X8 != nullptr, workspace, &w);
     cudaStream_t st = (cudaStream_t)stream;
     const Codebook cb = to_cb(codebook);
     const float s = alpha / (float)r;
@@ -503,7 +587,8 @@ int qlora_backward(const uint16_t *X, const uint16_t *dY, int64_t M, const nf4_w
         RC(launch_reduce(w.Gpart, pl.splits, M, pl.Qp, 0, r, 1.f, w.G32, r, 1, s, sG, d.rp64,
                          w.Gsplit, d.rp, st, d.f16));
     }
-    if (d.g > 1 && w.ph) RC(run_pool(d, X, w.ph, w.pl, st));
+    if (d.g > 1 && w.ph)
+        RC(X8 ? launch_int8_pool_split(*X8, d.Da, d.Dap, w.ph, w.pl, st, d.f16) : run_pool(d, X, w.ph, w.pl, st));
 
     // With the tensor-core dX GEMM, dA and dB go to the side stream (after
     // G): the GEMM is enqueued first, so its CTAs are placed first and the
@@ -539,7 +624,10 @@ int qlora_backward(const uint16_t *X, const uint16_t *dY, int64_t M, const nf4_w
     }
     int rc = QLORA_OK;
     if (side && cudaStreamWaitEvent(side, ev_fork, 0) != cudaSuccess) rc = QLORA_ECUDA;
-    if (rc == QLORA_OK && want_da) {
+    const bool digits = X8 && d.g == 1;
+    if (rc == QLORA_OK && want_da && digits) {
+        rc = run_dA_int8(d, *X8, w.G32, w.Gdig, w.Gstep, s, dA, d_status, ast);
+    } else if (rc == QLORA_OK && want_da) {
         ProdPlan pl;
         rc = run_prod(prod_dA(d, X, w.ph, w.pl, w.Gsplit), w.dApart, d_status, ast, &pl, d.f16);
         if (rc == QLORA_OK)
@@ -549,8 +637,9 @@ int qlora_backward(const uint16_t *X, const uint16_t *dY, int64_t M, const nf4_w
     if (rc == QLORA_OK && want_db) {
         const float *T32 = T_saved;
         if (!T32) {
-            rc = run_adapter_down(d, X, A, w.Apad, w.ph, w.pl, w.Tpart, w.T32, s, nullptr, d_status,
-                                  ast);
+            rc = digits ? run_T_int8(d, *X8, A, w.Adig, w.Astep, w.T32, d_status, ast)
+                        : run_adapter_down(d, X, A, w.Apad, w.ph, w.pl, w.Tpart, w.T32, s, nullptr,
+                                           d_status, ast);
             T32 = w.T32;
         }
         if (rc == QLORA_OK) rc = launch_split_f32(T32, M, r, d.rp, w.Tsplit, ast, d.f16);
@@ -570,6 +659,98 @@ int qlora_backward(const uint16_t *X, const uint16_t *dY, int64_t M, const nf4_w
     if (ev_fork) cudaEventDestroy(ev_fork);
     if (ev_join) cudaEventDestroy(ev_join);
     return rc;
+}
+
+int qlora_backward(const uint16_t *X, const uint16_t *dY, int64_t M, const nf4_weight_t *q,
+                   const float codebook[16], const uint16_t *A, const uint16_t *B, int32_t r,
+                   float alpha, int32_t pool_group, const float *T_saved, uint16_t *dX, float *dA,
+                   float *dB, void *workspace, size_t ws_bytes, uint32_t *d_status, void *stream) {
+    return backward_impl(X, nullptr, dY, M, q, codebook, A, B, r, alpha, pool_group, T_saved, dX, dA, dB, workspace,
+                         ws_bytes, d_status, stream);
+}
+
+int qlora_backward_int8(const int8_rows_t *X8, const uint16_t *dY, int64_t M, const nf4_weight_t *q,
+                        const float codebook[16], const uint16_t *A, const uint16_t *B, int32_t r, float alpha,
+                        int32_t pool_group, const float *T_saved, uint16_t *dX, float *dA, float *dB,
+                        void *workspace, size_t ws_bytes, uint32_t *d_status, void *stream) {
+    RC(check_layer_args(M, q, codebook, r, alpha, pool_group, nullptr));
+    RC(check_rows8(X8));
+    if (X8->rows != M || X8->cols != q->cols) return QLORA_EINVAL;
+    if (M > kInt8MaxTerms || q->cols > kInt8MaxTerms) return QLORA_EUNSUPPORTED;
+    return backward_impl(nullptr, X8, dY, M, q, codebook, A, B, r, alpha, pool_group, T_saved, dX, dA, dB, workspace,
+                         ws_bytes, d_status, stream);
+}
+
+size_t qlora_backward_int8_workspace_size(int64_t M, const nf4_weight_t *q, int32_t r, int32_t pool_group) {
+    if (qlora_workspace_size(M, q, r, pool_group, 1) == 0) return 0;   // invalid, or M == 0
+    return layout_bwd(make_dims(M, q, r, pool_group), false, true, true, true, true, nullptr, nullptr);
+}
+
+int int8_quantize(const void *X, int32_t dtype, int64_t ldx, const int8_rows_t *q, uint32_t *d_status,
+                  void *stream) {
+    RC(check_rows8(q));
+    if (!known_dtype(dtype) || ldx < q->cols) return QLORA_EINVAL;
+    if (q->rows == 0) return QLORA_OK;
+    if (!X || !aligned_to(X, dtype)) return QLORA_EINVAL;
+    return launch_int8_quantize(X, dtype, ldx, *q, d_status, (cudaStream_t)stream);
+}
+
+int int8_dequantize(const int8_rows_t *q, int32_t dtype, void *out, void *stream) {
+    RC(check_rows8(q));
+    if (!known_dtype(dtype)) return QLORA_EINVAL;
+    if (q->rows == 0) return QLORA_OK;
+    if (!out || !aligned_to(out, dtype)) return QLORA_EINVAL;
+    return launch_int8_dequantize(*q, dtype, out, (cudaStream_t)stream);
+}
+
+int int8_matmul(const void *X, int32_t x_dtype, int64_t ldx, const int8_rows_t *X8, const int8_rows_t *W,
+                const void *bias, void *Y, int32_t y_dtype, uint32_t *d_status, void *stream) {
+    RC(check_rows8(X8));
+    RC(check_rows8(W));
+    if (X8->cols != W->cols || !known_dtype(y_dtype)) return QLORA_EINVAL;
+    if (X && (!known_dtype(x_dtype) || ldx < X8->cols || !aligned_to(X, x_dtype))) return QLORA_EINVAL;
+    if (W->cols > kInt8MaxTerms) return QLORA_EUNSUPPORTED;
+    if (X8->rows == 0 || W->rows == 0) return QLORA_OK;
+    if (!Y || !aligned_to(Y, y_dtype) || (bias && !aligned_to(bias, y_dtype))) return QLORA_EINVAL;
+    cudaStream_t st = (cudaStream_t)stream;
+    if (X) RC(launch_int8_quantize(X, x_dtype, ldx, *X8, d_status, st));
+    Int8Product g{};
+    g.a = W->codes, g.lda = W->ld;
+    g.b = X8->codes, g.ldb = X8->ld, g.planes = 1;
+    g.P = W->rows, g.Q = X8->rows, g.R = W->cols;
+    g.qscale = X8->scales, g.pscale = W->scales, g.mul = 1.f;
+    g.bias = bias;
+    g.out = Y, g.ldo = W->rows, g.dtype = y_dtype;
+    g.pdl = X != nullptr;
+    return launch_int8_tall(g, d_status, st);
+}
+
+size_t int8_matmul_backward_workspace_size(int64_t M, const int8_rows_t *W) {
+    if (M < 1 || M > (int64_t)0x7fffffff || check_rows8(W) || W->rows > kInt8MaxTerms) return 0;
+    return layout_grad8(M, *W, nullptr, nullptr);
+}
+
+int int8_matmul_backward(const uint16_t *dY, int32_t dtype, int64_t M, const int8_rows_t *W, uint16_t *dX,
+                         void *workspace, size_t ws_bytes, uint32_t *d_status, void *stream) {
+    RC(check_rows8(W));
+    if (M < 0 || M > (int64_t)0x7fffffff || W->rows < 1) return QLORA_EINVAL;
+    if (dtype != QLORA_DTYPE_BF16 && dtype != QLORA_DTYPE_FP16) return QLORA_EINVAL;
+    if (W->rows > kInt8MaxTerms) return QLORA_EUNSUPPORTED;
+    if (M == 0) return QLORA_OK;
+    if (!dY || !dX || !aligned_to(dY, dtype) || !aligned_to(dX, dtype)) return QLORA_EINVAL;
+    if (!workspace || layout_grad8(M, *W, nullptr, nullptr) > ws_bytes) return QLORA_EWORKSPACE;
+    GradWs ws;
+    layout_grad8(M, *W, workspace, &ws);
+    cudaStream_t st = (cudaStream_t)stream;
+    RC(launch_int8_row_digits(dY, dtype == QLORA_DTYPE_FP16, M, W->rows, W->scales, ws.planes, ws.ld, ws.steps, st));
+    Int8Product g{};
+    g.a = W->codes, g.lda = W->ld, g.a_mn = 1;
+    g.b = ws.planes, g.ldb = ws.ld, g.plane_rows = M, g.planes = 2;
+    g.P = W->cols, g.Q = M, g.R = W->rows;
+    g.qscale = ws.steps, g.mul = 1.f;
+    g.out = dX, g.ldo = W->cols, g.dtype = dtype;
+    g.pdl = 1;
+    return launch_int8_tall(g, d_status, st);
 }
 
 }  // extern "C"

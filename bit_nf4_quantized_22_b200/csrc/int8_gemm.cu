@@ -1,0 +1,360 @@
+// int8_gemm.cu -- products of int8 operands on the 5th-gen tensor cores
+// (tcgen05 kind::i8, exact int32 sums in TMEM).
+//
+//   acc_d(p, q) = sum_t A(p, t) * B_d(q, t),      d = 0 .. planes - 1
+//   out(p, q)   = (sum_d 256^(planes-1-d) acc_d(p, q)) * qscale[q] * pscale[p] + bias[p]
+//
+// A, the tall operand, is read in place, K-major (the reduction t contiguous)
+// or MN-major (p contiguous); B holds `planes` signed base-256 digits of the
+// other operand (int8_rows.cu), K-major.  The products built on it:
+//   y  = x . W^T        p = output channel, q = token, A = W's codes, 1 plane
+//   dX = dY . W         p = input feature,  q = token, A = W's codes (MN-major), 2 planes
+//   T  = u . A          p = token, q = rank column, A = u's codes, 3 planes
+//   dA = u^T . G        p = input feature, q = rank column, A = u's codes (MN-major), 3 planes
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include "int8_gemm.cuh"
+#include "tcgen05.cuh"
+
+namespace qlora {
+namespace {
+using namespace tc;
+
+constexpr int kTK = 128;                       // reduction values (bytes) per k-tile: one swizzle row
+constexpr int kTP = 128;                       // rows of A per tile = TMEM lanes
+constexpr int kTABytes = kTP * kTK;            // 16 KB
+constexpr int kTThreads = 192;
+constexpr int kTMaxStages = 8;
+constexpr int kTMaxSplits = 8;                 // portable cluster size
+constexpr int kTSmemTwo = 112 * 1024;          // two CTAs fit on an SM
+constexpr int kTSmemOne = 222 * 1024;
+
+// kind::i8 instruction descriptor: signed 8-bit A and B, s32 accumulator.
+__host__ __device__ constexpr uint32_t idesc_i8(uint32_t m, uint32_t n, uint32_t a_mn, uint32_t b_mn) {
+    return (2u << 4) | (1u << 7) | (1u << 10) | (a_mn << 15) | (b_mn << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
+}
+__device__ __forceinline__ void umma_i8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];\n"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr));
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+}
+__device__ __forceinline__ int4 ld_cluster_int4(uint32_t addr) {
+    int4 v;
+    asm volatile("ld.shared::cluster.v4.s32 {%0,%1,%2,%3}, [%4];\n"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "r"(addr)
+                 : "memory");
+    return v;
+}
+
+struct TallParams {
+    int64_t P, Q;
+    int planes, nt;        // B rows per plane and tile; UMMA N = planes * nt
+    int64_t plane_rows;    // rows from one plane of B to the next
+    int nk, per;           // k-tiles, and per split
+    int a_mn;              // A is MN-major
+    int stages;
+    uint32_t stage_bytes, tmem_cols;
+    const float *qscale, *pscale;
+    float mul;
+    const void *bias;      // per p, in the output's dtype
+    void *out;
+    int64_t ldo;
+    int q_inner;           // out[p * ldo + q], else out[q * ldo + p]
+    int dtype, vec;
+    int pdl;               // B and the scales come from the kernel before (programmatic launch)
+    uint32_t *status;
+};
+
+__device__ __forceinline__ float load_any(const void *p, int64_t i, int dtype) {
+    if (dtype == QLORA_DTYPE_FP32) return __ldg(static_cast<const float *>(p) + i);
+    return dec16(__ldg(static_cast<const uint16_t *>(p) + i), dtype == QLORA_DTYPE_FP16);
+}
+
+// CTA (x, y, z): rows [128 x, +128) of A, rows [nt y, +nt) of each plane of B,
+// k-tiles [per z, +per).  Warp 0 loads by TMA into a ring of stages, warp 1
+// issues the MMAs, all warps share the epilogue.  The CTAs of a cluster (all
+// z) hold the splits of one tile: each leaves its int32 sums in its own shared
+// memory and finishes every gridDim.z-th column, reading its peers' sums over
+// distributed shared memory -- integer sums, so the split changes no result.
+__global__ void __launch_bounds__(kTThreads)
+k_int8_tall(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const TallParams p) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    const uint32_t base = (raw_addr + 1023u) & ~1023u;
+    uint8_t *gen_base = smem_raw + (base - raw_addr);
+    const int S = p.stages;
+    const uint32_t bar0 = base + S * p.stage_bytes;
+    auto full_bar = [&](int s) { return bar0 + 8u * s; };
+    auto empty_bar = [&](int s) { return bar0 + 8u * (kTMaxStages + s); };
+    const uint32_t acc_bar = bar0 + 8u * (2 * kTMaxStages);
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(gen_base + S * p.stage_bytes + 160);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(gen_base + S * p.stage_bytes + 192);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int64_t p0 = (int64_t)blockIdx.x * kTP;
+    const int64_t q0 = (int64_t)blockIdx.y * p.nt;
+    const int kbeg = blockIdx.z * p.per;
+    const int kend = kbeg + p.per < p.nk ? kbeg + p.per : p.nk;
+    const int nloc = kend - kbeg;                  // >= 1 by construction
+    const int N = p.planes * p.nt;
+    const uint32_t rank = blockIdx.z, splits = gridDim.z;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(full_bar(s), 1);
+            mbar_init(empty_bar(s), 1);
+        }
+        mbar_init(acc_bar, 1);
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+        fence_proxy_async();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(tmem_holder)),
+                     "r"(p.tmem_cols));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    bool ok = true;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            auto load_a = [&](int i) {
+                const int s = i % S;
+                const uint32_t sa = base + s * p.stage_bytes;
+                const int t0 = (kbeg + i) * kTK;
+                mbar_expect_tx(full_bar(s), p.stage_bytes);
+                if (p.a_mn) tma_load_2d(sa, &tmA, (int)p0, t0, full_bar(s));
+                else tma_load_2d(sa, &tmA, t0, (int)p0, full_bar(s));
+            };
+            auto load_b = [&](int i) {
+                const int s = i % S;
+                const uint32_t sb = base + s * p.stage_bytes + kTABytes;
+                const int t0 = (kbeg + i) * kTK;
+                for (int d = 0; d < p.planes; ++d)
+                    tma_load_2d(sb + d * p.nt * kTK, &tmB, t0, (int)(d * p.plane_rows + q0), full_bar(s));
+            };
+            int head = 0;
+            if (p.pdl) {
+                // the weight does not depend on the kernel before: fill the ring with it first
+                head = nloc < S ? nloc : S;
+                for (int i = 0; i < head; ++i) load_a(i);
+                asm volatile("griddepcontrol.wait;\n" ::: "memory");
+                for (int i = 0; i < head; ++i) load_b(i);
+            }
+            for (int i = head; i < nloc && ok; ++i) {
+                const int s = i % S;
+                if (i >= S) ok = mbar_wait(empty_bar(s), ((i / S) & 1) ^ 1, abort_flag);
+                if (!ok) break;
+                load_a(i);
+                load_b(i);
+            }
+            if (!ok) *abort_flag = 1;
+        }
+    } else if (warp == 1) {
+        if (lane == 0) {
+            const uint32_t idesc = idesc_i8(kTP, (uint32_t)N, p.a_mn ? 1u : 0u, 0u);
+            // K-major: rows of 128 t, 8-row groups 1 KB apart, a step of 32 t
+            // advances 32 B.  MN-major: rows of 128 p, 8 t a 1 KB group, a step
+            // of 32 t advances 4 KB (one 128-wide atom, so no leading stride).
+            const uint32_t astep = p.a_mn ? 256u : 2u;
+            for (int i = 0; i < nloc && ok; ++i) {
+                const int s = i % S;
+                ok = mbar_wait(full_bar(s), (i / S) & 1, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                const uint32_t sa = base + s * p.stage_bytes;
+                const uint64_t ad = sdesc(sa, 16, 1024), bd = sdesc(sa + kTABytes, 16, 1024);
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    umma_i8(tmem, ad + kk * astep, bd + kk * 2, idesc, (i > 0 || kk > 0) ? 1u : 0u);
+                umma_commit(empty_bar(s));
+            }
+            if (ok) umma_commit(acc_bar);
+            else *abort_flag = 1;
+        }
+    } else {
+        ok = __all_sync(0xffffffffu, mbar_wait(acc_bar, 0, abort_flag));
+        if (ok) {
+            // TMEM -> the idle ring, as int32 [column][128 rows]
+            tc_fence_after();
+            const int qt = warp & 3;
+            for (int c = 0; c < N; c += 16) {
+                uint32_t v[16];
+                tmem_ld16(tmem + ((uint32_t)(32 * qt) << 16) + c, v);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    *reinterpret_cast<uint32_t *>(gen_base + ((c + i) * kTP + 32 * qt + lane) * 4) = v[i];
+            }
+        } else {
+            *abort_flag = 1;
+        }
+    }
+
+    if (!ok && p.status) atomicOr(p.status, QLORA_STATUS_TIMEOUT);
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0 && lane == 0 && *abort_flag) {
+        // a wait gave up: let this CTA's copies land before its shared memory is released
+        for (int s = 0; s < S && s < nloc; ++s) {
+            const int last = ((nloc - 1 - s) / S) * S + s;
+            for (uint32_t i = 0; i < kWaitLimit; ++i)
+                if (mbar_try_wait(full_bar(s), (last / S) & 1)) break;
+        }
+    }
+    __syncwarp();
+    cluster_sync();   // the cluster's sums are in shared memory
+    if (p.pdl) asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    {
+        const int64_t prow = p0 + 4 * lane;
+        float ps[4], bs[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool in = prow + e < p.P;
+            ps[e] = in && p.pscale ? __ldg(p.pscale + prow + e) : 1.f;
+            bs[e] = in && p.bias ? load_any(p.bias, prow + e, p.dtype) : 0.f;
+        }
+        for (int c = (int)rank + warp * (int)splits; c < p.nt; c += (kTThreads / 32) * (int)splits) {
+            const int64_t q = q0 + c;
+            if (q >= p.Q) break;
+            int64_t sum[4] = {0, 0, 0, 0};
+            for (int d = 0; d < p.planes; ++d) {
+                int4 t = make_int4(0, 0, 0, 0);
+                const uint32_t at = base + ((d * p.nt + c) * kTP + 4 * lane) * 4;
+                for (uint32_t z = 0; z < splits; ++z) {
+                    const int4 v = ld_cluster_int4(mapa_shared(at, z));
+                    t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
+                }
+                sum[0] = sum[0] * 256 + t.x, sum[1] = sum[1] * 256 + t.y;
+                sum[2] = sum[2] * 256 + t.z, sum[3] = sum[3] * 256 + t.w;
+            }
+            const float qs = __ldg(p.qscale + q);
+            float v[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[e] = __fmaf_rn(__fmul_rn(__fmul_rn(__ll2float_rn(sum[e]), qs), p.mul), ps[e], bs[e]);
+            if (p.q_inner) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (prow + e < p.P) static_cast<float *>(p.out)[(prow + e) * p.ldo + q] = v[e];
+            } else if (p.dtype == QLORA_DTYPE_FP32) {
+                float *o = static_cast<float *>(p.out) + q * p.ldo + prow;
+                if (p.vec && prow + 4 <= p.P) {
+                    *reinterpret_cast<float4 *>(o) = make_float4(v[0], v[1], v[2], v[3]);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (prow + e < p.P) o[e] = v[e];
+                }
+            } else {
+                const bool f16 = p.dtype == QLORA_DTYPE_FP16;
+                uint16_t *o = static_cast<uint16_t *>(p.out) + q * p.ldo + prow;
+                if (p.vec && prow + 4 <= p.P) {
+                    *reinterpret_cast<uint2 *>(o) = make_uint2(pack2(v[0], v[1], f16), pack2(v[2], v[3], f16));
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (prow + e < p.P) o[e] = enc16(v[e], f16);
+                }
+            }
+        }
+    }
+    __syncwarp();
+    cluster_sync();   // no CTA leaves while a peer reads its sums
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(p.tmem_cols));
+    }
+}
+
+}  // namespace
+
+int launch_int8_tall(const Int8Product &g, uint32_t *d_status, cudaStream_t st) {
+    if (g.P <= 0 || g.Q <= 0) return QLORA_OK;
+    TallParams p{};
+    // columns per tile: all of them up to the UMMA's 256, else even tiles
+    const int cap = 256 / g.planes / 16 * 16;
+    const int64_t tiles_q = (g.Q + cap - 1) / cap;
+    p.nt = (int)(((g.Q + tiles_q - 1) / tiles_q + 15) / 16 * 16);
+    const int N = g.planes * p.nt;
+    p.P = g.P;
+    p.Q = g.Q;
+    p.planes = g.planes;
+    p.plane_rows = g.plane_rows;
+    p.nk = (int)((g.R + kTK - 1) / kTK);
+    p.a_mn = g.a_mn;
+    p.stage_bytes = kTABytes + N * kTK;
+    p.tmem_cols = 32;
+    while ((int)p.tmem_cols < N) p.tmem_cols *= 2;
+    const bool two = N <= 64;
+    p.stages = (int)((two ? kTSmemTwo : kTSmemOne) / p.stage_bytes);
+    if (p.stages > kTMaxStages) p.stages = kTMaxStages;
+    const int64_t tiles = ((g.P + kTP - 1) / kTP) * tiles_q;
+    int64_t splits = (two ? 2 : 1) * device_sms() / tiles;
+    if (splits > p.nk / 2) splits = p.nk / 2;
+    if (splits > kTMaxSplits) splits = kTMaxSplits;
+    if (splits < 1) splits = 1;
+    p.per = (int)((p.nk + splits - 1) / splits);
+    splits = (p.nk + p.per - 1) / p.per;
+    p.qscale = g.qscale;
+    p.pscale = g.pscale;
+    p.mul = g.mul;
+    p.bias = g.bias;
+    p.out = g.out;
+    p.ldo = g.ldo;
+    p.q_inner = g.q_inner;
+    p.dtype = g.dtype;
+    const int esize = g.dtype == QLORA_DTYPE_FP32 ? 4 : 2;
+    p.vec = g.ldo % 4 == 0 && (reinterpret_cast<uintptr_t>(g.out) & (4 * esize - 1)) == 0;
+    p.pdl = g.pdl;
+    p.status = d_status;
+    const int64_t brows = g.plane_rows * (g.planes - 1) + g.Q;
+    CUtensorMap tA, tB;
+    bool ok = g.a_mn ? make_map(&tA, g.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.P, g.R, g.lda, 128, kTK,
+                                CU_TENSOR_MAP_SWIZZLE_128B)
+                     : make_map(&tA, g.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.R, g.P, g.lda, kTK, 128,
+                                CU_TENSOR_MAP_SWIZZLE_128B);
+    ok = ok && make_map(&tB, g.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.R, brows, g.ldb, kTK, (uint32_t)p.nt,
+                        CU_TENSOR_MAP_SWIZZLE_128B);
+    if (!ok) return QLORA_EUNSUPPORTED;
+    const size_t ring = (size_t)p.stages * p.stage_bytes;
+    if (ring < (size_t)N * kTP * 4) return QLORA_EUNSUPPORTED;   // the sums take the ring's place
+    const int smem = (int)ring + 1024 + 256;
+    if (set_max_smem(reinterpret_cast<const void *>(k_int8_tall), smem) != cudaSuccess) return QLORA_ECUDA;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)((g.P + kTP - 1) / kTP), (unsigned)tiles_q, (unsigned)splits);
+    cfg.blockDim = dim3(kTThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = 1;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = (unsigned)splits;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = g.pdl ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, k_int8_tall, tA, tB, p) != cudaSuccess) return QLORA_ECUDA;
+    QLORA_LAUNCH_CHECK();
+    return QLORA_OK;
+}
+
+}  // namespace qlora

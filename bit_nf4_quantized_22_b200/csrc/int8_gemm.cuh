@@ -1,0 +1,41 @@
+// int8_gemm.cuh -- host interface of the integer products (int8_gemm.cu).
+#pragma once
+#include "common.cuh"
+
+namespace qlora {
+
+// out(p, q) = (sum_d 256^(planes-1-d) sum_t A(p, t) B_d(q, t)) * qscale[q] * mul * pscale[p] + bias[p]
+struct Int8Product {
+    const int8_t *a;       // a_mn: A(p, t) at a[t * lda + p], else a[p * lda + t]
+    int64_t lda;           // bytes, a multiple of 16
+    int a_mn;
+    const int8_t *b;       // B_d(q, t) at b[(d * plane_rows + q) * ldb + t]
+    int64_t ldb;           // bytes, a multiple of 16
+    int64_t plane_rows;
+    int planes;            // 1, 2 or 3
+    int64_t P, Q, R;       // extents of p, q and the reduction t (R <= 131072)
+    const float *qscale;
+    const float *pscale;   // or NULL
+    float mul;
+    const void *bias;      // per p, in the output's dtype, or NULL
+    void *out;             // q_inner: out[p * ldo + q] (fp32), else out[q * ldo + p]
+    int64_t ldo;
+    int q_inner;
+    int dtype;             // QLORA_DTYPE_*
+    int pdl;               // launch beside the kernel before, which writes B and the scales but not A
+};
+
+int launch_int8_tall(const Int8Product &g, uint32_t *d_status, cudaStream_t st);
+
+// int8_rows.cu
+int launch_int8_quantize(const void *X, int dtype, int64_t ldx, const int8_rows_t &q, uint32_t *d_status,
+                         cudaStream_t st);
+int launch_int8_row_digits(const uint16_t *Y, bool f16, int64_t rows, int64_t cols, const float *cscale,
+                           int8_t *planes, int64_t ld, float *steps, cudaStream_t st);
+int launch_int8_col_digits(const void *S, int dtype, int64_t R, int r, const float *f, int8_t *planes, int64_t ld,
+                           int rp, float *steps, cudaStream_t st);
+int launch_int8_pool_split(const int8_rows_t &q, int64_t Da, int64_t ld, uint16_t *hi, uint16_t *lo,
+                           cudaStream_t st, bool f16);
+int launch_int8_dequantize(const int8_rows_t &q, int dtype, void *out, cudaStream_t st);
+
+}  // namespace qlora

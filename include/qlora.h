@@ -257,6 +257,88 @@ int qlora_backward(const uint16_t *X, const uint16_t *dY, int64_t M, const nf4_w
                    float *dA, float *dB, void *workspace, size_t ws_bytes,
                    uint32_t *d_status, void *stream);
 
+/* ---- 8-bit rows: codes, integer products and the layer's 8-bit checkpoint ---
+ * bitsandbytes article (CSDN) section 4.1 (absmax INT8: s = 127 / max|x|, q =
+ * round(s x)) and 4.2 (the vector-wise product: one scale for each row of the
+ * input and each output channel of the weight).  One matrix of 8-bit rows:
+ *   codes    [rows][ld] int8, the first cols of a row valid; 16-byte aligned
+ *   scales   [rows] fp32
+ *   ld       bytes from one row to the next: >= cols, a multiple of 16
+ *   cols     >= 1
+ * Row m stands for codes[m][k] * scales[m].  The rows are tokens for an
+ * activation, output channels for a weight Wt:[Dout, Din]. */
+typedef struct {
+    int64_t rows;
+    int64_t cols;
+    int64_t ld;
+    int8_t *codes;
+    float *scales;
+} int8_rows_t;
+
+/* int8_quantize -- rows of X to codes and scales.  Per row: a = max|x|,
+ * scale = RN32(a / 127), code = the integer nearest to the exact quotient
+ * x / scale, ties to even, at most 127 in magnitude; a row whose scale is 0
+ * has codes 0.  A row with a NaN or an infinity has scale NaN and codes 0, so
+ * that what is computed from it is NaN, and sets QLORA_STATUS_NONFINITE.
+ *   X     device [q->rows, q->cols] of dtype (BF16, FP16 or FP32), ldx >= cols
+ *         elements from one row to the next
+ * Only the first cols bytes of a row of codes are written.
+ * Errors: EINVAL for a NULL or unaligned array, cols < 1, a bad ld or dtype. */
+int int8_quantize(const void *X, int32_t dtype, int64_t ldx, const int8_rows_t *q, uint32_t *d_status,
+                  void *stream);
+
+/* int8_dequantize -- out[m][k] = RN_dtype(RN32(code * scale)), out [rows, cols]
+ * dense.
+ * Errors as int8_quantize. */
+int int8_dequantize(const int8_rows_t *q, int32_t dtype, void *out, void *stream);
+
+/* int8_matmul -- y = x . W^T with both operands in 8 bits:
+ *   Y[m][n] = RN(fma(RN32(RN32(sum_k cx[m][k] cw[n][k]) * sx[m]), sw[n], bias[n])),
+ * the sum exact in 32-bit integers, then rounded to fp32, and the fma rounded
+ * once in fp32.
+ *   X     device [M, K] (x_dtype, row stride ldx) to be quantized into X8
+ *         first, as int8_quantize does; or NULL: X8 holds the tokens already
+ *   X8    [M = X8->rows, K]; with X its buffers receive the codes and scales,
+ *         which can serve as the checkpoint of qlora_backward_int8
+ *   W     [N, K], the frozen weight in 8-bit rows (one scale per channel)
+ *   bias  device [N] of y_dtype, or NULL
+ *   Y     device [M, N] dense of y_dtype (BF16, FP16 or FP32)
+ * Errors: EINVAL for a NULL or unaligned array, bad dtypes or differing K;
+ * EUNSUPPORTED for K > 131072 (the 32-bit sums). */
+int int8_matmul(const void *X, int32_t x_dtype, int64_t ldx, const int8_rows_t *X8, const int8_rows_t *W,
+                const void *bias, void *Y, int32_t y_dtype, uint32_t *d_status, void *stream);
+
+/* int8_matmul_backward -- the gradient of int8_matmul for its tokens, straight
+ * through their rounding:  dX = dY . dequant(W),
+ *   dX[m][k] = RN_dtype(sum_n dY[m][n] sw[n] cw[n][k]).
+ * dY sw is taken in 16-bit fixed point per token (step max / 32639), its two
+ * 8-bit digits go through the integer tensor cores and the sums are exact, so
+ * the result is within (step / 2) sum_n |cw[n][k]| of the exact one before its
+ * rounding to dtype.  A token of dY with a NaN or an infinity gets NaN.  The
+ * frozen weight and the bias get no gradient here.
+ *   dY    device [M, N] dense, dtype BF16 or FP16;  dX  device [M, K]
+ *   workspace/ws_bytes  at least int8_matmul_backward_workspace_size(M, W)
+ * Errors: as int8_matmul; EUNSUPPORTED for N > 131072; EWORKSPACE. */
+size_t int8_matmul_backward_workspace_size(int64_t M, const int8_rows_t *W);
+int int8_matmul_backward(const uint16_t *dY, int32_t dtype, int64_t M, const int8_rows_t *W, uint16_t *dX,
+                         void *workspace, size_t ws_bytes, uint32_t *d_status, void *stream);
+
+/* qlora_backward_int8 -- qlora_backward with the layer's input kept in 8 bits
+ * (1 byte a value between forward and backward instead of 2): everywhere x
+ * stands in dA and in a recomputed T, it is x^ = codes * scale.
+ *   X8    [M, Din], as int8_quantize(x) gives it: the token scales fold into
+ *         G, the codes are read as they are, and the sums over them are exact
+ *         integers (G's and A's columns in 24-bit fixed point).  May be shared
+ *         by every layer that reads the same x.
+ * The other arguments and results are qlora_backward's, dX among them.
+ * Errors: as qlora_backward; EINVAL when X8 is not [M, Din]; EUNSUPPORTED for
+ * M or Din > 131072.  Workspace: qlora_backward_int8_workspace_size(). */
+size_t qlora_backward_int8_workspace_size(int64_t M, const nf4_weight_t *q, int32_t r, int32_t pool_group);
+int qlora_backward_int8(const int8_rows_t *X8, const uint16_t *dY, int64_t M, const nf4_weight_t *q,
+                        const float codebook[16], const uint16_t *A, const uint16_t *B, int32_t r, float alpha,
+                        int32_t pool_group, const float *T_saved, uint16_t *dX, float *dA, float *dB,
+                        void *workspace, size_t ws_bytes, uint32_t *d_status, void *stream);
+
 /* ---- Forward without caller-provided scratch -------------------------------
  * No counterpart on the pages: this entry point exists for callers that cannot
  * allocate device memory -- code that runs where cudaMalloc is not allowed or
