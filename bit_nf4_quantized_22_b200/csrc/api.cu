@@ -388,7 +388,7 @@ int run_dA_int8(const Dims &d, const int8_rows_t &x, const float *G, int8_t *dig
     g.P = d.Din, g.Q = d.r, g.R = d.M;
     g.qscale = step, g.mul = s;
     g.out = dA, g.ldo = d.r, g.q_inner = 1, g.dtype = QLORA_DTYPE_FP32;
-    return launch_int8_tall(g, status, st);
+    return launch_int8_product(g, status, st);
 }
 
 // T[m][j] = scale_m step_j sum_k c[m][k] (digits of A's column j)
@@ -403,7 +403,7 @@ int run_T_int8(const Dims &d, const int8_rows_t &x, const uint16_t *A, int8_t *d
     g.P = d.M, g.Q = d.r, g.R = d.Din;
     g.qscale = step, g.pscale = x.scales, g.mul = 1.f;
     g.out = T, g.ldo = d.r, g.q_inner = 1, g.dtype = QLORA_DTYPE_FP32;
-    return launch_int8_tall(g, status, st);
+    return launch_int8_product(g, status, st);
 }
 
 // Scratch of int8_matmul_backward: the digit planes of dY times the channel scales, a step a token.
@@ -722,7 +722,7 @@ int int8_matmul(const void *X, int32_t x_dtype, int64_t ldx, const int8_rows_t *
     g.bias = bias;
     g.out = Y, g.ldo = W->rows, g.dtype = y_dtype;
     g.pdl = X != nullptr;
-    return launch_int8_tall(g, d_status, st);
+    return launch_int8_product(g, d_status, st);
 }
 
 size_t int8_matmul_backward_workspace_size(int64_t M, const int8_rows_t *W) {
@@ -750,7 +750,7 @@ int int8_matmul_backward(const uint16_t *dY, int32_t dtype, int64_t M, const int
     g.qscale = ws.steps, g.mul = 1.f;
     g.out = dX, g.ldo = W->cols, g.dtype = dtype;
     g.pdl = 1;
-    return launch_int8_tall(g, d_status, st);
+    return launch_int8_product(g, d_status, st);
 }
 
 }  // extern "C"

@@ -284,9 +284,312 @@ k_int8_tall(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     }
 }
 
+
+// ---------------------------------------------------------------- many tokens
+// A persistent kernel of CTA pairs for the products with tokens (y and dX):
+// tcgen05 cta_group::2, M = 256 token rows x N = 256 weight columns per MMA,
+// two accumulators a pair.  With one plane they hold two row blocks of a
+// 512 x 256 tile, with two the digits of one 256 x 256 tile.
+// CTA r of the pair holds rows [128 r, +128) of each block and 128 of the
+// columns.  Warp 0 loads (its ring runs on into the next tile), warp 1 of CTA
+// 0 issues the MMAs, warps 2..9 take the sums out of TMEM, scale and store.
+// The MMAs of the next tile start on an accumulator as soon as it is read:
+// its first four k-tiles go to accumulator 0 before accumulator 1 is needed.
+constexpr int kWStages = 4;
+constexpr int kWSlab = 128 * kTK;                  // 16 KB: 128 rows of one operand
+constexpr int kWStageBytes = 3 * kWSlab;           // two token slabs, one weight slab
+constexpr int kWThreads = 320, kWEpiThreads = 256;
+constexpr int kWSmemBytes = kWStages * kWStageBytes + 1024 + 256 + 2 * 2 * 256 * 4;
+constexpr int kWGroup = 8;                         // row tiles that share a column tile's pass through L2
+
+struct WideParams {
+    int64_t M, N;
+    int nk, mt, nt;            // k-tiles; row and column tiles
+    int digits;                // two planes: one 256-row block, else two of them
+    int64_t plane_rows;
+    int b_mn;                  // the weight is MN-major
+    const float *rscale, *cscale;
+    float mul;
+    const void *bias;
+    void *out;
+    int64_t ldo;
+    int dtype, align;          // bytes that every row of a tile starts on: 32, 16 or less
+    int pdl;
+    uint32_t *status;
+};
+
+__device__ __forceinline__ void umma_i8_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                                             uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+}
+__device__ __forceinline__ void stg256(void *p, const uint32_t *v) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
+                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+// Row and column tile of tile t: groups of kWGroup row tiles, columns within a group.
+__device__ __forceinline__ void tile_at(const WideParams &p, int t, int &tm, int &tn) {
+    const int per = kWGroup * p.nt, g = t / per, in = t % per;
+    const int rows = p.mt - g * kWGroup < kWGroup ? p.mt - g * kWGroup : kWGroup;
+    tm = g * kWGroup + in % rows;
+    tn = in / rows;
+}
+
+// 32 finished values of one row, columns [n, n + 32)
+__device__ __forceinline__ void store32(const WideParams &p, int64_t m, int64_t n, const float (&v)[32]) {
+    if (m >= p.M || n >= p.N) return;
+    if (p.dtype == QLORA_DTYPE_FP32) {
+        float *o = static_cast<float *>(p.out) + m * p.ldo + n;
+        if (p.align >= 32 && n + 32 <= p.N) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t w[8];
+#pragma unroll
+                for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[8 * i + j]);
+                stg256(o + 8 * i, w);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (n + i < p.N) o[i] = v[i];
+        }
+        return;
+    }
+    const bool f16 = p.dtype == QLORA_DTYPE_FP16;
+    uint16_t *o = static_cast<uint16_t *>(p.out) + m * p.ldo + n;
+    uint32_t w[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1], f16);
+    if (p.align >= 32 && n + 32 <= p.N) {
+        stg256(o, w);
+        stg256(o + 16, w + 8);
+    } else if (p.align >= 16 && n + 32 <= p.N) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            reinterpret_cast<uint4 *>(o)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (n + i < p.N) o[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+    }
+}
+
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWThreads, 1)
+k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const WideParams p) {
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    const uint32_t raw_addr = smem_u32(smem_raw);
+    const uint32_t base = (raw_addr + 1023u) & ~1023u;
+    uint8_t *gen_base = smem_raw + (base - raw_addr);
+    const uint32_t bar0 = base + kWStages * kWStageBytes;
+    auto full = [&](int s) { return bar0 + 8u * s; };                   // CTA 0: both CTAs' bytes landed
+    auto empty = [&](int s) { return bar0 + 8u * (kWStages + s); };     // stage free (in both CTAs)
+    const uint32_t acc_full = bar0 + 8u * (2 * kWStages);               // a tile's sums are complete (both)
+    auto acc_free = [&](int h) { return bar0 + 8u * (2 * kWStages + 1 + h); };   // CTA 0: accumulator h read
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(gen_base + kWStages * kWStageBytes + 208);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(gen_base + kWStages * kWStageBytes + 240);
+    float *cbuf = reinterpret_cast<float *>(gen_base + kWStages * kWStageBytes + 256);   // [2][2][256]
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
+    const int tiles = p.mt * p.nt;
+    const int mrows = p.digits ? 256 : 512;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kWStages; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        mbar_init(acc_full, 1);
+        for (int h = 0; h < 2; ++h) mbar_init(acc_free(h), 2 * (kWEpiThreads / 32));
+        *abort_flag = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+        fence_proxy_async();
+    }
+    if (warp == 1) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(tmem_holder)),
+                     "r"(512u));
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;\n");
+    }
+    tc_fence_before();
+    __syncthreads();
+    cluster_sync();   // both CTAs' barriers initialised before any cross-CTA use
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    bool ok = true;
+
+    if (warp == 0) {
+        if (lane == 0) {
+            auto load_w = [&](int s, int t0, int tn) {
+                const uint32_t fa0 = mapa_shared(full(s), 0);
+                const int c0 = tn * 256 + 128 * (int)rank;
+                if (rank == 0) mbar_expect_tx(full(s), 2 * kWStageBytes);
+                const uint32_t sb = base + s * kWStageBytes + 2 * kWSlab;
+                if (p.b_mn) tma_load_2d_pair(sb, &tmW, c0, t0, fa0);
+                else tma_load_2d_pair(sb, &tmW, t0, c0, fa0);
+            };
+            auto load_x = [&](int s, int t0, int tm) {
+                const uint32_t fa0 = mapa_shared(full(s), 0);
+                const uint32_t sa = base + s * kWStageBytes;
+                const int r0 = tm * mrows + 128 * (int)rank;
+                tma_load_2d_pair(sa, &tmX, t0, r0, fa0);
+                tma_load_2d_pair(sa + kWSlab, &tmX, t0, r0 + (p.digits ? (int)p.plane_rows : 256), fa0);
+            };
+            int it = 0, head = 0;
+            for (int t = pair; t < tiles && ok; t += pairs) {
+                int tm, tn;
+                tile_at(p, t, tm, tn);
+                if (it == 0 && p.pdl) {
+                    // the weight does not depend on the kernel before
+                    head = p.nk < kWStages ? p.nk : kWStages;
+                    for (int k = 0; k < head; ++k) load_w(k, k * kTK, tn);
+                    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+                }
+                for (int k = 0; k < p.nk && ok; ++k, ++it) {
+                    const int s = it % kWStages;
+                    if (it >= kWStages) ok = mbar_wait(empty(s), ((it / kWStages) & 1) ^ 1, abort_flag);
+                    if (!ok) break;
+                    if (it >= head) load_w(s, k * kTK, tn);
+                    load_x(s, k * kTK, tm);
+                }
+            }
+            if (!ok) *abort_flag = 1;
+        }
+    } else if (warp == 1) {
+        if (lane == 0 && rank == 0) {
+            const uint32_t idesc = idesc_i8(256, 256, 0, p.b_mn ? 1u : 0u);
+            const uint32_t bstep = p.b_mn ? 256u : 2u;
+            const uint64_t dX = sdesc(base, 16, 1024), dW = sdesc(base + 2 * kWSlab, 16, 1024);
+            constexpr uint32_t kStageD = kWStageBytes >> 4, kSlabD = kWSlab >> 4;
+            auto mma = [&](int s, int h, uint32_t acc) {
+                const uint64_t a = dX + s * kStageD + h * kSlabD, b = dW + s * kStageD;
+#pragma unroll
+                for (int kk = 0; kk < 4; ++kk)
+                    umma_i8_pair(tmem + h * 256, a + kk * 2, b + kk * bstep, idesc, kk > 0 ? 1u : acc);
+            };
+            int it = 0, i = 0;
+            for (int t = pair; t < tiles && ok; t += pairs, ++i) {
+                const int lead = p.nk < kWStages ? p.nk : kWStages;
+                if (i > 0) ok = mbar_wait_cluster(acc_free(0), (i - 1) & 1, abort_flag);
+                for (int k = 0; k < lead && ok; ++k) {
+                    const int s = (it + k) % kWStages;
+                    ok = mbar_wait_cluster(full(s), ((it + k) / kWStages) & 1, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    mma(s, 0, k > 0 ? 1u : 0u);
+                }
+                if (ok && i > 0) ok = mbar_wait_cluster(acc_free(1), (i - 1) & 1, abort_flag);
+                if (!ok) break;
+                tc_fence_after();
+                for (int k = 0; k < lead; ++k) {
+                    const int s = (it + k) % kWStages;
+                    mma(s, 1, k > 0 ? 1u : 0u);
+                    umma_commit_pair(empty(s), 0x3);
+                }
+                for (int k = lead; k < p.nk; ++k) {
+                    const int s = (it + k) % kWStages;
+                    ok = mbar_wait_cluster(full(s), ((it + k) / kWStages) & 1, abort_flag);
+                    if (!ok) break;
+                    tc_fence_after();
+                    mma(s, 0, 1u);
+                    mma(s, 1, 1u);
+                    umma_commit_pair(empty(s), 0x3);
+                }
+                if (ok) umma_commit_pair(acc_full, 0x3);
+                it += p.nk;
+            }
+            if (!ok) *abort_flag = 1;
+        }
+    } else {
+        if (p.pdl) asm volatile("griddepcontrol.wait;\n" ::: "memory");
+        const int e = threadIdx.x - 64;
+        const int qt = warp & 3, cg = (warp - 2) >> 2;     // TMEM lane quarter, column half
+        const uint32_t lanes = (uint32_t)(32 * qt) << 16;
+        const uint32_t free0 = mapa_shared(acc_free(0), 0);
+        int i = 0;
+        for (int t = pair; t < tiles && ok; t += pairs, ++i) {
+            int tm, tn;
+            tile_at(p, t, tm, tn);
+            const int64_t n0 = (int64_t)tn * 256;
+            float *cs = cbuf + (i & 1) * 512, *cb = cs + 256;
+            cs[e] = p.cscale && n0 + e < p.N ? __ldg(p.cscale + n0 + e) : 1.f;
+            cb[e] = p.bias && n0 + e < p.N ? load_any(p.bias, n0 + e, p.dtype) : 0.f;
+            asm volatile("bar.sync 1, 256;\n" ::: "memory");
+            ok = __all_sync(0xffffffffu, mbar_wait_cluster(acc_full, i & 1, abort_flag));
+            if (!ok) break;
+            tc_fence_after();
+            const int64_t mrow = (int64_t)tm * mrows + 128 * rank + 32 * qt + lane;
+            float rs[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int64_t m = mrow + 256 * h;
+                rs[h] = m < p.M && (h == 0 || !p.digits) ? __ldg(p.rscale + m) * p.mul : 0.f;
+            }
+            if (p.digits) {
+                for (int c = 0; c < 4; ++c) {
+                    const int col = cg * 128 + c * 32;
+                    uint32_t a[32], b[32];
+                    float v[32];
+                    tmem_ld32(tmem + lanes + col, a);
+                    tmem_ld32(tmem + lanes + 256 + col, b);
+                    if (c == 3) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_cluster(free0), mbar_arrive_cluster(free0 + 8);
+                    }
+#pragma unroll
+                    for (int j = 0; j < 32; ++j)
+                        v[j] = __fmaf_rn(__fmul_rn(__fmaf_rn((float)(int)a[j], 256.f, (float)(int)b[j]), rs[0]),
+                                         cs[col + j], cb[col + j]);
+                    store32(p, mrow, n0 + col, v);
+                }
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    for (int c = 0; c < 4; ++c) {
+                        const int col = cg * 128 + c * 32;
+                        uint32_t a[32];
+                        float v[32];
+                        tmem_ld32(tmem + lanes + h * 256 + col, a);
+                        if (c == 3) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive_cluster(free0 + 8 * h);
+                        }
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            v[j] = __fmaf_rn(__fmul_rn((float)(int)a[j], rs[h]), cs[col + j], cb[col + j]);
+                        store32(p, mrow + 256 * h, n0 + col, v);
+                    }
+            }
+        }
+        if (!ok) *abort_flag = 1;
+    }
+
+    if (!ok && p.status) atomicOr(p.status, QLORA_STATUS_TIMEOUT);
+    __syncwarp();   // reconverge single-lane roles before the barriers
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0 && lane == 0 && *abort_flag && rank == 0) {
+        // a wait gave up: time (tens of milliseconds) for both CTAs' copies to land
+        for (uint32_t i = 0; i < 20000; ++i) __nanosleep(1000);
+    }
+    __syncwarp();
+    cluster_sync();   // no CTA leaves while its peer may still signal it
+    if (warp == 1) {
+        tc_fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(512u));
+    }
+}
+
 }  // namespace
 
-int launch_int8_tall(const Int8Product &g, uint32_t *d_status, cudaStream_t st) {
+static int launch_int8_tall(const Int8Product &g, uint32_t *d_status, cudaStream_t st) {
     if (g.P <= 0 || g.Q <= 0) return QLORA_OK;
     TallParams p{};
     // columns per tile: all of them up to the UMMA's 256, else even tiles
@@ -355,6 +658,62 @@ int launch_int8_tall(const Int8Product &g, uint32_t *d_status, cudaStream_t st) 
     if (cudaLaunchKernelEx(&cfg, k_int8_tall, tA, tB, p) != cudaSuccess) return QLORA_ECUDA;
     QLORA_LAUNCH_CHECK();
     return QLORA_OK;
+}
+
+static int launch_int8_wide(const Int8Product &g, uint32_t *d_status, cudaStream_t st) {
+    WideParams p{};
+    p.M = g.Q;
+    p.N = g.P;
+    p.digits = g.planes == 2;
+    p.plane_rows = g.plane_rows;
+    p.nk = (int)((g.R + kTK - 1) / kTK);
+    const int mrows = p.digits ? 256 : 512;
+    p.mt = (int)((p.M + mrows - 1) / mrows);
+    p.nt = (int)((p.N + 255) / 256);
+    p.b_mn = g.a_mn;
+    p.rscale = g.qscale;
+    p.cscale = g.pscale;
+    p.mul = g.mul;
+    p.bias = g.bias;
+    p.out = g.out;
+    p.ldo = g.ldo;
+    p.dtype = g.dtype;
+    const uintptr_t at = reinterpret_cast<uintptr_t>(g.out) | (uintptr_t)(g.ldo * (g.dtype == QLORA_DTYPE_FP32 ? 4 : 2));
+    p.align = at % 32 == 0 ? 32 : (at % 16 == 0 ? 16 : 1);
+    p.pdl = g.pdl;
+    p.status = d_status;
+    const int64_t xrows = g.plane_rows * (g.planes - 1) + g.Q;
+    CUtensorMap tX, tW;
+    bool ok = make_map(&tX, g.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.R, xrows, g.ldb, kTK, 128,
+                       CU_TENSOR_MAP_SWIZZLE_128B);
+    ok = ok && (g.a_mn ? make_map(&tW, g.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.P, g.R, g.lda, 128, kTK,
+                                  CU_TENSOR_MAP_SWIZZLE_128B)
+                       : make_map(&tW, g.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.R, g.P, g.lda, kTK, 128,
+                                  CU_TENSOR_MAP_SWIZZLE_128B));
+    if (!ok) return QLORA_EUNSUPPORTED;
+    if (set_max_smem(reinterpret_cast<const void *>(k_int8_wide), kWSmemBytes) != cudaSuccess) return QLORA_ECUDA;
+    const int64_t tiles = (int64_t)p.mt * p.nt, pairs = device_sms() / 2;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
+    cfg.blockDim = dim3(kWThreads);
+    cfg.dynamicSmemBytes = kWSmemBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = g.pdl ? 1 : 0;
+    if (cudaLaunchKernelEx(&cfg, k_int8_wide, tX, tW, p) != cudaSuccess) return QLORA_ECUDA;
+    QLORA_LAUNCH_CHECK();
+    return QLORA_OK;
+}
+
+int launch_int8_product(const Int8Product &g, uint32_t *d_status, cudaStream_t st) {
+    if (g.P <= 0 || g.Q <= 0) return QLORA_OK;
+    const int64_t mrows = g.planes == 2 ? 256 : 512;
+    const int64_t tiles = ((g.Q + mrows - 1) / mrows) * ((g.P + 255) / 256);
+    if (!g.q_inner && g.planes <= 2 && g.Q > 128 && tiles >= device_sms() / 4) return launch_int8_wide(g, d_status, st);
+    return launch_int8_tall(g, d_status, st);
 }
 
 }  // namespace qlora

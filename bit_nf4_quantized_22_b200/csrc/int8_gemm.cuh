@@ -25,7 +25,7 @@ struct Int8Product {
     int pdl;               // launch beside the kernel before, which writes B and the scales but not A
 };
 
-int launch_int8_tall(const Int8Product &g, uint32_t *d_status, cudaStream_t st);
+int launch_int8_product(const Int8Product &g, uint32_t *d_status, cudaStream_t st);
 
 // int8_rows.cu
 int launch_int8_quantize(const void *X, int dtype, int64_t ldx, const int8_rows_t &q, uint32_t *d_status,

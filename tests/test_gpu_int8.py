@@ -119,7 +119,10 @@ def test_dequantize_exact(qlib, rows, cols, dtype):
 # ------------------------------------------------------------------------------ product
 MATMUL = [(1, 1, 1), (1, 64, 8), (1, 4096, 256), (2, 100, 130), (16, 4096, 1000), (17, 999, 77), (33, 257, 511),
           (64, 512, 384), (130, 1000, 264), (256, 640, 129), (257, 333, 128), (300, 128, 1001), (1000, 2048, 520),
-          (5, 131072, 8), (2049, 100, 16), (512, 4096, 4096), (700, 1500, 2504), (384, 96, 5000)]
+          (5, 131072, 8), (2049, 100, 16), (512, 4096, 4096), (700, 1500, 2504), (384, 96, 5000),
+          # many tokens: one tile a CTA pair and several, reductions shorter and longer than the ring
+          (1100, 200, 5000), (2600, 1500, 2504), (513, 96, 9999), (700, 5000, 333), (2100, 2053, 40),
+          (4100, 640, 3000), (4100, 200, 3001), (2100, 3000, 700), (9300, 130, 1000)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
