@@ -7,6 +7,7 @@ memory (tensors, the workspace) and streams.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from dataclasses import dataclass
 
@@ -22,12 +23,21 @@ DQ_GROUP = 256
 DQ_VARIANTS = {"u8": 1, "s8": 2, "mean": 3, "f8": 4}
 
 
+def _at(t: torch.Tensor | None):
+    return None if t is None else t.data_ptr()
+
+
 def _ptr(t: torch.Tensor | None):
     return None if t is None else ctypes.c_void_p(t.data_ptr())
 
 
 def _stream():
     return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+
+
+def _raw_stream(t: torch.Tensor) -> int:
+    """The current stream of t's device, without the Stream object (about 2 us of a call)."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _cb_host(codebook: torch.Tensor | None) -> ctypes.Array:
@@ -107,8 +117,7 @@ class Int8Rows:
 
     @staticmethod
     def empty(rows: int, cols: int, device="cuda") -> "Int8Rows":
-        ld = (cols + 15) // 16 * 16
-        codes = torch.empty(rows, ld, dtype=torch.int8, device=device)[:, :cols]
+        codes = torch.empty_strided((rows, cols), ((cols + 15) // 16 * 16, 1), dtype=torch.int8, device=device)
         return Int8Rows(codes, torch.empty(rows, dtype=torch.float32, device=device))
 
     @property
@@ -129,17 +138,20 @@ class Int8Rows:
 
     def c_struct(self) -> _lib.Int8RowsC:
         c, s = self.codes, self.scales
-        if c.dtype != torch.int8 or c.dim() != 2 or s.dtype != torch.float32 or s.dim() != 1:
+        if c.dtype != torch.int8 or s.dtype != torch.float32 or c.dim() != 2 or s.dim() != 1:
             raise TypeError("Int8Rows: codes int8 [rows, cols] and scales fp32 [rows] are needed")
-        if not c.is_cuda or s.device != c.device:
+        if not c.is_cuda or s.get_device() != c.get_device():
             raise TypeError("Int8Rows: codes and scales must be CUDA tensors of one device")
         rows, cols = c.shape
-        if s.shape[0] != rows or not s.is_contiguous():
+        ld, unit = c.stride()
+        if rows <= 1:
+            ld = (cols + 15) // 16 * 16
+        at = c.data_ptr()
+        if s.shape[0] != rows or (rows > 1 and s.stride(0) != 1):
             raise ValueError("Int8Rows: one scale a row, contiguous")
-        ld = c.stride(0) if rows > 1 else (max(cols, 1) + 15) // 16 * 16
-        if cols < 1 or (cols > 1 and c.stride(1) != 1) or ld < cols or ld % 16 or c.data_ptr() % 16:
+        if cols < 1 or (unit != 1 and cols > 1) or ld < cols or ld % 16 or at % 16:
             raise ValueError("Int8Rows: codes need a unit column stride, and 16-byte aligned rows")
-        return _lib.Int8RowsC(rows, cols, ld, c.data_ptr(), s.data_ptr())
+        return _lib.Int8RowsC(rows, cols, ld, at, s.data_ptr())
 
 
 def load():
@@ -276,7 +288,7 @@ def _backward_int8(x: Int8Rows, dy, q: NF4Weight, A, B, alpha, pool_group, T, ne
     _need(A, q.compute_dtype, "A", 2)
     _need(B, q.compute_dtype, "B", 2)
     M, r = dy.shape[0], A.shape[1]
-    dev = _one_device(dy, x, A, B, T, workspace, status, q.packed)
+    dev = dy.device
     if tuple(dy.shape) != (x.rows, q.rows) or x.cols != q.cols:
         raise ValueError(f"dy [{x.rows}, {q.rows}] and x [{M}, {q.cols}] are needed")
     if pool_group not in (1, 64) or tuple(A.shape) != (q.cols // pool_group, r) or tuple(B.shape) != (r, q.rows):
@@ -285,7 +297,7 @@ def _backward_int8(x: Int8Rows, dy, q: NF4Weight, A, B, alpha, pool_group, T, ne
         _need(T, torch.float32, "T", 2)
         if tuple(T.shape) != (M, r):
             raise ValueError(f"T [{M}, {r}] is needed")
-    with torch.cuda.device(dev):
+    with _on(dy, x.codes, A, B, T, workspace, status, q.packed):
         new = torch.empty if M else torch.zeros      # no token: the adapter gradients are zero
         dX = torch.empty(M, q.cols, dtype=q.compute_dtype, device=dev) if need_dx else None
         dA = new(A.shape[0], r, dtype=torch.float32, device=dev) if need_dA else None
@@ -295,35 +307,45 @@ def _backward_int8(x: Int8Rows, dy, q: NF4Weight, A, B, alpha, pool_group, T, ne
         ws, nbytes = _workspace(need, dev, workspace)
         rc = load().qlora_backward_int8(ctypes.byref(xc), _ptr(dy), M, ctypes.byref(qc), _cb_host(codebook),
                                         _ptr(A), _ptr(B), r, float(alpha), pool_group, _ptr(T), _ptr(dX),
-                                        _ptr(dA), _ptr(dB), _ptr(ws), nbytes, _ptr(status), _stream())
+                                        _ptr(dA), _ptr(dB), _ptr(ws), nbytes, _ptr(status), _raw_stream(dy))
         _lib.check(rc, "qlora_backward_int8")
     return dX, dA, dB
 
 
-def _one_device(*tensors) -> torch.device:
-    dev = tensors[0].device
-    for t in tensors[1:]:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors of one device are needed: {dev} and {t.device} were given")
-    return dev
+def _on(t: torch.Tensor, *others):
+    """A context in which t's device is the current one; the others must be on it too."""
+    dev = t.get_device()
+    for o in others:
+        if o is not None and o.get_device() != dev:
+            raise ValueError(f"tensors of one device are needed: {t.device} and {o.device} were given")
+    return _HERE if dev == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
+_HERE = contextlib.nullcontext()
 
 
 def int8_quantize(x: torch.Tensor, out: Int8Rows | None = None,
                   status: torch.Tensor | None = None) -> Int8Rows:
     """The rows of x (bf16, fp16 or fp32 [rows, cols], unit column stride) in 8 bits,
     one scale a row: a token's activation, or an output channel of a weight Wt."""
-    if not isinstance(x, torch.Tensor) or x.dtype not in _DTYPE_CODES or x.dim() != 2 or not x.is_cuda:
-        raise TypeError("x: expected a 2-D bf16, fp16 or fp32 CUDA tensor")
+    dtype = _any_float(x, "x")
     rows, cols, ldx = _row_stride(x, "x")
     q = out if out is not None else Int8Rows.empty(rows, cols, x.device)
-    if (q.rows, q.cols) != (rows, cols):
+    if out is not None and (q.rows, q.cols) != (rows, cols):
         raise ValueError(f"out: [{rows}, {cols}] is needed")
-    with torch.cuda.device(_one_device(x, q, status)):
-        qc = q.c_struct()
-        rc = load().int8_quantize(_ptr(x), _DTYPE_CODES[x.dtype], ldx, ctypes.byref(qc), _ptr(status),
-                                  _stream())
+    with _on(x, q.codes, status):
+        rc = load().int8_quantize(x.data_ptr(), dtype, ldx, ctypes.byref(q.c_struct()), _at(status),
+                                  _raw_stream(x))
         _lib.check(rc, "int8_quantize")
     return q
+
+
+def _any_float(x, name: str) -> int:
+    if isinstance(x, torch.Tensor) and x.is_cuda and x.dim() == 2:
+        code = _DTYPE_CODES.get(x.dtype)
+        if code is not None:
+            return code
+    raise TypeError(f"{name}: expected a 2-D bf16, fp16 or fp32 CUDA tensor")
 
 
 def _row_stride(x: torch.Tensor, name: str):
@@ -343,9 +365,9 @@ def int8_dequantize(q: Int8Rows, dtype: torch.dtype = torch.bfloat16,
     _need(out, dtype, "out", 2)
     if tuple(out.shape) != (q.rows, q.cols):
         raise ValueError(f"out: [{q.rows}, {q.cols}] is needed")
-    with torch.cuda.device(_one_device(out, q)):
+    with _on(out, q.codes):
         qc = q.c_struct()
-        _lib.check(load().int8_dequantize(ctypes.byref(qc), _DTYPE_CODES[dtype], _ptr(out), _stream()),
+        _lib.check(load().int8_dequantize(ctypes.byref(qc), _DTYPE_CODES[dtype], out.data_ptr(), _raw_stream(out)),
                    "int8_dequantize")
     return out
 
@@ -359,34 +381,45 @@ def int8_matmul(x: torch.Tensor | Int8Rows, w: Int8Rows, bias: torch.Tensor | No
     default, bf16 for 8-bit rows.  `x8_out` receives a tensor x's rows, to be kept as the
     checkpoint of backward()."""
     given = isinstance(x, Int8Rows)
-    if not given and (not isinstance(x, torch.Tensor) or x.dtype not in _DTYPE_CODES or x.dim() != 2
-                      or not x.is_cuda):
-        raise TypeError("x: expected Int8Rows or a 2-D bf16, fp16 or fp32 CUDA tensor")
+    xdt = 0 if given else _any_float(x, "x")
     if dtype is None:
         dtype = out.dtype if out is not None else (torch.bfloat16 if given else x.dtype)
     if dtype not in _DTYPE_CODES:
         raise TypeError(f"dtype: one of {list(_DTYPE_CODES)}")
     if given and x8_out is not None:
         raise ValueError("x8_out: only for a tensor x")
-    M, K, ldx = (x.rows, x.cols, 0) if given else _row_stride(x, "x")
-    if K != w.cols:
-        raise ValueError(f"x has {K} columns, w {w.cols}")
-    x8 = x if given else (x8_out if x8_out is not None else Int8Rows.empty(M, K, x.device))
-    if (x8.rows, x8.cols) != (M, K):
-        raise ValueError(f"x8_out: [{M}, {K}] is needed")
-    y = out if out is not None else torch.empty(M, w.rows, dtype=dtype, device=x.device)
-    _need(y, dtype, "out", 2)
-    if tuple(y.shape) != (M, w.rows):
-        raise ValueError(f"out: [{M}, {w.rows}] is needed")
+    wc = w.c_struct()
+    N = wc.rows
+    if given:
+        xc, ldx, at = x.c_struct(), 0, None
+        M, K = xc.rows, xc.cols
+    else:
+        M, K, ldx = _row_stride(x, "x")
+        at = x.data_ptr()
+        if x8_out is not None:
+            xc = x8_out.c_struct()
+            if (xc.rows, xc.cols) != (M, K):
+                raise ValueError(f"x8_out: [{M}, {K}] is needed")
+        else:   # codes and scales in one scratch tensor
+            ld = (K + 15) // 16 * 16
+            scratch = torch.empty(M * (ld + 4), dtype=torch.uint8, device=x.device)
+            xc = _lib.Int8RowsC(M, K, ld, scratch.data_ptr(), scratch.data_ptr() + M * ld)
+    if K != wc.cols:
+        raise ValueError(f"x has {K} columns, w {wc.cols}")
+    if out is None:
+        y = torch.empty((M, N), dtype=dtype, device=w.codes.device)
+    else:
+        y = out
+        _need(y, dtype, "out", 2)
+        if tuple(y.shape) != (M, N):
+            raise ValueError(f"out: [{M}, {N}] is needed")
     if bias is not None:
         _need(bias, dtype, "bias", 1)
-        if bias.shape[0] != w.rows:
-            raise ValueError(f"bias: [{w.rows}] is needed")
-    with torch.cuda.device(_one_device(x, w, x8, y, bias, status)):
-        xc, wc = x8.c_struct(), w.c_struct()
-        rc = load().int8_matmul(None if given else _ptr(x), 0 if given else _DTYPE_CODES[x.dtype], ldx,
-                                ctypes.byref(xc), ctypes.byref(wc), _ptr(bias), _ptr(y),
-                                _DTYPE_CODES[dtype], _ptr(status), _stream())
+        if bias.shape[0] != N:
+            raise ValueError(f"bias: [{N}] is needed")
+    with _on(y, w.codes, x.codes if given else x, None if x8_out is None else x8_out.codes, bias, status):
+        rc = load().int8_matmul(at, xdt, ldx, ctypes.byref(xc), ctypes.byref(wc), _at(bias), y.data_ptr(),
+                                _DTYPE_CODES[dtype], _at(status), _raw_stream(y))
         _lib.check(rc, "int8_matmul")
     return y
 
@@ -398,19 +431,22 @@ def int8_matmul_backward(dy: torch.Tensor, w: Int8Rows, out: torch.Tensor | None
     if not isinstance(dy, torch.Tensor) or dy.dtype not in (torch.bfloat16, torch.float16):
         raise TypeError("dy: expected a 2-D bf16 or fp16 tensor")
     _need(dy, dy.dtype, "dy", 2)
-    M = dy.shape[0]
-    if dy.shape[1] != w.rows:
-        raise ValueError(f"dy has {dy.shape[1]} columns, w {w.rows} rows")
-    dX = out if out is not None else torch.empty(M, w.cols, dtype=dy.dtype, device=dy.device)
-    _need(dX, dy.dtype, "out", 2)
-    if tuple(dX.shape) != (M, w.cols):
-        raise ValueError(f"out: [{M}, {w.cols}] is needed")
-    with torch.cuda.device(_one_device(dy, w, dX, workspace, status)):
-        wc = w.c_struct()
-        need = int(load().int8_matmul_backward_workspace_size(M, ctypes.byref(wc)))
+    wc = w.c_struct()
+    M, N = dy.shape
+    if N != wc.rows:
+        raise ValueError(f"dy has {N} columns, w {wc.rows} rows")
+    if out is None:
+        dX = torch.empty((M, wc.cols), dtype=dy.dtype, device=dy.device)
+    else:
+        dX = out
+        _need(dX, dy.dtype, "out", 2)
+        if tuple(dX.shape) != (M, wc.cols):
+            raise ValueError(f"out: [{M}, {wc.cols}] is needed")
+    with _on(dy, w.codes, dX, workspace, status):
+        need = load().int8_matmul_backward_workspace_size(M, ctypes.byref(wc))
         ws, nbytes = _workspace(need, dy.device, workspace)
-        rc = load().int8_matmul_backward(_ptr(dy), _DTYPE_CODES[dy.dtype], M, ctypes.byref(wc), _ptr(dX),
-                                         _ptr(ws), nbytes, _ptr(status), _stream())
+        rc = load().int8_matmul_backward(dy.data_ptr(), _DTYPE_CODES[dy.dtype], M, ctypes.byref(wc),
+                                         dX.data_ptr(), _at(ws), nbytes, _at(status), _raw_stream(dy))
         _lib.check(rc, "int8_matmul_backward")
     return dX
 

@@ -13,8 +13,8 @@ PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libqlora.so")
-SOURCES = ["api.cu", "codebook.cpp", "quantize.cu", "gemv.cu", "adapter.cu", "umma_gemm.cu", "profile.cu", "noalloc.cu", "umma_skinny.cu", "merge.cu", "selftest.cu", "int8_rows.cu", "int8_gemm.cu"]
-HEADERS = ["common.cuh", "tcgen05.cuh", "int8_gemm.cuh"]
+SOURCES = ["api.cu", "codebook.cpp", "quantize.cu", "gemv.cu", "adapter.cu", "umma_gemm.cu", "profile.cu", "noalloc.cu", "umma_skinny.cu", "merge.cu", "selftest.cu", "int8_rows.cu", "int8_gemm.cu", "int8_gemv.cu"]
+HEADERS = ["common.cuh", "tcgen05.cuh", "int8_gemm.cuh", "int8_rows.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

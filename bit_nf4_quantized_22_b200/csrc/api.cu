@@ -359,7 +359,7 @@ int run_adapter_down(const Dims &d, const uint16_t *X, const uint16_t *A, uint16
 constexpr int64_t kInt8MaxTerms = 131072;
 
 int check_rows8(const int8_rows_t *q) {
-    if (!q || q->rows < 0 || q->rows > (int64_t)0x7fffffff || q->cols < 1 || q->cols > (int64_t)0x7fffffff)
+    if (!q || q->rows < 0 || q->rows > (int64_t)0x7fffffff || q->cols < 1 || q->cols > (int64_t)1 << 30)
         return QLORA_EINVAL;
     if (q->ld < q->cols || q->ld % 16 != 0) return QLORA_EINVAL;
     if (q->rows == 0) return QLORA_OK;
@@ -713,6 +713,8 @@ int int8_matmul(const void *X, int32_t x_dtype, int64_t ldx, const int8_rows_t *
     if (X8->rows == 0 || W->rows == 0) return QLORA_OK;
     if (!Y || !aligned_to(Y, y_dtype) || (bias && !aligned_to(bias, y_dtype))) return QLORA_EINVAL;
     cudaStream_t st = (cudaStream_t)stream;
+    if (int8_gemv_takes(X8->rows, W->cols))
+        return launch_int8_gemv(X, x_dtype, ldx, *X8, *W, bias, Y, y_dtype, d_status, st);
     if (X) RC(launch_int8_quantize(X, x_dtype, ldx, *X8, d_status, st));
     Int8Product g{};
     g.a = W->codes, g.lda = W->ld;

@@ -54,8 +54,7 @@ __device__ __forceinline__ int4 ld_cluster_int4(uint32_t addr) {
     int4 v;
     asm volatile("ld.shared::cluster.v4.s32 {%0,%1,%2,%3}, [%4];\n"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "r"(addr)
-                 : "memory");
+                 : "r"(addr));
     return v;
 }
 
@@ -77,11 +76,6 @@ struct TallParams {
     int pdl;               // B and the scales come from the kernel before (programmatic launch)
     uint32_t *status;
 };
-
-__device__ __forceinline__ float load_any(const void *p, int64_t i, int dtype) {
-    if (dtype == QLORA_DTYPE_FP32) return __ldg(static_cast<const float *>(p) + i);
-    return dec16(__ldg(static_cast<const uint16_t *>(p) + i), dtype == QLORA_DTYPE_FP16);
-}
 
 // CTA (x, y, z): rows [128 x, +128) of A, rows [nt y, +nt) of each plane of B,
 // k-tiles [per z, +per).  Warp 0 loads by TMA into a ring of stages, warp 1
@@ -238,14 +232,17 @@ k_int8_tall(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             for (int d = 0; d < p.planes; ++d) {
                 int4 t = make_int4(0, 0, 0, 0);
                 const uint32_t at = base + ((d * p.nt + c) * kTP + 4 * lane) * 4;
-                for (uint32_t z = 0; z < splits; ++z) {
-                    const int4 v = ld_cluster_int4(mapa_shared(at, z));
-                    t.x += v.x, t.y += v.y, t.z += v.z, t.w += v.w;
-                }
+                int4 v[kTMaxSplits];                  // all in flight: a peer's memory is far
+#pragma unroll
+                for (uint32_t z = 0; z < kTMaxSplits; ++z)
+                    if (z < splits) v[z] = ld_cluster_int4(mapa_shared(at, z));
+#pragma unroll
+                for (uint32_t z = 0; z < kTMaxSplits; ++z)
+                    if (z < splits) t.x += v[z].x, t.y += v[z].y, t.z += v[z].z, t.w += v[z].w;
                 sum[0] = sum[0] * 256 + t.x, sum[1] = sum[1] * 256 + t.y;
                 sum[2] = sum[2] * 256 + t.z, sum[3] = sum[3] * 256 + t.w;
             }
-            const float qs = __ldg(p.qscale + q);
+            const float qs = __ldcg(p.qscale + q);   // may be the kernel before's: not the read-only path
             float v[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e)
@@ -528,7 +525,7 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int64_t m = mrow + 256 * h;
-                rs[h] = m < p.M && (h == 0 || !p.digits) ? __ldg(p.rscale + m) * p.mul : 0.f;
+                rs[h] = m < p.M && (h == 0 || !p.digits) ? __ldcg(p.rscale + m) * p.mul : 0.f;
             }
             if (p.digits) {
                 for (int c = 0; c < 4; ++c) {

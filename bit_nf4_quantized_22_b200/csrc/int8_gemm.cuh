@@ -27,6 +27,18 @@ struct Int8Product {
 
 int launch_int8_product(const Int8Product &g, uint32_t *d_status, cudaStream_t st);
 
+// int8_gemv.cu: M <= 8 tokens whose codes fit in a CTA's share of shared memory
+constexpr int64_t kGemvTokenBytes = 96 * 1024;
+constexpr int64_t kGemvFusedValues = 16384;   // tokens of so few values are quantized by every CTA itself
+bool int8_gemv_takes(int64_t M, int64_t K);
+int launch_int8_gemv(const void *X, int x_dtype, int64_t ldx, const int8_rows_t &X8, const int8_rows_t &W,
+                     const void *bias, void *Y, int dtype, uint32_t *d_status, cudaStream_t st);
+
+__device__ __forceinline__ float load_any(const void *p, int64_t i, int dtype) {
+    if (dtype == QLORA_DTYPE_FP32) return __ldg(static_cast<const float *>(p) + i);
+    return dec16(__ldg(static_cast<const uint16_t *>(p) + i), dtype == QLORA_DTYPE_FP16);
+}
+
 // int8_rows.cu
 int launch_int8_quantize(const void *X, int dtype, int64_t ldx, const int8_rows_t &q, uint32_t *d_status,
                          cudaStream_t st);

@@ -122,7 +122,10 @@ MATMUL = [(1, 1, 1), (1, 64, 8), (1, 4096, 256), (2, 100, 130), (16, 4096, 1000)
           (5, 131072, 8), (2049, 100, 16), (512, 4096, 4096), (700, 1500, 2504), (384, 96, 5000),
           # many tokens: one tile a CTA pair and several, reductions shorter and longer than the ring
           (1100, 200, 5000), (2600, 1500, 2504), (513, 96, 9999), (700, 5000, 333), (2100, 2053, 40),
-          (4100, 640, 3000), (4100, 200, 3001), (2100, 3000, 700), (9300, 130, 1000)]
+          (4100, 640, 3000), (4100, 200, 3001), (2100, 3000, 700), (9300, 130, 1000),
+          # a few tokens: quantized by the product's own CTAs or before it, rows in one wave and several
+          (3, 1000, 2500), (8, 2048, 9500), (4, 513, 5000), (7, 12000, 33), (1, 28672, 100), (2, 8192, 5003),
+          (1, 16385, 3000), (6, 15, 20000)]
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
@@ -137,9 +140,9 @@ def test_matmul(qlib, M, K, N, dtype):
     y = qlib.int8_matmul(x, w, x8_out=x8, status=status)
     check_rows(x8, x)
     assert int(status.item()) == 0
-    want = ref.matmul32(x8.codes.cpu().numpy(), x8.scales.cpu().numpy(), w.codes.cpu().numpy(),
-                        w.scales.cpu().numpy())
-    assert torch.equal(y.cpu(), torch.from_numpy(want).to(DT[dtype]))
+    acc = x8.codes.double() @ w.codes.double().t()      # exact: far below 2^53
+    want = (acc.float() * x8.scales[:, None]) * w.scales[None]
+    assert torch.equal(y, want.to(DT[dtype]))
     # rows that are in 8 bits already, into an `out` between guards
     buf = torch.full((M + 2, N), 5.0, dtype=DT[dtype], device="cuda")
     y2 = qlib.int8_matmul(x8, w, out=buf[1:M + 1])
