@@ -713,7 +713,7 @@ int int8_matmul(const void *X, int32_t x_dtype, int64_t ldx, const int8_rows_t *
     if (X8->rows == 0 || W->rows == 0) return QLORA_OK;
     if (!Y || !aligned_to(Y, y_dtype) || (bias && !aligned_to(bias, y_dtype))) return QLORA_EINVAL;
     cudaStream_t st = (cudaStream_t)stream;
-    if (int8_gemv_takes(X8->rows, W->cols))
+    if (int8_gemv_takes(X8->rows, W->rows, W->cols))
         return launch_int8_gemv(X, x_dtype, ldx, *X8, *W, bias, Y, y_dtype, d_status, st);
     if (X) RC(launch_int8_quantize(X, x_dtype, ldx, *X8, d_status, st));
     Int8Product g{};

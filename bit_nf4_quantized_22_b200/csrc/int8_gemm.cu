@@ -27,19 +27,50 @@ constexpr int kTABytes = kTP * kTK;            // 16 KB
 constexpr int kTThreads = 192;
 constexpr int kTMaxStages = 8;
 constexpr int kTMaxSplits = 8;                 // portable cluster size
-constexpr int kTSmemTwo = 112 * 1024;          // two CTAs fit on an SM
-constexpr int kTSmemOne = 222 * 1024;
+constexpr int kTTwoN = 64;                     // UMMA N up to which two CTAs share an SM
+constexpr int kTSmemTwo = 110 * 1024;
+constexpr int kTSmemOne = 220 * 1024;
 
 // kind::i8 instruction descriptor: signed 8-bit A and B, s32 accumulator.
 __host__ __device__ constexpr uint32_t idesc_i8(uint32_t m, uint32_t n, uint32_t a_mn, uint32_t b_mn) {
     return (2u << 4) | (1u << 7) | (1u << 10) | (a_mn << 15) | (b_mn << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
 }
-__device__ __forceinline__ void umma_i8(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+// The warp's index and its elected lane, in forms that the compiler knows to be
+// the same for all lanes: the MMAs' descriptors then stay in uniform registers.
+// (Issued from inside `if (lane == 0)` each MMA took some 175 cycles whatever
+// its size, which bounded both kernels below.)
+__device__ __forceinline__ int warp_index() { return __shfl_sync(0xffffffffu, (int)threadIdx.x >> 5, 0); }
+__device__ __forceinline__ bool elect_one() {
+    uint32_t e;
     asm volatile(
         "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}\n"
+        : "=r"(e));
+    return e != 0;
+}
+// One k-tile of 128 reduction values: four MMAs, by one elected lane of a
+// converged warp; the first adds to the accumulator only if acc.
+__device__ __forceinline__ void umma_i8_ktile(uint32_t d_tmem, uint64_t a, uint64_t b, uint64_t astep, uint64_t bstep,
+                                              uint32_t idesc, uint32_t acc) {
+    asm volatile(
+        "{\n\t.reg .pred e, p, q;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %10, 0;\n\t"
+        "setp.eq.b32 q, %10, %10;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::i8 [%0], %1, %2, %9, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::i8 [%0], %3, %4, %9, q;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::i8 [%0], %5, %6, %9, q;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::i8 [%0], %7, %8, %9, q;\n\t}\n" ::"r"(d_tmem),
+        "l"(a), "l"(b), "l"(a + astep), "l"(b + bstep), "l"(a + 2 * astep), "l"(b + 2 * bstep), "l"(a + 3 * astep),
+        "l"(b + 3 * bstep), "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void umma_commit_elect(uint32_t bar) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar)
+        : "memory");
 }
 __device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&v)[16]) {
     asm volatile(
@@ -96,8 +127,9 @@ k_int8_tall(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     const uint32_t acc_bar = bar0 + 8u * (2 * kTMaxStages);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(gen_base + S * p.stage_bytes + 160);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gen_base + S * p.stage_bytes + 192);
+    float *qs = reinterpret_cast<float *>(gen_base + S * p.stage_bytes + 256);   // [nt <= 256]
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     const int64_t p0 = (int64_t)blockIdx.x * kTP;
     const int64_t q0 = (int64_t)blockIdx.y * p.nt;
     const int kbeg = blockIdx.z * p.per;
@@ -106,7 +138,24 @@ k_int8_tall(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     const int N = p.planes * p.nt;
     const uint32_t rank = blockIdx.z, splits = gridDim.z;
 
-    if (threadIdx.x == 0) {
+    bool ok = true;
+    const int head = nloc < S ? nloc : S;          // k-tiles that find their stage free
+    // tile i of this CTA into stage s
+    auto load_a = [&](int i, int s) {
+        const uint32_t sa = base + s * p.stage_bytes;
+        const int t0 = (kbeg + i) * kTK;
+        mbar_expect_tx(full_bar(s), p.stage_bytes);
+        if (p.a_mn) tma_load_2d(sa, &tmA, (int)p0, t0, full_bar(s));
+        else tma_load_2d(sa, &tmA, t0, (int)p0, full_bar(s));
+    };
+    auto load_b = [&](int i, int s) {
+        const uint32_t sb = base + s * p.stage_bytes + kTABytes;
+        const int t0 = (kbeg + i) * kTK;
+        for (int d = 0; d < p.planes; ++d)
+            tma_load_2d(sb + d * p.nt * kTK, &tmB, t0, (int)(d * p.plane_rows + q0), full_bar(s));
+    };
+    const bool leader = elect_one();               // one lane of each warp
+    if (warp == 0 && leader) {
         for (int s = 0; s < S; ++s) {
             mbar_init(full_bar(s), 1);
             mbar_init(empty_bar(s), 1);
@@ -115,75 +164,61 @@ k_int8_tall(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
         fence_proxy_async();
+        // A fills the ring at once; with pdl it is all that does not depend on the kernel before
+        for (int i = 0; i < head; ++i) load_a(i, i);
     }
     if (warp == 1) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;\n" ::"r"(smem_u32(tmem_holder)),
                      "r"(p.tmem_cols));
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;\n");
     }
+    if (warp == 0 && leader) {
+        if (p.pdl) asm volatile("griddepcontrol.wait;\n" ::: "memory");
+        for (int i = 0; i < head; ++i) load_b(i, i);
+    }
+    __syncwarp();
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
-    bool ok = true;
 
     if (warp == 0) {
-        if (lane == 0) {
-            auto load_a = [&](int i) {
-                const int s = i % S;
-                const uint32_t sa = base + s * p.stage_bytes;
-                const int t0 = (kbeg + i) * kTK;
-                mbar_expect_tx(full_bar(s), p.stage_bytes);
-                if (p.a_mn) tma_load_2d(sa, &tmA, (int)p0, t0, full_bar(s));
-                else tma_load_2d(sa, &tmA, t0, (int)p0, full_bar(s));
-            };
-            auto load_b = [&](int i) {
-                const int s = i % S;
-                const uint32_t sb = base + s * p.stage_bytes + kTABytes;
-                const int t0 = (kbeg + i) * kTK;
-                for (int d = 0; d < p.planes; ++d)
-                    tma_load_2d(sb + d * p.nt * kTK, &tmB, t0, (int)(d * p.plane_rows + q0), full_bar(s));
-            };
-            int head = 0;
-            if (p.pdl) {
-                // the weight does not depend on the kernel before: fill the ring with it first
-                head = nloc < S ? nloc : S;
-                for (int i = 0; i < head; ++i) load_a(i);
-                asm volatile("griddepcontrol.wait;\n" ::: "memory");
-                for (int i = 0; i < head; ++i) load_b(i);
-            }
-            for (int i = head; i < nloc && ok; ++i) {
-                const int s = i % S;
-                if (i >= S) ok = mbar_wait(empty_bar(s), ((i / S) & 1) ^ 1, abort_flag);
+        if (leader) {
+            int s = 0;
+            uint32_t parity = 0;
+            for (int i = head; i < nloc; ++i) {
+                ok = mbar_wait(empty_bar(s), parity, abort_flag);
                 if (!ok) break;
-                load_a(i);
-                load_b(i);
+                load_a(i, s);
+                load_b(i, s);
+                if (++s == S) s = 0, parity ^= 1;
             }
             if (!ok) *abort_flag = 1;
         }
     } else if (warp == 1) {
-        if (lane == 0) {
-            const uint32_t idesc = idesc_i8(kTP, (uint32_t)N, p.a_mn ? 1u : 0u, 0u);
-            // K-major: rows of 128 t, 8-row groups 1 KB apart, a step of 32 t
-            // advances 32 B.  MN-major: rows of 128 p, 8 t a 1 KB group, a step
-            // of 32 t advances 4 KB (one 128-wide atom, so no leading stride).
-            const uint32_t astep = p.a_mn ? 256u : 2u;
-            for (int i = 0; i < nloc && ok; ++i) {
-                const int s = i % S;
-                ok = mbar_wait(full_bar(s), (i / S) & 1, abort_flag);
-                if (!ok) break;
-                tc_fence_after();
-                const uint32_t sa = base + s * p.stage_bytes;
-                const uint64_t ad = sdesc(sa, 16, 1024), bd = sdesc(sa + kTABytes, 16, 1024);
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    umma_i8(tmem, ad + kk * astep, bd + kk * 2, idesc, (i > 0 || kk > 0) ? 1u : 0u);
-                umma_commit(empty_bar(s));
-            }
-            if (ok) umma_commit(acc_bar);
-            else *abort_flag = 1;
+        const uint32_t idesc = idesc_i8(kTP, (uint32_t)N, p.a_mn ? 1u : 0u, 0u);
+        // K-major: rows of 128 t, 8-row groups 1 KB apart, a step of 32 t
+        // advances 32 B.  MN-major: rows of 128 p, 8 t a 1 KB group, a step
+        // of 32 t advances 4 KB (one 128-wide atom, so no leading stride).
+        const uint64_t astep = p.a_mn ? 256u : 2u;
+        uint32_t s = 0, parity = 0;
+        uint64_t ad = sdesc(base, 16, 1024);
+        const uint64_t bdiff = kTABytes >> 4, sdiff = p.stage_bytes >> 4;
+        for (int i = 0; i < nloc; ++i) {
+            ok = __all_sync(0xffffffffu, mbar_wait(full_bar(s), parity, abort_flag));   // the warp stays together
+            if (!ok) break;
+            tc_fence_after();
+            umma_i8_ktile(tmem, ad, ad + bdiff, astep, 2, idesc, i > 0 ? 1u : 0u);
+            umma_commit_elect(empty_bar(s));
+            ad += sdiff;
+            if (++s == (uint32_t)S) s = 0, parity ^= 1, ad = sdesc(base, 16, 1024);
         }
+        if (ok) umma_commit_elect(acc_bar);
+        else *abort_flag = 1;
     } else {
+        if (p.pdl) asm volatile("griddepcontrol.wait;\n" ::: "memory");
+        for (int c = threadIdx.x - 64; c < p.nt; c += kTThreads - 64)   // not the read-only path: may be the kernel before's
+            qs[c] = q0 + c < p.Q ? __ldcg(p.qscale + q0 + c) * p.mul : 0.f;
         ok = __all_sync(0xffffffffu, mbar_wait(acc_bar, 0, abort_flag));
         if (ok) {
             // TMEM -> the idle ring, as int32 [column][128 rows]
@@ -214,39 +249,47 @@ k_int8_tall(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         }
     }
     __syncwarp();
-    cluster_sync();   // the cluster's sums are in shared memory
-    if (p.pdl) asm volatile("griddepcontrol.wait;\n" ::: "memory");
-    {
-        const int64_t prow = p0 + 4 * lane;
-        float ps[4], bs[4];
+    const int64_t prow = p0 + 4 * lane;
+    float ps[4], bs[4];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const bool in = prow + e < p.P;
-            ps[e] = in && p.pscale ? __ldg(p.pscale + prow + e) : 1.f;
-            bs[e] = in && p.bias ? load_any(p.bias, prow + e, p.dtype) : 0.f;
-        }
+    for (int e = 0; e < 4; ++e) {
+        const bool in = prow + e < p.P;
+        ps[e] = in && p.pscale ? __ldg(p.pscale + prow + e) : 1.f;
+        bs[e] = in && p.bias ? load_any(p.bias, prow + e, p.dtype) : 0.f;
+    }
+    cluster_sync();   // the cluster's sums are in shared memory
+    {
+        // column c of plane d over the splits, 4 rows
+        auto column = [&](int d, int c) {
+            int4 t = make_int4(0, 0, 0, 0);
+            const uint32_t at = base + ((d * p.nt + c) * kTP + 4 * lane) * 4;
+            int4 v[kTMaxSplits];                  // all in flight: a peer's memory is far
+#pragma unroll
+            for (uint32_t z = 0; z < kTMaxSplits; ++z)
+                if (z < splits) v[z] = ld_cluster_int4(mapa_shared(at, z));
+#pragma unroll
+            for (uint32_t z = 0; z < kTMaxSplits; ++z)
+                if (z < splits) t.x += v[z].x, t.y += v[z].y, t.z += v[z].z, t.w += v[z].w;
+            return t;
+        };
+#pragma unroll 4
         for (int c = (int)rank + warp * (int)splits; c < p.nt; c += (kTThreads / 32) * (int)splits) {
             const int64_t q = q0 + c;
             if (q >= p.Q) break;
-            int64_t sum[4] = {0, 0, 0, 0};
-            for (int d = 0; d < p.planes; ++d) {
-                int4 t = make_int4(0, 0, 0, 0);
-                const uint32_t at = base + ((d * p.nt + c) * kTP + 4 * lane) * 4;
-                int4 v[kTMaxSplits];                  // all in flight: a peer's memory is far
+            int4 t = column(0, c);
+            float v[4] = {(float)t.x, (float)t.y, (float)t.z, (float)t.w};
+            if (p.planes > 1) {
+                int64_t sum[4] = {t.x, t.y, t.z, t.w};
+                for (int d = 1; d < p.planes; ++d) {
+                    t = column(d, c);
+                    sum[0] = sum[0] * 256 + t.x, sum[1] = sum[1] * 256 + t.y;
+                    sum[2] = sum[2] * 256 + t.z, sum[3] = sum[3] * 256 + t.w;
+                }
 #pragma unroll
-                for (uint32_t z = 0; z < kTMaxSplits; ++z)
-                    if (z < splits) v[z] = ld_cluster_int4(mapa_shared(at, z));
-#pragma unroll
-                for (uint32_t z = 0; z < kTMaxSplits; ++z)
-                    if (z < splits) t.x += v[z].x, t.y += v[z].y, t.z += v[z].z, t.w += v[z].w;
-                sum[0] = sum[0] * 256 + t.x, sum[1] = sum[1] * 256 + t.y;
-                sum[2] = sum[2] * 256 + t.z, sum[3] = sum[3] * 256 + t.w;
+                for (int e = 0; e < 4; ++e) v[e] = __ll2float_rn(sum[e]);
             }
-            const float qs = __ldcg(p.qscale + q);   // may be the kernel before's: not the read-only path
-            float v[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                v[e] = __fmaf_rn(__fmul_rn(__fmul_rn(__ll2float_rn(sum[e]), qs), p.mul), ps[e], bs[e]);
+            for (int e = 0; e < 4; ++e) v[e] = __fmaf_rn(__fmul_rn(v[e], qs[c]), ps[e], bs[e]);
             if (p.q_inner) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
@@ -315,13 +358,28 @@ struct WideParams {
     uint32_t *status;
 };
 
-__device__ __forceinline__ void umma_i8_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
-                                             uint32_t accumulate) {
+// One k-tile (four MMAs of the CTA pair) on one accumulator, as umma_i8_ktile.
+__device__ __forceinline__ void umma_i8_pair_ktile(uint32_t d_tmem, uint64_t a, uint64_t b, uint64_t bstep,
+                                                   uint32_t idesc, uint32_t acc) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate));
+        "{\n\t.reg .pred e, p, q;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "setp.ne.b32 p, %10, 0;\n\t"
+        "setp.eq.b32 q, %10, %10;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::i8 [%0], %1, %2, %9, p;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::i8 [%0], %3, %4, %9, q;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::i8 [%0], %5, %6, %9, q;\n\t"
+        "@e tcgen05.mma.cta_group::2.kind::i8 [%0], %7, %8, %9, q;\n\t}\n" ::"r"(d_tmem),
+        "l"(a), "l"(b), "l"(a + 2), "l"(b + bstep), "l"(a + 4), "l"(b + 2 * bstep), "l"(a + 6), "l"(b + 3 * bstep),
+        "r"(idesc), "r"(acc));
+}
+__device__ __forceinline__ void umma_commit_pair_elect(uint32_t bar, uint16_t mask) {
+    asm volatile(
+        "{\n\t.reg .pred e;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;\n\t}\n" ::"r"(bar),
+        "h"(mask)
+        : "memory");
 }
 __device__ __forceinline__ void stg256(void *p, const uint32_t *v) {
     asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
@@ -391,7 +449,7 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gen_base + kWStages * kWStageBytes + 240);
     float *cbuf = reinterpret_cast<float *>(gen_base + kWStages * kWStageBytes + 256);   // [2][2][256]
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = warp_index(), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
     const int tiles = p.mt * p.nt;
@@ -421,7 +479,7 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
     bool ok = true;
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             auto load_w = [&](int s, int t0, int tn) {
                 const uint32_t fa0 = mapa_shared(full(s), 0);
                 const int c0 = tn * 256 + 128 * (int)rank;
@@ -458,47 +516,45 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
             if (!ok) *abort_flag = 1;
         }
     } else if (warp == 1) {
-        if (lane == 0 && rank == 0) {
+        if (rank == 0) {
             const uint32_t idesc = idesc_i8(256, 256, 0, p.b_mn ? 1u : 0u);
-            const uint32_t bstep = p.b_mn ? 256u : 2u;
+            const uint64_t bstep = p.b_mn ? 256u : 2u;
             const uint64_t dX = sdesc(base, 16, 1024), dW = sdesc(base + 2 * kWSlab, 16, 1024);
             constexpr uint32_t kStageD = kWStageBytes >> 4, kSlabD = kWSlab >> 4;
-            auto mma = [&](int s, int h, uint32_t acc) {
-                const uint64_t a = dX + s * kStageD + h * kSlabD, b = dW + s * kStageD;
-#pragma unroll
-                for (int kk = 0; kk < 4; ++kk)
-                    umma_i8_pair(tmem + h * 256, a + kk * 2, b + kk * bstep, idesc, kk > 0 ? 1u : acc);
+            auto mma = [&](uint32_t s, uint32_t h, uint32_t acc) {
+                umma_i8_pair_ktile(tmem + h * 256, dX + s * kStageD + h * kSlabD, dW + s * kStageD, bstep, idesc, acc);
             };
-            int it = 0, i = 0;
+            static_assert((kWStages & (kWStages - 1)) == 0, "stage and parity from the running k-tile's bits");
+            uint32_t it = 0, i = 0;
             for (int t = pair; t < tiles && ok; t += pairs, ++i) {
-                const int lead = p.nk < kWStages ? p.nk : kWStages;
-                if (i > 0) ok = mbar_wait_cluster(acc_free(0), (i - 1) & 1, abort_flag);
-                for (int k = 0; k < lead && ok; ++k) {
-                    const int s = (it + k) % kWStages;
-                    ok = mbar_wait_cluster(full(s), ((it + k) / kWStages) & 1, abort_flag);
+                const uint32_t nk = p.nk, lead = nk < kWStages ? nk : kWStages;
+                if (i > 0) ok = __all_sync(0xffffffffu, mbar_wait_cluster(acc_free(0), (i - 1) & 1, abort_flag));
+                for (uint32_t k = 0; k < lead && ok; ++k) {
+                    const uint32_t s = (it + k) % kWStages;
+                    ok = __all_sync(0xffffffffu, mbar_wait_cluster(full(s), ((it + k) / kWStages) & 1, abort_flag));
                     if (!ok) break;
                     tc_fence_after();
                     mma(s, 0, k > 0 ? 1u : 0u);
                 }
-                if (ok && i > 0) ok = mbar_wait_cluster(acc_free(1), (i - 1) & 1, abort_flag);
+                if (ok && i > 0) ok = __all_sync(0xffffffffu, mbar_wait_cluster(acc_free(1), (i - 1) & 1, abort_flag));
                 if (!ok) break;
                 tc_fence_after();
-                for (int k = 0; k < lead; ++k) {
-                    const int s = (it + k) % kWStages;
+                for (uint32_t k = 0; k < lead; ++k) {
+                    const uint32_t s = (it + k) % kWStages;
                     mma(s, 1, k > 0 ? 1u : 0u);
-                    umma_commit_pair(empty(s), 0x3);
+                    umma_commit_pair_elect(empty(s), 0x3);
                 }
-                for (int k = lead; k < p.nk; ++k) {
-                    const int s = (it + k) % kWStages;
-                    ok = mbar_wait_cluster(full(s), ((it + k) / kWStages) & 1, abort_flag);
+                for (uint32_t k = lead; k < nk; ++k) {
+                    const uint32_t s = (it + k) % kWStages;
+                    ok = __all_sync(0xffffffffu, mbar_wait_cluster(full(s), ((it + k) / kWStages) & 1, abort_flag));
                     if (!ok) break;
                     tc_fence_after();
                     mma(s, 0, 1u);
                     mma(s, 1, 1u);
-                    umma_commit_pair(empty(s), 0x3);
+                    umma_commit_pair_elect(empty(s), 0x3);
                 }
-                if (ok) umma_commit_pair(acc_full, 0x3);
-                it += p.nk;
+                if (ok) umma_commit_pair_elect(acc_full, 0x3);
+                it += nk;
             }
             if (!ok) *abort_flag = 1;
         }
@@ -586,33 +642,64 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
 
 }  // namespace
 
+// How a product is cut: columns of B a tile, splits of the reduction.  The
+// least of a model of the measured times (4096 x 4096 and 4096 x 11008 weights,
+// 16 to 1024 tokens, within 10%): about 5 us whatever the size, 0.17 us + 1.8 ns
+// a column of the MMA for each k-tile of a CTA (a quarter more where two CTAs
+// share the SM, which N <= 64 lets them), 1.2 us + 0.2 us a split for a
+// cluster's exchange.  Clusters of big CTAs past 6 do not all find a place at
+// once (8 splits of N = 176 took twice the time of 6).
+struct TallPlan {
+    int nt, splits, per;
+};
+static TallPlan plan_tall(const Int8Product &g, int nk) {
+    const int sms = device_sms();
+    const int cap = 256 / g.planes / 16 * 16;
+    const int64_t pt = (g.P + kTP - 1) / kTP, least = (g.Q + cap - 1) / cap;
+    TallPlan best{};
+    double best_us = 0;
+    int last = 0;
+    for (int64_t tq = least; tq <= 16 * least; ++tq) {
+        const int nt = (int)(((g.Q + tq - 1) / tq + 15) / 16 * 16);
+        if (nt == last) continue;
+        last = nt;
+        const int N = nt * g.planes, most = N <= kTTwoN ? kTMaxSplits : 6;
+        const int64_t slots = (N <= kTTwoN ? 2 : 1) * (int64_t)sms, tiles = pt * ((g.Q + nt - 1) / nt);
+        for (int s = 1; s <= most && (s == 1 || 2 * s <= nk); ++s) {
+            const int per = (nk + s - 1) / s;
+            if ((nk + per - 1) / per != s) continue;
+            const int64_t units = tiles * s, waves = (units + slots - 1) / slots;
+            const double tile = (0.17 + 0.0018 * N) * (units > sms && N <= kTTwoN ? 1.25 : 1.0);
+            const double us = 2.0 + (double)waves * (3.0 + per * tile) + (s > 1 ? 1.2 + 0.2 * s : 0.0) + 0.004 * N;
+            if (best.nt == 0 || us < best_us) {
+                best = TallPlan{nt, s, per};
+                best_us = us;
+            }
+        }
+        if (nt == 16) break;
+    }
+    return best;
+}
+
 static int launch_int8_tall(const Int8Product &g, uint32_t *d_status, cudaStream_t st) {
     if (g.P <= 0 || g.Q <= 0) return QLORA_OK;
     TallParams p{};
-    // columns per tile: all of them up to the UMMA's 256, else even tiles
-    const int cap = 256 / g.planes / 16 * 16;
-    const int64_t tiles_q = (g.Q + cap - 1) / cap;
-    p.nt = (int)(((g.Q + tiles_q - 1) / tiles_q + 15) / 16 * 16);
-    const int N = g.planes * p.nt;
     p.P = g.P;
     p.Q = g.Q;
     p.planes = g.planes;
     p.plane_rows = g.plane_rows;
     p.nk = (int)((g.R + kTK - 1) / kTK);
     p.a_mn = g.a_mn;
+    const TallPlan plan = plan_tall(g, p.nk);
+    p.nt = plan.nt;
+    p.per = plan.per;
+    const int N = p.planes * p.nt;
+    const int64_t tiles_q = (g.Q + p.nt - 1) / p.nt, splits = plan.splits;
     p.stage_bytes = kTABytes + N * kTK;
     p.tmem_cols = 32;
     while ((int)p.tmem_cols < N) p.tmem_cols *= 2;
-    const bool two = N <= 64;
-    p.stages = (int)((two ? kTSmemTwo : kTSmemOne) / p.stage_bytes);
+    p.stages = (int)((N <= kTTwoN ? kTSmemTwo : kTSmemOne) / p.stage_bytes);
     if (p.stages > kTMaxStages) p.stages = kTMaxStages;
-    const int64_t tiles = ((g.P + kTP - 1) / kTP) * tiles_q;
-    int64_t splits = (two ? 2 : 1) * device_sms() / tiles;
-    if (splits > p.nk / 2) splits = p.nk / 2;
-    if (splits > kTMaxSplits) splits = kTMaxSplits;
-    if (splits < 1) splits = 1;
-    p.per = (int)((p.nk + splits - 1) / splits);
-    splits = (p.nk + p.per - 1) / p.per;
     p.qscale = g.qscale;
     p.pscale = g.pscale;
     p.mul = g.mul;
@@ -629,14 +716,14 @@ static int launch_int8_tall(const Int8Product &g, uint32_t *d_status, cudaStream
     CUtensorMap tA, tB;
     bool ok = g.a_mn ? make_map(&tA, g.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.P, g.R, g.lda, 128, kTK,
                                 CU_TENSOR_MAP_SWIZZLE_128B)
-                     : make_map(&tA, g.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.R, g.P, g.lda, kTK, 128,
+                     : make_map(&tA, g.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.R, g.P, g.lda, kTK, kTP,
                                 CU_TENSOR_MAP_SWIZZLE_128B);
     ok = ok && make_map(&tB, g.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.R, brows, g.ldb, kTK, (uint32_t)p.nt,
                         CU_TENSOR_MAP_SWIZZLE_128B);
     if (!ok) return QLORA_EUNSUPPORTED;
     const size_t ring = (size_t)p.stages * p.stage_bytes;
     if (ring < (size_t)N * kTP * 4) return QLORA_EUNSUPPORTED;   // the sums take the ring's place
-    const int smem = (int)ring + 1024 + 256;
+    const int smem = (int)ring + 1024 + 256 + 1024;
     if (set_max_smem(reinterpret_cast<const void *>(k_int8_tall), smem) != cudaSuccess) return QLORA_ECUDA;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)((g.P + kTP - 1) / kTP), (unsigned)tiles_q, (unsigned)splits);

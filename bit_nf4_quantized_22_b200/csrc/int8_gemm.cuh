@@ -27,10 +27,9 @@ struct Int8Product {
 
 int launch_int8_product(const Int8Product &g, uint32_t *d_status, cudaStream_t st);
 
-// int8_gemv.cu: M <= 8 tokens whose codes fit in a CTA's share of shared memory
-constexpr int64_t kGemvTokenBytes = 96 * 1024;
-constexpr int64_t kGemvFusedValues = 16384;   // tokens of so few values are quantized by every CTA itself
-bool int8_gemv_takes(int64_t M, int64_t K);
+// int8_gemv.cu: M <= 4 tokens whose codes fit in a CTA's share of shared memory
+constexpr int64_t kGemvTokenBytes = 48 * 1024;
+bool int8_gemv_takes(int64_t M, int64_t N, int64_t K);
 int launch_int8_gemv(const void *X, int x_dtype, int64_t ldx, const int8_rows_t &X8, const int8_rows_t &W,
                      const void *bias, void *Y, int dtype, uint32_t *d_status, cudaStream_t st);
 

@@ -1,12 +1,13 @@
-// int8_gemv.cu -- the product of a few tokens (M <= 8) with a weight of 8-bit
+// int8_gemv.cu -- the product of a few tokens (M <= 4) with a weight of 8-bit
 // rows, bound by the weight's bytes:
 //
 //   y[m][n] = (sum_k cx[m][k] cw[n][k]) * sx[m] * sw[n] + bias[n]
 //
-// A warp takes RW weight rows at a time, its lanes 16 codes each of every 512;
-// the tokens' codes lie in shared memory and four-way integer dot products
-// (exact) do the sums.  Warp w of all takes rows w, w + warps, ...: one wave of
-// CTAs whose rows differ by one at most.  The first weight loads are issued
+// A warp takes a row (short rows: two) at a time, its lanes 16 codes each of
+// every 512; the tokens' codes lie in shared memory and four-way integer dot
+// products (exact) do the sums.  Warp w of all takes rows w, w + warps, ...: one
+// wave of CTAs whose rows differ by one at most.  Four CTAs an SM with eight
+// loads a lane keep up to 128 KB in flight; a warp's first loads are issued
 // before anything that depends on the tokens.
 // FUSED: the CTA also quantizes the tokens itself (each CTA all of them: a few
 // KB from L2), which saves a launch where the tokens are short; CTA 0 writes
@@ -17,7 +18,7 @@ namespace qlora {
 namespace {
 
 constexpr int kGThreads = 256, kGWarps = kGThreads / 32;
-constexpr int kGAhead = 2;                 // 512-value steps of loads in flight per row
+constexpr int kGBatch = 8;                 // 16-byte loads a lane has in flight
 
 struct GemvParams {
     const int8_t *w;
@@ -91,26 +92,31 @@ __device__ __forceinline__ uint4 load_codes(const int8_t *row, int k, int K) {
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+// RW * ST = kGBatch: rows at a time and 512-value steps of each in a batch.
 template <int MT, int RW, bool FUSED>
-__global__ void __launch_bounds__(kGThreads, 2)
+__global__ void __launch_bounds__(kGThreads, 4)
 k_int8_gemv(const GemvParams p) {
+    constexpr int ST = kGBatch / RW;
     extern __shared__ __align__(16) int8_t xs[];     // [MT][kp]
     __shared__ float sx[MT];
     __shared__ uint32_t part[MT * kGWarps];
     const int lane = threadIdx.x & 31;
     const int64_t warps = (int64_t)gridDim.x * kGWarps;
     const int64_t w0 = (int64_t)blockIdx.x * kGWarps + threadIdx.x / 32;
-    uint4 buf[kGAhead][RW];
-    auto load = [&](int64_t n, int step, uint4 (&d)[RW]) {
+    uint4 buf[RW][ST];
+    auto load = [&](int64_t n, int s0) {
 #pragma unroll
         for (int i = 0; i < RW; ++i) {
             const int64_t row = n + i * warps;
-            d[i] = row < p.N && step * 512 < p.K ? load_codes(p.w + row * p.ldw, step * 512 + lane * 16, p.K)
-                                                 : make_uint4(0, 0, 0, 0);
+            const int8_t *at = p.w + row * p.ldw;
+#pragma unroll
+            for (int j = 0; j < ST; ++j) {
+                const int k = (s0 + j) * 512 + lane * 16;
+                buf[i][j] = row < p.N && k < p.K ? load_codes(at, k, p.K) : make_uint4(0, 0, 0, 0);
+            }
         }
     };
-#pragma unroll
-    for (int a = 0; a < kGAhead; ++a) load(w0, a, buf[a]);
+    load(w0, 0);
     if (FUSED) {
         if (p.x_dtype == QLORA_DTYPE_BF16) quantize_tokens<QLORA_DTYPE_BF16, MT>(p, xs, sx, part);
         else if (p.x_dtype == QLORA_DTYPE_FP16) quantize_tokens<QLORA_DTYPE_FP16, MT>(p, xs, sx, part);
@@ -122,7 +128,8 @@ k_int8_gemv(const GemvParams p) {
         for (int m = 0; m < MT; ++m) {
             if (m >= p.M) break;
             for (int k = threadIdx.x * 16; k < p.kp; k += kGThreads * 16)
-                *reinterpret_cast<uint4 *>(xs + (int64_t)m * p.kp + k) = load_codes(p.codes + m * p.ldc, k, p.K);
+                *reinterpret_cast<uint4 *>(xs + (int64_t)m * p.kp + k) =
+                    k < p.K ? load_codes(p.codes + m * p.ldc, k, p.K) : make_uint4(0, 0, 0, 0);
         }
     }
     for (int m = p.M; m < MT; ++m)
@@ -130,33 +137,29 @@ k_int8_gemv(const GemvParams p) {
             *reinterpret_cast<uint4 *>(xs + (int64_t)m * p.kp + k) = make_uint4(0, 0, 0, 0);
     __syncthreads();
     const int steps = p.kp / 512;
+    bool loaded = true;
     for (int64_t n = w0; n < p.N; n += RW * warps) {
         int acc[RW][MT];
 #pragma unroll
         for (int i = 0; i < RW; ++i)
 #pragma unroll
             for (int m = 0; m < MT; ++m) acc[i][m] = 0;
-        for (int s0 = 0; s0 < steps; s0 += kGAhead) {
+        for (int s0 = 0; s0 < steps; s0 += ST) {
+            if (!loaded) load(n, s0);
+            loaded = false;
 #pragma unroll
-            for (int a = 0; a < kGAhead; ++a) {
-                const int s = s0 + a;
-                uint4 c[RW];
+            for (int j = 0; j < ST; ++j) {
+                if (s0 + j >= steps) break;
 #pragma unroll
-                for (int i = 0; i < RW; ++i) c[i] = buf[a][i];
-                // the loads kGAhead steps on: of these rows, or of the warp's next ones
-                if (s + kGAhead < steps) load(n, s + kGAhead, buf[a]);
-                else load(n + RW * warps, a, buf[a]);
-                if (s < steps) {
+                for (int m = 0; m < MT; ++m) {
+                    const uint4 x =
+                        *reinterpret_cast<const uint4 *>(xs + (int64_t)m * p.kp + (s0 + j) * 512 + lane * 16);
 #pragma unroll
-                    for (int m = 0; m < MT; ++m) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(xs + (int64_t)m * p.kp + s * 512 + lane * 16);
-#pragma unroll
-                        for (int i = 0; i < RW; ++i) {
-                            acc[i][m] = __dp4a((int)c[i].x, (int)x.x, acc[i][m]);
-                            acc[i][m] = __dp4a((int)c[i].y, (int)x.y, acc[i][m]);
-                            acc[i][m] = __dp4a((int)c[i].z, (int)x.z, acc[i][m]);
-                            acc[i][m] = __dp4a((int)c[i].w, (int)x.w, acc[i][m]);
-                        }
+                    for (int i = 0; i < RW; ++i) {
+                        acc[i][m] = __dp4a((int)buf[i][j].x, (int)x.x, acc[i][m]);
+                        acc[i][m] = __dp4a((int)buf[i][j].y, (int)x.y, acc[i][m]);
+                        acc[i][m] = __dp4a((int)buf[i][j].z, (int)x.z, acc[i][m]);
+                        acc[i][m] = __dp4a((int)buf[i][j].w, (int)x.w, acc[i][m]);
                     }
                 }
             }
@@ -186,7 +189,7 @@ int launch_gemv(const GemvParams &p, bool fused, cudaStream_t st) {
     const int smem = MT * p.kp;
     void (*k)(GemvParams) = fused ? k_int8_gemv<MT, RW, true> : k_int8_gemv<MT, RW, false>;
     if (set_max_smem(reinterpret_cast<const void *>(k), smem) != cudaSuccess) return QLORA_ECUDA;
-    const int64_t want = (p.N + kGWarps * RW - 1) / (kGWarps * RW), most = 2 * device_sms();
+    const int64_t want = (p.N + kGWarps * RW - 1) / (kGWarps * RW), most = 4 * device_sms();
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(want < most ? want : most));
     cfg.blockDim = dim3(kGThreads);
@@ -204,21 +207,25 @@ int launch_gemv(const GemvParams &p, bool fused, cudaStream_t st) {
 
 template <int MT>
 int pick_rows(const GemvParams &p, bool fused, cudaStream_t st) {
-    // as many rows a warp as still leave every warp of the wave some
-    const int64_t warps = 2 * device_sms() * kGWarps;
-    if (p.N > 2 * warps) return launch_gemv<MT, 4>(p, fused, st);
-    if (p.N > warps) return launch_gemv<MT, 2>(p, fused, st);
+    if (p.kp <= 2048) return launch_gemv<MT, 2>(p, fused, st);   // a batch of 4 steps holds a row: two rows at a time
     return launch_gemv<MT, 1>(p, fused, st);
 }
 
 }  // namespace
 
-bool int8_gemv_takes(int64_t M, int64_t K) { return M <= 8 && M * ((K + 511) / 512 * 512) <= kGemvTokenBytes; }
+// Against the tall kernel at 16 tokens (one MMA width serves them all): one and
+// two tokens are faster here at every size (4096 x 4096: 6.4 and 7.4 us, there
+// 8.5; 8192 x 28672: 40.8 us, there 42.7), three and four on small weights alone
+// (1024 x 1024: 5.4, there 7.2; 4096 x 11008: 15.6, there 12.5).
+bool int8_gemv_takes(int64_t M, int64_t N, int64_t K) {
+    return M * ((K + 511) / 512 * 512) <= kGemvTokenBytes && (M <= 2 || (M <= 4 && N * K <= (int64_t)8 << 20));
+}
 
 int launch_int8_gemv(const void *X, int x_dtype, int64_t ldx, const int8_rows_t &X8, const int8_rows_t &W,
                      const void *bias, void *Y, int dtype, uint32_t *d_status, cudaStream_t st) {
     const int M = (int)X8.rows;
-    const bool fused = X && M * W.cols <= kGemvFusedValues;
+    // quantizing in every CTA costs about 0.5 us for 2048 values, a launch of its own 1 us (and the host's 2)
+    const bool fused = X && M * W.cols <= 4096;
     if (X && !fused) {
         const int rc = launch_int8_quantize(X, x_dtype, ldx, X8, d_status, st);
         if (rc) return rc;
@@ -235,8 +242,7 @@ int launch_int8_gemv(const void *X, int x_dtype, int64_t ldx, const int8_rows_t 
     p.status = d_status;
     if (M == 1) return pick_rows<1>(p, fused, st);
     if (M == 2) return pick_rows<2>(p, fused, st);
-    if (M <= 4) return pick_rows<4>(p, fused, st);
-    return pick_rows<8>(p, fused, st);
+    return pick_rows<4>(p, fused, st);
 }
 
 }  // namespace qlora
