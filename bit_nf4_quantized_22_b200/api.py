@@ -40,6 +40,14 @@ def _raw_stream(t: torch.Tensor) -> int:
     return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
+def _cb_at(codebook: torch.Tensor | None):
+    """The 16 host floats a call reads: the tensor's own where it has them in that form."""
+    if codebook is not None and codebook.dtype == torch.float32 and codebook.shape == (16,) \
+            and not codebook.is_cuda and codebook.is_contiguous():
+        return codebook.data_ptr()
+    return _cb_host(codebook)
+
+
 def _cb_host(codebook: torch.Tensor | None) -> ctypes.Array:
     cb = nf4_codebook() if codebook is None else codebook.detach().to("cpu", torch.float32)
     arr = (ctypes.c_float * 16)(*cb.tolist())
@@ -284,30 +292,33 @@ def backward(x: torch.Tensor | Int8Rows | None, dy: torch.Tensor, q: NF4Weight, 
 
 def _backward_int8(x: Int8Rows, dy, q: NF4Weight, A, B, alpha, pool_group, T, need_dx, need_dA, need_dB,
                    codebook, workspace, status):
-    _need(dy, q.compute_dtype, "dy", 2)
-    _need(A, q.compute_dtype, "A", 2)
-    _need(B, q.compute_dtype, "B", 2)
-    M, r = dy.shape[0], A.shape[1]
-    dev = dy.device
-    if tuple(dy.shape) != (x.rows, q.rows) or x.cols != q.cols:
-        raise ValueError(f"dy [{x.rows}, {q.rows}] and x [{M}, {q.cols}] are needed")
-    if pool_group not in (1, 64) or tuple(A.shape) != (q.cols // pool_group, r) or tuple(B.shape) != (r, q.rows):
+    dt = q.compute_dtype
+    _need(dy, dt, "dy", 2)
+    _need(A, dt, "A", 2)
+    _need(B, dt, "B", 2)
+    xc, qc = x.c_struct(), q.c_struct()
+    M, K, N = xc.rows, qc.cols, qc.rows
+    Da, r = A.shape
+    if tuple(dy.shape) != (M, N) or xc.cols != K:
+        raise ValueError(f"dy [{M}, {N}] and x [{M}, {K}] are needed")
+    if pool_group not in (1, 64) or Da != K // pool_group or tuple(B.shape) != (r, N):
         raise ValueError("A [Din/pool_group, r] and B [r, Dout] are needed")
     if T is not None:
         _need(T, torch.float32, "T", 2)
         if tuple(T.shape) != (M, r):
             raise ValueError(f"T [{M}, {r}] is needed")
+    dev, lib = dy.device, load()
     with _on(dy, x.codes, A, B, T, workspace, status, q.packed):
         new = torch.empty if M else torch.zeros      # no token: the adapter gradients are zero
-        dX = torch.empty(M, q.cols, dtype=q.compute_dtype, device=dev) if need_dx else None
-        dA = new(A.shape[0], r, dtype=torch.float32, device=dev) if need_dA else None
-        dB = new(r, q.rows, dtype=torch.float32, device=dev) if need_dB else None
-        qc, xc = q.c_struct(), x.c_struct()
-        need = int(load().qlora_backward_int8_workspace_size(M, ctypes.byref(qc), r, pool_group))
+        dX = torch.empty((M, K), dtype=dt, device=dev) if need_dx else None
+        dA = new((Da, r), dtype=torch.float32, device=dev) if need_dA else None
+        dB = new((r, N), dtype=torch.float32, device=dev) if need_dB else None
+        need = lib.qlora_backward_int8_workspace_size(M, ctypes.byref(qc), r, pool_group)
         ws, nbytes = _workspace(need, dev, workspace)
-        rc = load().qlora_backward_int8(ctypes.byref(xc), _ptr(dy), M, ctypes.byref(qc), _cb_host(codebook),
-                                        _ptr(A), _ptr(B), r, float(alpha), pool_group, _ptr(T), _ptr(dX),
-                                        _ptr(dA), _ptr(dB), _ptr(ws), nbytes, _ptr(status), _raw_stream(dy))
+        cb = _cb_at(codebook)
+        rc = lib.qlora_backward_int8(ctypes.byref(xc), dy.data_ptr(), M, ctypes.byref(qc), cb,
+                                     A.data_ptr(), B.data_ptr(), r, alpha, pool_group, _at(T), _at(dX),
+                                     _at(dA), _at(dB), _at(ws), nbytes, _at(status), _raw_stream(dy))
         _lib.check(rc, "qlora_backward_int8")
     return dX, dA, dB
 

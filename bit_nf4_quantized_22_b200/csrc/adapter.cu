@@ -72,6 +72,7 @@ __global__ void k_split_f32(const float *__restrict__ src, int64_t rows, int r, 
 //   out_f32[p*fsp + q*fsq]  = f32_scale * v
 //   out_bf16[p*bsp + q]     = RN_bf16(bf_scale * v)          (row stride bsp)
 //   out_split[p*2*sp + q], [p*2*sp + sp + q] = hi/lo of v    (row stride 2 sp)
+// Columns from Qv up to bsp (out_bf16) and up to sp (out_split's halves) become zero.
 struct ReduceArgs {
     const float *partial;
     int splits;
@@ -82,14 +83,21 @@ struct ReduceArgs {
     float bf_scale; uint16_t *out_bf16; int64_t bsp;
     uint16_t *out_split; int64_t sp;
     bool f16;             // 16-bit outputs in fp16 (else bf16)
+    int Qz;               // columns written: Qv and the padding of the 16-bit outputs
 };
+
+__device__ __forceinline__ void reduce_pad(const ReduceArgs &a, int64_t p, int q) {
+    if (a.out_bf16 && q < a.bsp) a.out_bf16[p * a.bsp + q] = 0;
+    if (a.out_split && q < a.sp) a.out_split[p * 2 * a.sp + q] = a.out_split[p * 2 * a.sp + a.sp + q] = 0;
+}
 
 // General layout (any Qp): one thread per output element.
 __global__ void k_reduce_scalar(ReduceArgs a) {
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= a.P * a.Qv) return;
-    const int64_t p = i / a.Qv;
-    const int q = (int)(i % a.Qv);
+    if (i >= a.P * a.Qz) return;
+    const int64_t p = i / a.Qz;
+    const int q = (int)(i % a.Qz);
+    if (q >= a.Qv) return reduce_pad(a, p, q);
     float v = 0.f;
     for (int z = 0; z < a.splits; ++z) {
         const float *base = a.partial + ((int64_t)z * a.P + p) * a.Qp;
@@ -111,7 +119,12 @@ __global__ void k_reduce_scalar(ReduceArgs a) {
 __global__ void __launch_bounds__(256) k_reduce(ReduceArgs a) {
     const int64_t p = (int64_t)blockIdx.y * 8 + threadIdx.y;
     const int q0 = 4 * (blockIdx.x * 32 + threadIdx.x);
-    if (p >= a.P || q0 >= a.Qv) return;
+    if (p >= a.P || q0 >= a.Qz) return;
+    if (q0 >= a.Qv) {
+        for (int e = 0; e < 4; ++e)
+            if (q0 + e < a.Qz) reduce_pad(a, p, q0 + e);
+        return;
+    }
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
     const float *base = a.partial + p * a.Qp + q0;
     const int64_t zs = a.P * a.Qp;
@@ -128,7 +141,10 @@ __global__ void __launch_bounds__(256) k_reduce(ReduceArgs a) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         const int q = q0 + e;
-        if (q >= a.Qv) break;
+        if (q >= a.Qv) {
+            if (q < a.Qz) reduce_pad(a, p, q);
+            continue;
+        }
         if (a.out_f32) a.out_f32[p * a.fsp + q * a.fsq] = a.f32_scale * vv[e];
         if (a.out_bf16) a.out_bf16[p * a.bsp + q] = enc16(a.bf_scale * vv[e], a.f16);
         if (a.out_split) {
@@ -175,12 +191,14 @@ int launch_reduce(const float *partial, int splits, int64_t P, int64_t Qp, int H
                   uint16_t *out_bf16, int64_t bsp, uint16_t *out_split, int64_t sp,
                   cudaStream_t st, bool f16) {
     ReduceArgs a{partial, splits, P, Qp, H, Qv, f32_scale, out_f32, fsp, fsq,
-                 bf_scale, out_bf16, bsp, out_split, sp, f16};
+                 bf_scale, out_bf16, bsp, out_split, sp, f16, Qv};
     if (P * Qv == 0) return QLORA_OK;
+    if (out_bf16 && bsp > a.Qz) a.Qz = (int)bsp;
+    if (out_split && sp > a.Qz) a.Qz = (int)sp;
     if (Qp % 4 != 0 || H % 4 != 0 || (reinterpret_cast<uintptr_t>(partial) & 15u) != 0) {
-        k_reduce_scalar<<<blocks_for(P * Qv), 256, 0, st>>>(a);
+        k_reduce_scalar<<<blocks_for(P * a.Qz), 256, 0, st>>>(a);
     } else {
-        dim3 grid((unsigned)((Qv + 127) / 128), (unsigned)((P + 7) / 8));
+        dim3 grid((unsigned)((a.Qz + 127) / 128), (unsigned)((P + 7) / 8));
         k_reduce<<<grid, dim3(32, 8), 0, st>>>(a);
     }
     QLORA_LAUNCH_CHECK();

@@ -348,8 +348,6 @@ int run_adapter_down(const Dims &d, const uint16_t *X, const uint16_t *A, uint16
     }
     ProdPlan plan;
     RC(run_prod(prod_T(d, X, Ause, ph, pl), Tpart, status, st, &plan, d.f16));
-    if (sT && cudaMemsetAsync(sT, 0, d.M * d.rp64 * sizeof(uint16_t), st) != cudaSuccess)
-        return QLORA_ECUDA;
     return launch_reduce(Tpart, plan.splits, d.M, plan.Qp, 0, d.r, 1.f, T32, d.r, 1, s, sT, d.rp64,
                          nullptr, 0, st, d.f16);
 }
@@ -581,9 +579,6 @@ static int backward_impl(const uint16_t *X, const int8_rows_t *X8, const uint16_
         ProdPlan pl;
         RC(run_prod(prod_G(d, dY, B), w.Gpart, d_status, st, &pl, d.f16));
         uint16_t *sG = (want_dx && !d.small) ? w.sG : nullptr;
-        if (sG && cudaMemsetAsync(sG, 0, M * d.rp64 * 2, st) != cudaSuccess) return QLORA_ECUDA;
-        if (w.Gsplit && cudaMemsetAsync(w.Gsplit, 0, M * 2 * d.rp * 2, st) != cudaSuccess)
-            return QLORA_ECUDA;
         RC(launch_reduce(w.Gpart, pl.splits, M, pl.Qp, 0, r, 1.f, w.G32, r, 1, s, sG, d.rp64,
                          w.Gsplit, d.rp, st, d.f16));
     }
