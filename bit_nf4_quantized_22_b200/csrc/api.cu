@@ -739,7 +739,8 @@ int int8_matmul_backward(const uint16_t *dY, int32_t dtype, int64_t M, const int
     GradWs ws;
     layout_grad8(M, *W, workspace, &ws);
     cudaStream_t st = (cudaStream_t)stream;
-    RC(launch_int8_row_digits(dY, dtype == QLORA_DTYPE_FP16, M, W->rows, W->scales, ws.planes, ws.ld, ws.steps, st));
+    RC(launch_int8_row_digits(dY, dtype == QLORA_DTYPE_FP16, M, W->rows, W->scales, ws.planes, ws.ld, ws.steps,
+                              st));
     Int8Product g{};
     g.a = W->codes, g.lda = W->ld, g.a_mn = 1;
     g.b = ws.planes, g.ldb = ws.ld, g.plane_rows = M, g.planes = 2;

@@ -48,7 +48,7 @@ __device__ __forceinline__ void quantize_tokens(const GemvParams &p, int8_t *xs,
         am[m] = 0;
         const char *row = static_cast<const char *>(p.x) + m * p.ldx * esize;
         if (m < p.M)
-            for (int v = threadIdx.x; v < nv; v += kGThreads) am[m] = absmax8<DT>(load8<DT>(row, v, p.K), am[m]);
+            for (int v = threadIdx.x; v < nv; v += kGThreads) am[m] = absmax8<DT>(load8<DT, false>(row, v, p.K), am[m]);
         am[m] = __reduce_max_sync(0xffffffffu, absmax_bits<DT>(am[m]));
         if ((threadIdx.x & 31) == 0) part[m * kGWarps + threadIdx.x / 32] = am[m];
     }
@@ -59,26 +59,25 @@ __device__ __forceinline__ void quantize_tokens(const GemvParams &p, int8_t *xs,
         uint32_t b = 0;
 #pragma unroll
         for (int i = 0; i < kGWarps; ++i) b = part[m * kGWarps + i] > b ? part[m * kGWarps + i] : b;
-        const bool fin = b < 0x7f800000u;
-        const float a = __uint_as_float(b);
-        const float s = fin ? __fdiv_rn(a, 127.f) : __uint_as_float(0x7fffffffu);
+        const RowCode rc = row_code<DT>(b);
         if (threadIdx.x == 0) {
-            sx[m] = s;
+            sx[m] = rc.s;
             if (blockIdx.x == 0) {
-                p.xscale[m] = s;
-                if (!fin && p.status) atomicOr(p.status, QLORA_STATUS_NONFINITE);
+                p.xscale[m] = rc.s;
+                if (!rc.mask && p.status) atomicOr(p.status, QLORA_STATUS_NONFINITE);
             }
         }
-        const bool zero = !fin || s == 0.f;
-        float inv = 0.f;
-        const Decide how = zero ? kExact : decide<DT>(a, s, inv);
         const char *row = static_cast<const char *>(p.x) + m * p.ldx * esize;
+        int8_t *dst = xs + (int64_t)m * p.kp, *out = p.codes + m * p.ldc;
+        float far = 0.f;
         for (int v = threadIdx.x; v < p.kp / kVec; v += kGThreads) {
             uint2 c = make_uint2(0u, 0u);
-            if (v < nv && !zero) c = encode8<DT>(load8<DT>(row, v, p.K), s, inv, how);
-            *reinterpret_cast<uint2 *>(xs + (int64_t)m * p.kp + v * kVec) = c;
-            if (blockIdx.x == 0 && v < nv) store8(p.codes + m * p.ldc, v * kVec, p.K, c.x, c.y);
+            if (v < nv) c = encode8<DT>(load8<DT, false>(row, v, p.K), rc, far);
+            *reinterpret_cast<uint2 *>(dst + v * kVec) = c;
+            if (blockIdx.x == 0 && v < nv) store8<false>(out, v * kVec, p.K, c.x, c.y);
         }
+        if (rc.exact || far > kFar)
+            encode_exact<DT>(row, threadIdx.x, kGThreads, p.K, rc.s, dst, blockIdx.x == 0 ? out : nullptr);
     }
 }
 

@@ -20,145 +20,164 @@
 namespace qlora {
 namespace {
 
-constexpr int kMaxRowThreads = 1024;
-constexpr int kDigitThreads = 512;
+// Most threads of a row's CTA: what the steps' registers leave room for.
+constexpr int row_threads(int steps) { return steps >= 8 ? 512 : 1024; }
 
-// One CTA per row; see launch_int8_quantize for its threads.  HBM-bound: the
-// CTAs of an SM have to keep some 50 KB of loads in flight between them, so
-// the variant for short rows holds its registers down for more CTAs.
-template <int DT, int MOST>
-__global__ void __launch_bounds__(MOST, MOST == kMaxRowThreads ? 1 : 1280 / MOST)
-k_int8_quantize(const void *X, int64_t ldx, int cols, int8_t *codes, int64_t ld, float *scales,
+// A CTA (WARP: a warp, eight rows a CTA) per row, STEPS x 8 values a thread in
+// registers between the maximum and the codes (what a longer row has past them
+// is read again).  HBM-bound: many rows want few threads with many loads each
+// (28672 x 8192 bf16: 8 steps 102 us, 6.9 TB/s; 4 steps 116, 1 step 204; rows
+// brought through shared memory by bulk copies into persistent CTAs 119), short
+// rows a warp each without a barrier (28672 x 1024: 15 us, a CTA 31).
+template <int DT, bool FULL, int STEPS, bool WARP>
+__global__ void __launch_bounds__(WARP ? 256 : row_threads(STEPS))
+k_int8_quantize(const void *X, int64_t ldx, int64_t rows, int cols, int8_t *codes, int64_t ld, float *scales,
                 uint32_t *status) {
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     constexpr int esize = DT == QLORA_DTYPE_FP32 ? 4 : 2;
-    constexpr int kSteps = kKeep<DT>;
     const int nv = (cols + kVec - 1) / kVec;
-    const int64_t m = blockIdx.x;
+    const int64_t m = WARP ? (int64_t)blockIdx.x * 8 + threadIdx.x / 32 : blockIdx.x;
+    if (WARP && m >= rows) return;
+    const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, threads = WARP ? 32 : blockDim.x;
     const char *row = static_cast<const char *>(X) + m * ldx * esize;
-    Raw8<DT> keep[kSteps];
+    Raw8<DT> keep[STEPS];
     uint32_t am = 0;
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-        const int v = i * blockDim.x + threadIdx.x;
-        if (v < nv) keep[i] = load8<DT>(row, v, cols);
-    }
+    for (int i = 0; i < STEPS; ++i)
+        if (i * threads + tid < nv) keep[i] = load8<DT, FULL>(row, i * threads + tid, cols);
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i)
-        if (i * (int)blockDim.x + (int)threadIdx.x < nv) am = absmax8<DT>(keep[i], am);
-    for (int v = kSteps * blockDim.x + threadIdx.x; v < nv; v += blockDim.x)
-        am = absmax8<DT>(load8<DT>(row, v, cols), am);
-    am = block_max(absmax_bits<DT>(am));
-    const bool fin = am < 0x7f800000u;
-    const float a = __uint_as_float(am);
-    const float s = fin ? __fdiv_rn(a, 127.f) : __uint_as_float(0x7fffffffu);
-    if (threadIdx.x == 0) {
-        scales[m] = s;
-        if (!fin && status) atomicOr(status, QLORA_STATUS_NONFINITE);
+    for (int i = 0; i < STEPS; ++i)
+        if (i * threads + tid < nv) am = absmax8<DT>(keep[i], am);
+    for (int v = STEPS * threads + tid; v < nv; v += threads) am = absmax8<DT>(load8<DT, FULL>(row, v, cols), am);
+    am = absmax_bits<DT>(am);
+    am = WARP ? __reduce_max_sync(0xffffffffu, am) : block_max(am);
+    const RowCode rc = row_code<DT>(am);
+    if (tid == 0) {
+        scales[m] = rc.s;
+        if (!rc.mask && status) atomicOr(status, QLORA_STATUS_NONFINITE);
     }
     int8_t *dst = codes + m * ld;
-    const bool zero = !fin || s == 0.f;
-    float inv = 0.f;
-    const Decide how = zero ? kExact : decide<DT>(a, s, inv);
+    float far = 0.f;
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
-        const int v = i * blockDim.x + threadIdx.x;
+    for (int i = 0; i < STEPS; ++i) {
+        const int v = i * threads + tid;
         if (v < nv) {
-            const uint2 c = zero ? make_uint2(0u, 0u) : encode8<DT>(keep[i], s, inv, how);
-            store8(dst, v * kVec, cols, c.x, c.y);
+            const uint2 c = encode8<DT>(keep[i], rc, far);
+            store8<FULL>(dst, v * kVec, cols, c.x, c.y);
         }
     }
-    for (int v = kSteps * blockDim.x + threadIdx.x; v < nv; v += blockDim.x) {
-        const uint2 c = zero ? make_uint2(0u, 0u) : encode8<DT>(load8<DT>(row, v, cols), s, inv, how);
-        store8(dst, v * kVec, cols, c.x, c.y);
+    for (int v = STEPS * threads + tid; v < nv; v += threads) {
+        const uint2 c = encode8<DT>(load8<DT, FULL>(row, v, cols), rc, far);
+        store8<FULL>(dst, v * kVec, cols, c.x, c.y);
     }
+    if (rc.exact || far > kFar) encode_exact<DT>(row, tid, threads, cols, rc.s, dst, nullptr);
 }
 
 // Rows of D = dY * scale[column] (RN32) in 16-bit fixed point, q = RN(D / step),
 // step = a / 32639, as two digit planes.  A rounding is off by half a step,
 // a / 65278, so a row by at most sqrt(cols) / 65278 of its norm whatever its
 // values (about 4e-5 for normal ones): below the 16-bit output's own rounding.
-template <int DT, int MOST>
-__global__ void __launch_bounds__(MOST, MOST == kDigitThreads ? 2 : 1152 / MOST)
+//
+// d[e] = y[e] * scale[e] of one vector; the scales come from L1.
+template <int DT, bool FULL>
+__device__ __forceinline__ void digit_products(const Raw8<DT> &r, const float *__restrict__ cscale, int v, int cols,
+                                               float (&d)[kVec]) {
+    float f[kVec];
+    if (FULL) {
+        const float4 x = __ldg(reinterpret_cast<const float4 *>(cscale + v * kVec));
+        const float4 y = __ldg(reinterpret_cast<const float4 *>(cscale + v * kVec) + 1);
+        f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w, f[4] = y.x, f[5] = y.y, f[6] = y.z, f[7] = y.w;
+    } else {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) f[e] = __ldg(cscale + (v * kVec + e < cols ? v * kVec + e : cols - 1));
+    }
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) d[e] = __fmul_rn(val8(r, e), f[e]);
+}
+// Running maximum of magnitudes that keeps a NaN (the sign of m is of no account).
+__device__ __forceinline__ float digit_max(const float (&d)[kVec], float m) {
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) asm("max.NaN.xorsign.abs.f32 %0, %0, %1;\n" : "+f"(m) : "f"(d[e]));
+    return m;
+}
+struct RowDigits {
+    float step, up, inv;
+    bool fin;
+};
+__device__ __forceinline__ RowDigits row_digits(uint32_t am) {
+    RowDigits r;
+    r.fin = am < 0x7f800000u;
+    // magnitudes below 2^-60 are raised by 2^64 first, so that 1/step stays finite
+    r.up = am < 0x21800000u ? 0x1p64f : 1.f;
+    const float a = __uint_as_float(am) * r.up;
+    r.inv = r.fin && a > 0.f ? __fdiv_rn(32639.f, a) : 0.f;
+    r.step = r.fin ? __fdiv_rn(a, 32639.f) / r.up : __uint_as_float(0x7fffffffu);
+    return r;
+}
+// |d up inv| <= 32639 (1 + 2^-23), so the magic addition rounds it to an integer
+// q in +-32639.  With 32768 + 128 in the magic number, the sum's 16 low bits are
+// 256 (d1 + 128) + (d0 + 128): both digits with their top bit flipped, each in
+// a byte of its own.
+template <bool FULL>
+__device__ __forceinline__ void put_digits(float (&d)[kVec], const RowDigits &r, int8_t *hi, int8_t *lo, int e0,
+                                           int cols) {
+    uint32_t q[kVec / 2];
+    if (r.up != 1.f) {
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) d[e] = __fmul_rn(d[e], r.up);
+    }
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) d[e] = __fmaf_rn(d[e], r.inv, kMagic + 32896.f);
+    const uint32_t keep = r.fin ? 0xffffffffu : 0u;
+#pragma unroll
+    for (int i = 0; i < kVec / 2; ++i)
+        q[i] = (__byte_perm(__float_as_uint(d[2 * i]), __float_as_uint(d[2 * i + 1]), 0x5410) ^ 0x80808080u) & keep;
+    store8<FULL>(hi, e0, cols, __byte_perm(q[0], q[1], 0x7531), __byte_perm(q[2], q[3], 0x7531));
+    store8<FULL>(lo, e0, cols, __byte_perm(q[0], q[1], 0x6420), __byte_perm(q[2], q[3], 0x6420));
+}
+
+template <int DT, bool FULL, int STEPS>
+__global__ void __launch_bounds__(row_threads(STEPS))
 k_int8_row_digits(const void *Y, int64_t rows, int cols, const float *__restrict__ cscale,
-                  int8_t *planes, int64_t ld, float *steps, bool vscale) {
+                  int8_t *planes, int64_t ld, float *steps) {
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-    constexpr int kSteps = 4;
     const int nv = (cols + kVec - 1) / kVec;
     const int64_t m = blockIdx.x;
-    const char *row = static_cast<const char *>(Y) + m * cols * 2;
-    // the scales come from L1 both times; the raw values alone stay in registers
-    auto products = [&](const Raw8<DT> &r, int v, float (&d)[kVec]) {
-        float f[kVec];
-        if (vscale && v * kVec + kVec <= cols) {
-            const float4 x = __ldg(reinterpret_cast<const float4 *>(cscale + v * kVec));
-            const float4 y = __ldg(reinterpret_cast<const float4 *>(cscale + v * kVec) + 1);
-            f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w, f[4] = y.x, f[5] = y.y, f[6] = y.z, f[7] = y.w;
-        } else {
+    const char *row = static_cast<const char *>(Y) + m * (int64_t)cols * 2;
+    Raw8<DT> keep[STEPS];
+    float top = 0.f, d[kVec];
 #pragma unroll
-            for (int e = 0; e < kVec; ++e) f[e] = v * kVec + e < cols ? __ldg(cscale + v * kVec + e) : 0.f;
-        }
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) d[e] = __fmul_rn(val8(r, e), f[e]);
-    };
-    // NaN-keeping maximum of magnitudes, as integers
-    auto join = [&](const Raw8<DT> &r, int v, uint32_t m) {
-        float d[kVec];
-        products(r, v, d);
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-            const uint32_t b = __float_as_uint(d[e]) & 0x7fffffffu;
-            m = b > m ? b : m;
-        }
-        return m;
-    };
-    Raw8<DT> keep[kSteps];
-    uint32_t am = 0;
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
+    for (int i = 0; i < STEPS; ++i) {
         const int v = i * blockDim.x + threadIdx.x;
-        if (v < nv) keep[i] = load8<DT>(row, v, cols);
+        if (v < nv) keep[i] = load8<DT, FULL>(row, v, cols);
     }
 #pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
+    for (int i = 0; i < STEPS; ++i) {
         const int v = i * blockDim.x + threadIdx.x;
-        if (v < nv) am = join(keep[i], v, am);
+        if (v < nv) {
+            digit_products<DT, FULL>(keep[i], cscale, v, cols, d);
+            top = digit_max(d, top);
+        }
     }
-    for (int v = kSteps * blockDim.x + threadIdx.x; v < nv; v += blockDim.x)
-        am = join(load8<DT>(row, v, cols), v, am);
-    am = block_max(am);
-    const bool fin = am < 0x7f800000u;
-    // magnitudes below 2^-60 are raised by 2^64 first, so that 1/step stays finite
-    const float up = am < 0x21800000u ? 0x1p64f : 1.f;
-    const float a = __uint_as_float(am) * up;
-    const float inv = fin && a > 0.f ? __fdiv_rn(32639.f, a) : 0.f;
-    if (threadIdx.x == 0) steps[m] = fin ? __fdiv_rn(a, 32639.f) / up : __uint_as_float(0x7fffffffu);
+    for (int v = STEPS * blockDim.x + threadIdx.x; v < nv; v += blockDim.x) {
+        digit_products<DT, FULL>(load8<DT, FULL>(row, v, cols), cscale, v, cols, d);
+        top = digit_max(d, top);
+    }
+    const RowDigits r = row_digits(block_max(__float_as_uint(top) & 0x7fffffffu));
+    if (threadIdx.x == 0) steps[m] = r.step;
     int8_t *hi = planes + m * ld, *lo = planes + (rows + m) * ld;
-    // |d * up * inv| <= 32639 (1 + 2^-23), so the magic addition rounds it to an
-    // integer q in +-32639, whose 16 low bits are those of the sum's pattern;
-    // the upper digit is the byte of q + 128 above its lower one.
-    auto put = [&](const Raw8<DT> &r, int v) {
-        float d[kVec];
-        products(r, v, d);
-        uint32_t q[kVec], h[kVec];
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-            q[e] = fin ? __float_as_uint(__fmaf_rn(__fmul_rn(d[e], up), inv, kMagic)) : 0u;
-            h[e] = q[e] + 128u;
-        }
-        auto second = [&](int e) {
-            return __byte_perm(__byte_perm(h[e], h[e + 1], 0x0051), __byte_perm(h[e + 2], h[e + 3], 0x0051), 0x5410);
-        };
-        store8(hi, v * kVec, cols, second(0), second(4));
-        store8(lo, v * kVec, cols, bytes4(q[0], q[1], q[2], q[3]), bytes4(q[4], q[5], q[6], q[7]));
-    };
-#pragma unroll
-    for (int i = 0; i < kSteps; ++i) {
+    for (int i = 0; i < STEPS; ++i) {
         const int v = i * blockDim.x + threadIdx.x;
-        if (v < nv) put(keep[i], v);
+        if (v < nv) {
+            digit_products<DT, FULL>(keep[i], cscale, v, cols, d);
+            put_digits<FULL>(d, r, hi, lo, v * kVec, cols);
+        }
     }
-    for (int v = kSteps * blockDim.x + threadIdx.x; v < nv; v += blockDim.x)
-        put(load8<DT>(row, v, cols), v);
+    for (int v = STEPS * blockDim.x + threadIdx.x; v < nv; v += blockDim.x) {
+        digit_products<DT, FULL>(load8<DT, FULL>(row, v, cols), cscale, v, cols, d);
+        put_digits<FULL>(d, r, hi, lo, v * kVec, cols);
+    }
 }
 
 // Columns of S[t][j] (rows t < R, columns j < r; 16-bit or fp32), optionally
@@ -333,46 +352,72 @@ __global__ void k_int8_dequantize(const int8_t *__restrict__ codes, int64_t ld, 
     }
 }
 
-// Threads of a row's CTA, `steps` of 8 values each in registers; what a row
-// has past most * steps * 8 values is read a second time.
-int row_threads(int64_t cols, int steps, int most) {
-    const int64_t nv = (cols + kVec - 1) / kVec;
-    const int64_t t = ((nv + steps - 1) / steps + 31) / 32 * 32;
-    return (int)(t > most ? most : t);
+// Steps of a row's CTA: one while every warp of every row has a place on the
+// GPU at once, two up to six times that, eight past it (fp32, whose codes cost
+// more instructions: two).
+int row_steps(int64_t rows, int64_t cols, bool f32) {
+    const int64_t nv = (cols + kVec - 1) / kVec, warps = rows * ((nv + 31) / 32), places = 32 * (int64_t)device_sms();
+    if (nv <= row_threads(1) && warps <= places) return 1;
+    if (f32 || (nv <= 2 * row_threads(2) && warps <= 6 * places)) return 2;
+    return 8;
+}
+int row_cta(int64_t cols, int steps) {
+    const int64_t nv = (cols + kVec - 1) / kVec, t = ((nv + steps - 1) / steps + 31) / 32 * 32;
+    return (int)(t > row_threads(steps) ? row_threads(steps) : t);
 }
 
-template <int DT>
-auto pick_quantize(int threads) {
-    return threads <= 256 ? k_int8_quantize<DT, 256> : k_int8_quantize<DT, kMaxRowThreads>;
+template <int DT, bool FULL>
+int launch_quantize(const void *X, int64_t ldx, const int8_rows_t &q, uint32_t *status, cudaStream_t st) {
+    constexpr bool f32 = DT == QLORA_DTYPE_FP32;
+    constexpr int kWarpSteps = f32 ? 2 : 4;
+    const int cols = (int)q.cols;
+    if (cols <= 32 * kVec * kWarpSteps && q.rows >= 2 * device_sms()) {
+        k_int8_quantize<DT, FULL, kWarpSteps, true><<<(unsigned)((q.rows + 7) / 8), 256, 0, st>>>(
+            X, ldx, q.rows, cols, q.codes, q.ld, q.scales, status);
+    } else {
+        const int steps = row_steps(q.rows, q.cols, f32);
+        auto *k = steps == 1   ? k_int8_quantize<DT, FULL, 1, false>
+                  : steps == 2 ? k_int8_quantize<DT, FULL, 2, false>
+                               : k_int8_quantize<DT, FULL, f32 ? 2 : 8, false>;
+        k<<<(unsigned)q.rows, row_cta(q.cols, steps), 0, st>>>(X, ldx, q.rows, cols, q.codes, q.ld, q.scales, status);
+    }
+    QLORA_LAUNCH_CHECK();
+    return QLORA_OK;
 }
 
-template <int DT>
-auto pick_row_digits(int threads) {
-    return threads <= 384 ? k_int8_row_digits<DT, 384> : k_int8_row_digits<DT, kDigitThreads>;
+template <int DT, bool FULL>
+int launch_row_digits(const uint16_t *Y, int64_t rows, int64_t cols, const float *cscale, int8_t *planes, int64_t ld,
+                      float *steps, cudaStream_t st) {
+    const int n = row_steps(rows, cols, false);
+    auto *k = n == 1   ? k_int8_row_digits<DT, FULL, 1>
+              : n == 2 ? k_int8_row_digits<DT, FULL, 2>
+                       : k_int8_row_digits<DT, FULL, 8>;
+    k<<<(unsigned)rows, row_cta(cols, n), 0, st>>>(Y, rows, (int)cols, cscale, planes, ld, steps);
+    QLORA_LAUNCH_CHECK();
+    return QLORA_OK;
 }
 
 }  // namespace
 
 int launch_int8_quantize(const void *X, int dtype, int64_t ldx, const int8_rows_t &q, uint32_t *d_status,
                          cudaStream_t st) {
-    const int t = row_threads(q.cols, dtype == QLORA_DTYPE_FP32 ? kKeep<QLORA_DTYPE_FP32> : kKeep<QLORA_DTYPE_BF16>,
-                              kMaxRowThreads);
-    auto *k = dtype == QLORA_DTYPE_BF16   ? pick_quantize<QLORA_DTYPE_BF16>(t)
-              : dtype == QLORA_DTYPE_FP16 ? pick_quantize<QLORA_DTYPE_FP16>(t)
-                                          : pick_quantize<QLORA_DTYPE_FP32>(t);
-    k<<<(unsigned)q.rows, t, 0, st>>>(X, ldx, (int)q.cols, q.codes, q.ld, q.scales, d_status);
-    QLORA_LAUNCH_CHECK();
-    return QLORA_OK;
+    const int esize = dtype == QLORA_DTYPE_FP32 ? 4 : 2;
+    const bool full = (reinterpret_cast<uintptr_t>(X) & 15u) == 0 && (ldx * esize) % 16 == 0 && q.cols % kVec == 0;
+    auto *f = dtype == QLORA_DTYPE_BF16
+                  ? (full ? launch_quantize<QLORA_DTYPE_BF16, true> : launch_quantize<QLORA_DTYPE_BF16, false>)
+              : dtype == QLORA_DTYPE_FP16
+                  ? (full ? launch_quantize<QLORA_DTYPE_FP16, true> : launch_quantize<QLORA_DTYPE_FP16, false>)
+                  : (full ? launch_quantize<QLORA_DTYPE_FP32, true> : launch_quantize<QLORA_DTYPE_FP32, false>);
+    return f(X, ldx, q, d_status, st);
 }
 
 int launch_int8_row_digits(const uint16_t *Y, bool f16, int64_t rows, int64_t cols, const float *cscale,
                            int8_t *planes, int64_t ld, float *steps, cudaStream_t st) {
-    const bool vscale = (reinterpret_cast<uintptr_t>(cscale) & 15u) == 0;
-    const int t = row_threads(cols, 4, kDigitThreads);
-    auto *k = f16 ? pick_row_digits<QLORA_DTYPE_FP16>(t) : pick_row_digits<QLORA_DTYPE_BF16>(t);
-    k<<<(unsigned)rows, t, 0, st>>>(Y, rows, (int)cols, cscale, planes, ld, steps, vscale);
-    QLORA_LAUNCH_CHECK();
-    return QLORA_OK;
+    const bool full = ((reinterpret_cast<uintptr_t>(Y) | reinterpret_cast<uintptr_t>(cscale)) & 15u) == 0 &&
+                      cols % kVec == 0;
+    auto *f = f16 ? (full ? launch_row_digits<QLORA_DTYPE_FP16, true> : launch_row_digits<QLORA_DTYPE_FP16, false>)
+                  : (full ? launch_row_digits<QLORA_DTYPE_BF16, true> : launch_row_digits<QLORA_DTYPE_BF16, false>);
+    return f(Y, rows, cols, cscale, planes, ld, steps, st);
 }
 
 int launch_int8_col_digits(const void *S, int dtype, int64_t R, int r, const float *f, int8_t *planes, int64_t ld,

@@ -8,8 +8,6 @@ namespace {
 
 constexpr int kVec = 8;           // values per thread and step
 constexpr float kMagic = 12582912.f;   // 1.5 * 2^23: adding it rounds to an integer, ties to even
-// steps whose values stay in registers between the maximum and the codes
-template <int DT> constexpr int kKeep = DT == QLORA_DTYPE_FP32 ? 2 : 4;
 
 // Eight consecutive values of a row as they were loaded.
 template <int DT>
@@ -17,18 +15,21 @@ struct Raw8 {
     uint32_t w[DT == QLORA_DTYPE_FP32 ? 8 : 4];
 };
 
-// Values [8 v, 8 v + 8) of a row, zeros past its end.  A 16-bit row that starts
-// off a 16-byte border is read in the two aligned pieces around the values,
-// where both lie inside the row, and shifted into place.
-template <int DT>
+// Values [8 v, 8 v + 8) of a row, zeros past its end.  FULL: rows start on
+// 16-byte borders and hold a multiple of 8 values.  Otherwise a 16-bit row that
+// starts off a border is read in the two aligned pieces around the values,
+// where both lie inside the row, and shifted into place; what is left, at the
+// row's ends, comes value by value (the addresses clamped, so that the eight
+// loads do not wait for one another).
+template <int DT, bool FULL>
 __device__ __forceinline__ Raw8<DT> load8(const void *row, int v, int cols) {
     Raw8<DT> r;
     constexpr int kWords = sizeof(r.w) / 4;
     constexpr int kSize = kWords / 2;      // bytes a value
     const int e0 = v * kVec;
     const char *at = static_cast<const char *>(row) + (int64_t)e0 * kSize;
-    const uint32_t off = (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u);
-    if (off == 0 && e0 + kVec <= cols) {
+    const uint32_t off = FULL ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u);
+    if (FULL || (off == 0 && e0 + kVec <= cols)) {
 #pragma unroll
         for (int i = 0; i < kWords / 4; ++i) {
             const uint4 t = __ldg(reinterpret_cast<const uint4 *>(at) + i);
@@ -52,16 +53,18 @@ __device__ __forceinline__ Raw8<DT> load8(const void *row, int v, int cols) {
         for (int i = 0; i < kWords; ++i) r.w[i] = __funnelshift_r(t[i % 4], t[i % 4 + 1], 8 * (off & 3u));
         return r;
     }
-#pragma unroll
-    for (int i = 0; i < kWords; ++i) r.w[i] = 0;
+    uint32_t one[kVec];
 #pragma unroll
     for (int e = 0; e < kVec; ++e) {
-        if (e0 + e >= cols) break;
-        if (DT == QLORA_DTYPE_FP32)
-            r.w[e % kWords] = __ldg(static_cast<const uint32_t *>(row) + e0 + e);
-        else
-            r.w[e / 2] |= (uint32_t)__ldg(static_cast<const uint16_t *>(row) + e0 + e) << (16 * (e & 1));
+        const int i = e0 + e < cols ? e0 + e : cols - 1;
+        one[e] = DT == QLORA_DTYPE_FP32 ? __ldg(static_cast<const uint32_t *>(row) + i)
+                                        : (uint32_t)__ldg(static_cast<const uint16_t *>(row) + i);
     }
+#pragma unroll
+    for (int e = 0; e < kVec; ++e) one[e] = e0 + e < cols ? one[e] : 0u;
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
+        r.w[i] = DT == QLORA_DTYPE_FP32 ? one[i % kVec] : one[2 * i % kVec] | (one[(2 * i + 1) % kVec] << 16);
     return r;
 }
 
@@ -107,17 +110,10 @@ __device__ __forceinline__ uint32_t block_max(uint32_t m) {
     return __reduce_max_sync(0xffffffffu, v);
 }
 
-// Code of x exactly: the quotient in fp64 is never within 2^-33 (relative) of
-// a border between two codes without lying on it, since x and s have 24 bits.
-__device__ __noinline__ int code_exact(float x, float s) {
-    const double q = (double)x / (double)s;
-    const int c = __double2int_rn(q > 127.0 ? 127.0 : (q < -127.0 ? -127.0 : q));
-    return c;
-}
-
 // Store 8 code bytes at element e0 of a row (16-byte aligned start).
+template <bool FULL>
 __device__ __forceinline__ void store8(int8_t *row, int e0, int cols, uint32_t lo, uint32_t hi) {
-    if (e0 + kVec <= cols) {
+    if (FULL || e0 + kVec <= cols) {
         *reinterpret_cast<uint2 *>(row + e0) = make_uint2(lo, hi);
         return;
     }
@@ -129,58 +125,90 @@ __device__ __forceinline__ uint32_t bytes4(uint32_t a, uint32_t b, uint32_t c, u
     return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 
-// How a row's codes are decided.
-//   fp32: fma(x, 1/s, magic) rounds x * RN(1/s) to the nearest integer in its
-// low bits.  The rounded reciprocal puts the quotient at most 127 * 2^-23 off,
-// so a code is decided unless the quotient lies within 1e-4 of a border, where
-// code_exact decides (kNear).
+// How a row's codes are decided: fma(x, inv, magic) rounds x * inv to the
+// nearest integer in its low bits, with inv chosen for the row.
 //   16 bits: x and a have at most 11 significant bits, so the quotient by the
-// unrounded a / 127 either lies on a border or differs from it by at least
-// 1 / (254 * 2^11) > 2^-19 of itself.  Only border values need the direction
-// in which s was rounded, and a reciprocal moved by 2^-21 of itself that way
-// decides them: the other codes keep their side, 2^-21 + 3 * 2^-24 < 2^-19
-// (kSure).  Where s = a / 127 exactly, a power of two has an exact reciprocal
-// (true ties, to even), and other scales take the fp32 way.
-//   1/s near the ends of fp32's range: every code by code_exact (kExact).
-enum Decide { kSure, kNear, kExact };
+// unrounded a / 127 either lies on a border between two codes or differs from
+// it by at least 1 / (254 * 2^11) > 2^-19 of itself.  Only border values need
+// the direction in which s was rounded, and a reciprocal moved by 2^-21 of
+// itself that way decides them: the other codes keep their side, as
+// 2^-21 + 3 * 2^-24 < 2^-19.  Where s = a / 127 exactly, a power of two has an
+// exact reciprocal (true ties, to even); other scales (0.7% of fp16 rows, no
+// bf16 one) take code_exact.
+//   fp32: inv = RN(1/s) puts the quotient at most 127 * 2^-23 < 1.6e-5 off, so a
+// code is decided unless the quotient lies within 2e-5 of a border; a thread
+// that met such a one (`far`) does its part again by code_exact.
+//   1/s near the ends of fp32's range: code_exact.
+// Rows whose codes are all 0 (s = 0, or a NaN or an infinity in them): inv = 0
+// and a mask, since a NaN has no code.
+struct RowCode {
+    float s, inv;
+    uint32_t mask;
+    bool exact;
+};
 
 template <int DT>
-__device__ __forceinline__ Decide decide(float a, float s, float &inv) {
-    inv = 0.f;
-    if (s < 0x1p-120f) return kExact;
-    inv = __frcp_rn(s);
-    if (DT == QLORA_DTYPE_FP32) return kNear;
-    const float over = __fmaf_rn(s, 127.f, -a);   // > 0: s was rounded up
-    if (over == 0.f) return (__float_as_uint(s) & 0x7fffffu) == 0 ? kSure : kNear;
-    inv = __fmaf_rn(over > 0.f ? -0x1p-21f : 0x1p-21f, inv, inv);
-    return kSure;
+__device__ __forceinline__ RowCode row_code(uint32_t am) {
+    RowCode r;
+    const bool fin = am < 0x7f800000u;
+    const float a = __uint_as_float(am);
+    r.s = fin ? __fdiv_rn(a, 127.f) : __uint_as_float(0x7fffffffu);
+    r.mask = fin ? 0xffffffffu : 0u;
+    r.inv = 0.f;
+    r.exact = false;
+    if (!fin || r.s == 0.f) return r;
+    if (r.s < 0x1p-120f) {
+        r.exact = true;
+        return r;
+    }
+    r.inv = __frcp_rn(r.s);
+    if (DT == QLORA_DTYPE_FP32) return r;
+    const float over = __fmaf_rn(r.s, 127.f, -a);   // > 0: s was rounded up
+    if (over == 0.f) r.exact = (__float_as_uint(r.s) & 0x7fffffu) != 0;
+    else r.inv = __fmaf_rn(over > 0.f ? -0x1p-21f : 0x1p-21f, r.inv, r.inv);
+    return r;
 }
 
 template <int DT>
-__device__ __forceinline__ uint2 encode8(const Raw8<DT> &r, float s, float inv, Decide how) {
+__device__ __forceinline__ uint2 encode8(const Raw8<DT> &r, const RowCode &rc, float &far) {
     uint32_t c[kVec];
-    if (how == kSure) {
 #pragma unroll
-        for (int e = 0; e < kVec; e += 2) {
-            float t0, t1;
-            fma2_rn(inv, val8(r, e), val8(r, e + 1), kMagic, kMagic, t0, t1);
-            c[e] = __float_as_uint(t0), c[e + 1] = __float_as_uint(t1);
-        }
-    } else {
-        float far = how == kExact ? 1.f : 0.f;
-#pragma unroll
-        for (int e = 0; e < kVec; ++e) {
-            const float x = val8(r, e);
-            const float t = __fmaf_rn(x, inv, kMagic);
-            c[e] = __float_as_uint(t);
-            far = fmaxf(far, fabsf(__fmaf_rn(x, inv, -(t - kMagic))));
-        }
-        if (far > 0.4999f) {
-#pragma unroll
-            for (int e = 0; e < kVec; ++e) c[e] = (uint32_t)code_exact(val8(r, e), s);
-        }
+    for (int e = 0; e < kVec; ++e) {
+        const float x = val8(r, e);
+        const float t = __fmaf_rn(x, rc.inv, kMagic);
+        c[e] = __float_as_uint(t);
+        if (DT == QLORA_DTYPE_FP32) far = fmaxf(far, fabsf(__fmaf_rn(x, rc.inv, -(t - kMagic))));
     }
-    return make_uint2(bytes4(c[0], c[1], c[2], c[3]), bytes4(c[4], c[5], c[6], c[7]));
+    return make_uint2(bytes4(c[0], c[1], c[2], c[3]) & rc.mask, bytes4(c[4], c[5], c[6], c[7]) & rc.mask);
+}
+constexpr float kFar = 0.49998f;
+
+// Code of x by division.  fp16 (s = a / 127 exactly): a rounded fp32 quotient
+// is on a border only if the quotient is.  Else in fp64, where the quotient of
+// two numbers of 24 bits is never within 2^-33 (relative) of a border without
+// lying on it.
+template <int DT>
+__device__ __forceinline__ int code_exact(float x, float s) {
+    if (DT == QLORA_DTYPE_FP16) return __float2int_rn(__fdiv_rn(x, s));
+    const double q = (double)x / (double)s;
+    return __double2int_rn(q > 127.0 ? 127.0 : (q < -127.0 ? -127.0 : q));
+}
+
+// A thread's part of a row (vectors v0, v0 + stride, ...) by code_exact, to dst
+// and, if it is not NULL, to also.  Out of line: few rows come here.
+template <int DT>
+__device__ __noinline__ void encode_exact(const void *row, int v0, int stride, int cols, float s, int8_t *dst,
+                                          int8_t *also) {
+#pragma unroll 1
+    for (int v = v0; v * kVec < cols; v += stride) {
+        const Raw8<DT> r = load8<DT, false>(row, v, cols);
+        uint32_t c[kVec];
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) c[e] = (uint32_t)code_exact<DT>(val8(r, e), s);
+        const uint32_t lo = bytes4(c[0], c[1], c[2], c[3]), hi = bytes4(c[4], c[5], c[6], c[7]);
+        store8<false>(dst, v * kVec, cols, lo, hi);
+        if (also) store8<false>(also, v * kVec, cols, lo, hi);
+    }
 }
 
 }  // namespace

@@ -79,6 +79,31 @@ def test_quantize_extremes(qlib):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("rows,cols,stride", [(2000, 2048, 2048), (1000, 4099, 4104), (700, 20000, 20000),
+                                              (900, 3001, 3001), (3000, 1000, 1000), (400, 300, 301), (901, 1024, 2048),
+                                              (641, 9000, 9008)])
+def test_quantize_many_rows(qlib, rows, cols, stride, dtype):
+    """Persistent CTAs, a warp a row and a CTA a row; among the rows: zero, tiny, huge and non-finite
+    ones, scales that a / 127 gives exactly (a = 127 m 2^e, quotients of k + 1/2 among them), ties."""
+    g = torch.Generator().manual_seed(rows + cols)
+    x = torch.randn(rows, stride, generator=g)
+    x[5] = 0
+    x[6] *= 1e-6 if dtype == "fp16" else 1e-37
+    x[7] *= 1e3 if dtype == "fp16" else 1e37
+    x[8, 3] = float("inf")
+    x[9, cols - 1] = float("nan")
+    k = torch.arange(stride) % 253
+    for i, m in enumerate((1, 2, 3, 5, 7, 9, 11, 13, 15)):
+        x[20 + i] = (k - 126 + 0.5) * m * 2.0 ** (i % 3 - 1) / 2      # k + 1/2 steps, where the type holds them
+        x[20 + i, 0] = 127 * m * 2.0 ** (i % 3 - 1) / 2
+    x = x.to(DT[dtype]).cuda()[:, :cols]
+    out = qlib.Int8Rows(torch.full((rows + 1, (cols + 31) // 16 * 16), 77, dtype=torch.int8, device="cuda")[:rows, :cols],
+                        torch.empty(rows, device="cuda"))
+    check_rows(qlib.int8_quantize(x, out=out), x)
+    assert (out.codes.as_strided((rows, 16), out.codes.stride(), out.codes.storage_offset() + cols) == 77).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
 def test_quantize_nonfinite(qlib, dtype, bad):
     x = rand(3, 6, 100, dtype=dtype)
@@ -122,6 +147,7 @@ MATMUL = [(1, 1, 1), (1, 64, 8), (1, 4096, 256), (2, 100, 130), (16, 4096, 1000)
           (5, 131072, 8), (2049, 100, 16), (512, 4096, 4096), (700, 1500, 2504), (384, 96, 5000),
           # many tokens: one tile a CTA pair and several, reductions shorter and longer than the ring
           (1100, 200, 5000), (2600, 1500, 2504), (513, 96, 9999), (700, 5000, 333), (2100, 2053, 40),
+          (1200, 40, 3000), (1000, 24, 2504), (600, 16, 11008), (950, 33, 2500), (620, 200, 25000),
           (4100, 640, 3000), (4100, 200, 3001), (2100, 3000, 700), (9300, 130, 1000),
           # a few tokens: quantized by the product's own CTAs or before it, rows in one wave and several
           (3, 1000, 2500), (8, 2048, 9500), (4, 513, 5000), (7, 12000, 33), (1, 28672, 100), (2, 8192, 5003),
