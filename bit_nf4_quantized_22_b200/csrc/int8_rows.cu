@@ -78,11 +78,9 @@ k_int8_quantize(const void *X, int64_t ldx, int64_t rows, int cols, int8_t *code
 // a / 65278, so a row by at most sqrt(cols) / 65278 of its norm whatever its
 // values (about 4e-5 for normal ones): below the 16-bit output's own rounding.
 //
-// d[e] = y[e] * scale[e] of one vector; the scales come from L1.
-template <int DT, bool FULL>
-__device__ __forceinline__ void digit_products(const Raw8<DT> &r, const float *__restrict__ cscale, int v, int cols,
-                                               float (&d)[kVec]) {
-    float f[kVec];
+// The scales of one vector's columns (from L1 the second time).
+template <bool FULL>
+__device__ __forceinline__ void digit_scales(const float *__restrict__ cscale, int v, int cols, float (&f)[kVec]) {
     if (FULL) {
         const float4 x = __ldg(reinterpret_cast<const float4 *>(cscale + v * kVec));
         const float4 y = __ldg(reinterpret_cast<const float4 *>(cscale + v * kVec) + 1);
@@ -91,6 +89,9 @@ __device__ __forceinline__ void digit_products(const Raw8<DT> &r, const float *_
 #pragma unroll
         for (int e = 0; e < kVec; ++e) f[e] = __ldg(cscale + (v * kVec + e < cols ? v * kVec + e : cols - 1));
     }
+}
+template <int DT>
+__device__ __forceinline__ void digit_products(const Raw8<DT> &r, const float (&f)[kVec], float (&d)[kVec]) {
 #pragma unroll
     for (int e = 0; e < kVec; ++e) d[e] = __fmul_rn(val8(r, e), f[e]);
 }
@@ -136,47 +137,85 @@ __device__ __forceinline__ void put_digits(float (&d)[kVec], const RowDigits &r,
     store8<FULL>(lo, e0, cols, __byte_perm(q[0], q[1], 0x6420), __byte_perm(q[2], q[3], 0x6420));
 }
 
-template <int DT, bool FULL, int STEPS>
-__global__ void __launch_bounds__(row_threads(STEPS))
+// ROWS rows a CTA: the scales, read for the maxima and again for the digits, are
+// most of the traffic inside the SM, and two rows share them (4096 x 11008: 37 us,
+// one row 41 us).
+template <int DT, bool FULL, int STEPS, int ROWS>
+__global__ void __launch_bounds__(STEPS == 4 ? 512 : 1024)
 k_int8_row_digits(const void *Y, int64_t rows, int cols, const float *__restrict__ cscale,
                   int8_t *planes, int64_t ld, float *steps) {
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
+    __shared__ uint32_t part[ROWS][32];
     const int nv = (cols + kVec - 1) / kVec;
-    const int64_t m = blockIdx.x;
-    const char *row = static_cast<const char *>(Y) + m * (int64_t)cols * 2;
-    Raw8<DT> keep[STEPS];
-    float top = 0.f, d[kVec];
+    const int64_t m0 = (int64_t)blockIdx.x * ROWS;
+    const char *row[ROWS];
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-        const int v = i * blockDim.x + threadIdx.x;
-        if (v < nv) keep[i] = load8<DT, FULL>(row, v, cols);
+    for (int i = 0; i < ROWS; ++i)   // a last odd row stands in for its missing neighbour too
+        row[i] = static_cast<const char *>(Y) + (m0 + i < rows ? m0 + i : m0) * (int64_t)cols * 2;
+    Raw8<DT> keep[STEPS][ROWS];
+    float top[ROWS] = {}, d[kVec];
+#pragma unroll
+    for (int j = 0; j < STEPS; ++j) {
+        const int v = j * blockDim.x + threadIdx.x;
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+            if (v < nv) keep[j][i] = load8<DT, FULL>(row[i], v, cols);
     }
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-        const int v = i * blockDim.x + threadIdx.x;
+    for (int j = 0; j < STEPS; ++j) {
+        const int v = j * blockDim.x + threadIdx.x;
         if (v < nv) {
-            digit_products<DT, FULL>(keep[i], cscale, v, cols, d);
-            top = digit_max(d, top);
+            float f[kVec];
+            digit_scales<FULL>(cscale, v, cols, f);
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) {
+                digit_products<DT>(keep[j][i], f, d);
+                top[i] = digit_max(d, top[i]);
+            }
         }
     }
     for (int v = STEPS * blockDim.x + threadIdx.x; v < nv; v += blockDim.x) {
-        digit_products<DT, FULL>(load8<DT, FULL>(row, v, cols), cscale, v, cols, d);
-        top = digit_max(d, top);
-    }
-    const RowDigits r = row_digits(block_max(__float_as_uint(top) & 0x7fffffffu));
-    if (threadIdx.x == 0) steps[m] = r.step;
-    int8_t *hi = planes + m * ld, *lo = planes + (rows + m) * ld;
+        float f[kVec];
+        digit_scales<FULL>(cscale, v, cols, f);
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-        const int v = i * blockDim.x + threadIdx.x;
+        for (int i = 0; i < ROWS; ++i) {
+            digit_products<DT>(load8<DT, FULL>(row[i], v, cols), f, d);
+            top[i] = digit_max(d, top[i]);
+        }
+    }
+    RowDigits r[ROWS];
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(top[i]) & 0x7fffffffu);
+        if ((threadIdx.x & 31) == 0) part[i][threadIdx.x >> 5] = m;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const uint32_t m = (threadIdx.x & 31) < blockDim.x >> 5 ? part[i][threadIdx.x & 31] : 0u;
+        r[i] = row_digits(__reduce_max_sync(0xffffffffu, m));
+        if (threadIdx.x == 0 && m0 + i < rows) steps[m0 + i] = r[i].step;
+    }
+    auto put = [&](const Raw8<DT> &x, int i, int v, const float (&f)[kVec]) {
+        if (m0 + i >= rows) return;
+        digit_products<DT>(x, f, d);
+        put_digits<FULL>(d, r[i], planes + (m0 + i) * ld, planes + (rows + m0 + i) * ld, v * kVec, cols);
+    };
+#pragma unroll
+    for (int j = 0; j < STEPS; ++j) {
+        const int v = j * blockDim.x + threadIdx.x;
         if (v < nv) {
-            digit_products<DT, FULL>(keep[i], cscale, v, cols, d);
-            put_digits<FULL>(d, r, hi, lo, v * kVec, cols);
+            float f[kVec];
+            digit_scales<FULL>(cscale, v, cols, f);
+#pragma unroll
+            for (int i = 0; i < ROWS; ++i) put(keep[j][i], i, v, f);
         }
     }
     for (int v = STEPS * blockDim.x + threadIdx.x; v < nv; v += blockDim.x) {
-        digit_products<DT, FULL>(load8<DT, FULL>(row, v, cols), cscale, v, cols, d);
-        put_digits<FULL>(d, r, hi, lo, v * kVec, cols);
+        float f[kVec];
+        digit_scales<FULL>(cscale, v, cols, f);
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i) put(load8<DT, FULL>(row[i], v, cols), i, v, f);
     }
 }
 
@@ -388,11 +427,13 @@ int launch_quantize(const void *X, int64_t ldx, const int8_rows_t &q, uint32_t *
 template <int DT, bool FULL>
 int launch_row_digits(const uint16_t *Y, int64_t rows, int64_t cols, const float *cscale, int8_t *planes, int64_t ld,
                       float *steps, cudaStream_t st) {
-    const int n = row_steps(rows, cols, false);
-    auto *k = n == 1   ? k_int8_row_digits<DT, FULL, 1>
-              : n == 2 ? k_int8_row_digits<DT, FULL, 2>
-                       : k_int8_row_digits<DT, FULL, 8>;
-    k<<<(unsigned)rows, row_cta(cols, n), 0, st>>>(Y, rows, (int)cols, cscale, planes, ld, steps);
+    const int n = row_steps(rows, cols, false), per = n == 8 ? 2 : 1;
+    auto *k = n == 1   ? k_int8_row_digits<DT, FULL, 1, 1>
+              : n == 2 ? k_int8_row_digits<DT, FULL, 2, 1>
+                       : k_int8_row_digits<DT, FULL, 4, 2>;
+    const int t = n == 8 ? row_cta(cols, 4) : row_cta(cols, n);
+    k<<<(unsigned)((rows + per - 1) / per), n == 8 && t > 512 ? 512 : t, 0, st>>>(Y, rows, (int)cols, cscale, planes, ld,
+                                                                                steps);
     QLORA_LAUNCH_CHECK();
     return QLORA_OK;
 }

@@ -147,7 +147,8 @@ MATMUL = [(1, 1, 1), (1, 64, 8), (1, 4096, 256), (2, 100, 130), (16, 4096, 1000)
           (5, 131072, 8), (2049, 100, 16), (512, 4096, 4096), (700, 1500, 2504), (384, 96, 5000),
           # many tokens: one tile a CTA pair and several, reductions shorter and longer than the ring
           (1100, 200, 5000), (2600, 1500, 2504), (513, 96, 9999), (700, 5000, 333), (2100, 2053, 40),
-          (1200, 40, 3000), (1000, 24, 2504), (600, 16, 11008), (950, 33, 2500), (620, 200, 25000),
+          (1200, 40, 3000), (1000, 24, 2504), (600, 16, 11008), (950, 33, 2500), (620, 200, 25000), (1501, 8, 8192),
+          (3001, 16, 11001),
           (4100, 640, 3000), (4100, 200, 3001), (2100, 3000, 700), (9300, 130, 1000),
           # a few tokens: quantized by the product's own CTAs or before it, rows in one wave and several
           (3, 1000, 2500), (8, 2048, 9500), (4, 513, 5000), (7, 12000, 33), (1, 28672, 100), (2, 8192, 5003),
