@@ -357,7 +357,7 @@ int run_adapter_down(const Dims &d, const uint16_t *X, const uint16_t *A, uint16
 constexpr int64_t kInt8MaxTerms = 131072;
 
 int check_rows8(const int8_rows_t *q) {
-    if (!q || q->rows < 0 || q->rows > (int64_t)0x7fffffff || q->cols < 1 || q->cols > (int64_t)1 << 30)
+    if (!q || q->rows < 0 || q->rows > (int64_t)1 << 30 || q->cols < 1 || q->cols > (int64_t)1 << 30)
         return QLORA_EINVAL;
     if (q->ld < q->cols || q->ld % 16 != 0) return QLORA_EINVAL;
     if (q->rows == 0) return QLORA_OK;
@@ -723,14 +723,14 @@ int int8_matmul(const void *X, int32_t x_dtype, int64_t ldx, const int8_rows_t *
 }
 
 size_t int8_matmul_backward_workspace_size(int64_t M, const int8_rows_t *W) {
-    if (M < 1 || M > (int64_t)0x7fffffff || check_rows8(W) || W->rows > kInt8MaxTerms) return 0;
+    if (M < 1 || M > (int64_t)1 << 30 || check_rows8(W) || W->rows > kInt8MaxTerms) return 0;
     return layout_grad8(M, *W, nullptr, nullptr);
 }
 
 int int8_matmul_backward(const uint16_t *dY, int32_t dtype, int64_t M, const int8_rows_t *W, uint16_t *dX,
                          void *workspace, size_t ws_bytes, uint32_t *d_status, void *stream) {
     RC(check_rows8(W));
-    if (M < 0 || M > (int64_t)0x7fffffff || W->rows < 1) return QLORA_EINVAL;
+    if (M < 0 || M > (int64_t)1 << 30 || W->rows < 1) return QLORA_EINVAL;
     if (dtype != QLORA_DTYPE_BF16 && dtype != QLORA_DTYPE_FP16) return QLORA_EINVAL;
     if (W->rows > kInt8MaxTerms) return QLORA_EUNSUPPORTED;
     if (M == 0) return QLORA_OK;

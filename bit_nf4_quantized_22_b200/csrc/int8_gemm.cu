@@ -31,6 +31,11 @@ constexpr int kTTwoN = 64;                     // UMMA N up to which two CTAs sh
 constexpr int kTSmemTwo = 110 * 1024;
 constexpr int kTSmemOne = 220 * 1024;
 
+// 256 * (a rounded upper sum) + the lower sum, in fp32: off by 2^-23 of the larger of the two terms
+__device__ __forceinline__ float join_digits(float upper, int lower) {
+    return __fmaf_rn(upper, 256.f, (float)lower);
+}
+
 // kind::i8 instruction descriptor: signed 8-bit A and B, s32 accumulator.
 __host__ __device__ constexpr uint32_t idesc_i8(uint32_t m, uint32_t n, uint32_t a_mn, uint32_t b_mn) {
     return (2u << 4) | (1u << 7) | (1u << 10) | (a_mn << 15) | (b_mn << 16) | ((n >> 3) << 17) | ((m >> 4) << 24);
@@ -278,7 +283,12 @@ k_int8_tall(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             if (q >= p.Q) break;
             int4 t = column(0, c);
             float v[4] = {(float)t.x, (float)t.y, (float)t.z, (float)t.w};
-            if (p.planes > 1) {
+            if (p.planes == 2) {
+                // as k_int8_wide does, so that a token's gradient does not depend on its batch
+                t = column(1, c);
+                v[0] = join_digits(v[0], t.x), v[1] = join_digits(v[1], t.y);
+                v[2] = join_digits(v[2], t.z), v[3] = join_digits(v[3], t.w);
+            } else if (p.planes > 2) {
                 int64_t sum[4] = {t.x, t.y, t.z, t.w};
                 for (int d = 1; d < p.planes; ++d) {
                     t = column(d, c);
@@ -597,7 +607,7 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                     }
 #pragma unroll
                     for (int j = 0; j < 32; ++j)
-                        v[j] = __fmaf_rn(__fmul_rn(__fmaf_rn((float)(int)a[j], 256.f, (float)(int)b[j]), rs[0]),
+                        v[j] = __fmaf_rn(__fmul_rn(join_digits((float)(int)a[j], (int)b[j]), rs[0]),
                                          cs[col + j], cb[col + j]);
                     store32(p, mrow, n0 + col, v);
                 }

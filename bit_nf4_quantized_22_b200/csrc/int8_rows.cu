@@ -363,9 +363,17 @@ __global__ void k_int8_dequantize(const int8_t *__restrict__ codes, int64_t ld, 
         const int64_t m = i / nv, e0 = (i % nv) * kVec;
         const float s = __ldg(scales + m);
         const int8_t *src = codes + m * ld + e0;
+        uint2 c = make_uint2(0u, 0u);
+        if (e0 + kVec <= cols) {
+            c = __ldg(reinterpret_cast<const uint2 *>(src));
+        } else {
+            for (int e = 0; e0 + e < cols; ++e)
+                (e < 4 ? c.x : c.y) |= (uint32_t)(uint8_t)__ldg(src + e) << (8 * (e & 3));
+        }
         float v[kVec];
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) v[e] = e0 + e < cols ? __fmul_rn((float)__ldg(src + e), s) : 0.f;
+        for (int e = 0; e < kVec; ++e)
+            v[e] = __fmul_rn((float)(int8_t)(uint8_t)((e < 4 ? c.x : c.y) >> (8 * (e & 3))), s);
         if (DT == QLORA_DTYPE_FP32) {
             float *o = static_cast<float *>(out) + m * cols + e0;
             if (vec) {

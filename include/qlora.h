@@ -264,7 +264,7 @@ int qlora_backward(const uint16_t *X, const uint16_t *dY, int64_t M, const nf4_w
  *   codes    [rows][ld] int8, the first cols of a row valid; 16-byte aligned
  *   scales   [rows] fp32
  *   ld       bytes from one row to the next: >= cols, a multiple of 16
- *   cols     1 .. 2^30
+ *   rows     up to 2^30;  cols  1 .. 2^30
  * Row m stands for codes[m][k] * scales[m].  The rows are tokens for an
  * activation, output channels for a weight Wt:[Dout, Din]. */
 typedef struct {
@@ -295,7 +295,7 @@ int int8_dequantize(const int8_rows_t *q, int32_t dtype, void *out, void *stream
 /* int8_matmul -- y = x . W^T with both operands in 8 bits:
  *   Y[m][n] = RN(fma(RN32(RN32(sum_k cx[m][k] cw[n][k]) * sx[m]), sw[n], bias[n])),
  * the sum exact in 32-bit integers, then rounded to fp32, and the fma rounded
- * once in fp32.
+ * once in fp32: a token's result depends on nothing else in its batch.
  *   X     device [M, K] (x_dtype, row stride ldx) to be quantized into X8
  *         first, as int8_quantize does; or NULL: X8 holds the tokens already
  *   X8    [M = X8->rows, K]; with X its buffers receive the codes and scales,

@@ -272,6 +272,74 @@ def test_input_gradient_rows_of_any_size(qlib):
         assert ((dx[m].double() - want[m]).abs() <= tol).all(), m
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("K,N", [(1000, 3000), (512, 4096)])
+def test_tokens_do_not_depend_on_their_batch(qlib, K, N, dtype):
+    """The same bits for a token alone, in a few, in some and in many (four kernels and every split)."""
+    x = rand(1, 4000, K, dtype=dtype)
+    w = qlib.int8_quantize(rand(2, N, K, dtype="fp32"))
+    dy = rand(3, 4000, N, dtype=dtype)
+    y, dx = qlib.int8_matmul(x, w), qlib.int8_matmul_backward(dy, w)
+    for m in (1, 2, 4, 5, 16, 40, 130, 400, 1100):
+        assert torch.equal(qlib.int8_matmul(x[:m], w), y[:m]), m
+        assert torch.equal(qlib.int8_matmul_backward(dy[:m], w), dx[:m]), m
+
+
+def test_nonfinite_and_zero_weight_rows(qlib):
+    """A channel with a NaN gives NaN in its column and, through its scale, in every input gradient;
+    a zero channel gives zeros."""
+    w0 = rand(1, 70, 96, dtype="fp32")
+    w0[5, 3] = float("nan")
+    w0[6] = 0
+    w = qlib.int8_quantize(w0)
+    for M in (1, 30, 700):
+        y = qlib.int8_matmul(rand(2, M, 96), w)
+        assert torch.isnan(y[:, 5]).all() and not y[:, 6].any() and torch.isfinite(y[:, 7:]).all()
+    assert torch.isnan(qlib.int8_matmul_backward(rand(3, 4, 70), w)).all()
+    v = qlib.int8_dequantize(w)
+    assert torch.isnan(v[5]).all() and not v[6].any()
+
+
+def test_refusals_on_the_device(qlib):
+    x, w8 = rand(1, 4, 64), qlib.int8_quantize(rand(2, 16, 64, dtype="fp32"))
+    x8, dy = qlib.int8_quantize(x), rand(3, 4, 16)
+    E = qlib.Int8Rows
+    for call in (lambda: qlib.int8_quantize(x.double()), lambda: qlib.int8_quantize(x[0]),
+                 lambda: qlib.int8_matmul(x.int(), w8), lambda: qlib.int8_matmul(x, w8, dtype=torch.float64),
+                 lambda: qlib.int8_matmul(x, w8, bias=torch.zeros(16, device="cuda")),
+                 lambda: qlib.int8_matmul(x, w8, out=torch.zeros(4, 16, device="cuda"), dtype=torch.bfloat16),
+                 lambda: qlib.int8_matmul_backward(dy.float(), w8), lambda: qlib.int8_matmul(x, w8.codes),
+                 lambda: qlib.int8_matmul(E(x8.codes.short(), x8.scales), w8),
+                 lambda: qlib.int8_matmul(E(x8.codes, x8.scales.cpu()), w8),
+                 lambda: qlib.Int8LinearFn.apply(x.float(), w8),
+                 lambda: qlib.int8_dequantize(x8, torch.int8)):
+        with pytest.raises((TypeError, AttributeError)):
+            call()
+    for call in (lambda: qlib.int8_quantize(x.t()), lambda: qlib.int8_quantize(x[:, :0]),
+                 lambda: qlib.int8_quantize(x[:1].expand(4, 64)), lambda: qlib.int8_quantize(x, out=w8),
+                 lambda: qlib.int8_matmul(x[:, :32], w8), lambda: qlib.int8_matmul(x, w8, out=dy[:2]),
+                 lambda: qlib.int8_matmul(x, w8, bias=dy[0, :8]), lambda: qlib.int8_matmul(x8, w8, x8_out=x8),
+                 lambda: qlib.int8_matmul(x, w8, x8_out=w8), lambda: qlib.int8_matmul_backward(dy[:, :8].contiguous(), w8),
+                 lambda: qlib.int8_matmul(E(x8.codes[:, 1:33], x8.scales), w8),
+                 lambda: qlib.int8_matmul(E(x8.codes, x8.scales[:3]), w8),
+                 lambda: qlib.int8_matmul(E(x8.codes.t().contiguous().t(), x8.scales), w8)):
+        with pytest.raises(ValueError):
+            call()
+    w, x, A, B, dy = layer_case(qlib, 20, 128, 64, 4, 1, "bf16")
+    x8 = qlib.int8_quantize(x)
+    bad8 = qlib.int8_quantize(x[:19])
+    for call in (lambda: qlib.backward(bad8, dy, w, A, B, 8.0), lambda: qlib.backward(x8, dy, w, A[:64], B, 8.0),
+                 lambda: qlib.backward(x8, dy, w, A, B[:, :32].contiguous(), 8.0),
+                 lambda: qlib.backward(x8, dy, w, A, B, 8.0, T=torch.zeros(20, 3, device="cuda")),
+                 lambda: qlib.backward(x8, dy, w, A, B, 8.0, pool_group=2)):
+        with pytest.raises(ValueError):
+            call()
+    with pytest.raises(TypeError):
+        qlib.backward(x8, dy.half(), w, A, B, 8.0)
+    with pytest.raises(qlib.QLoRAError):
+        qlib.backward(x8, dy, w, A, B, float("inf"))
+
+
 # ------------------------------------------------------------------------------ checkpoint
 def layer_case(qlib, M, K, N, r, g, dtype, seed=0):
     w = qlib.quantize(rand(seed + 1, N, K, dtype="fp32", scale=0.02), compute_dtype=DT[dtype])
@@ -400,6 +468,74 @@ def test_merge_then_eight_bits(qlib):
     tol = ex * W.double().abs().sum(1)[None] + x.double().abs().sum(1, keepdim=True) * ew + K * ex * ew
     assert ((y.double() - exact).abs() <= tol + 2.0 ** -8 * (exact.abs() + tol)).all()
     assert torch.equal(xg.grad, qlib.int8_matmul_backward(dy, w8))
+
+
+def test_autograd_captured(qlib):
+    """Forward and backward of both autograd functions in one graph, replayed on new inputs."""
+    M, K, N = 30, 256, 128
+    w, x, A, B, dy = layer_case(qlib, M, K, N, 8, 1, "bf16")
+    w8 = qlib.int8_quantize(qlib.dequantize(w, dtype=torch.float32))
+
+    def step(x, A, B, dy):
+        x, A, B = (t.detach().requires_grad_() for t in (x, A, B))
+        y = qlib.QLoRALinear8BitInputFn.apply(x, A, B, w, 16.0)
+        z = qlib.Int8LinearFn.apply(x, w8)
+        return torch.autograd.grad((y, z), (x, A, B), (dy, dy))
+
+    xs, dys = x.clone(), dy.clone()
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step(xs, A, B, dys)
+    torch.cuda.current_stream().wait_stream(s)
+    gr = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(gr):
+        out = step(xs, A, B, dys)
+    for seed in (50, 51):
+        x2, dy2 = rand(seed, M, K), rand(seed + 9, M, N)
+        xs.copy_(x2)
+        dys.copy_(dy2)
+        gr.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, step(x2, A, B, dy2)))
+
+
+def test_two_streams_at_once(qlib):
+    """Calls in flight on two streams, each with its own buffers, from two host threads."""
+    import threading
+    w = qlib.int8_quantize(rand(1, 1500, 700, dtype="fp32"))
+    xs = [rand(2 + i, 300 + 100 * i, 700) for i in range(2)]
+    want = [(qlib.int8_matmul(x, w), qlib.int8_matmul_backward(rand(9, x.shape[0], 1500), w)) for x in xs]
+    torch.cuda.synchronize()
+    got, errors = [None, None], []
+
+    def work(i):
+        try:
+            st = torch.cuda.Stream()
+            dy = rand(9, xs[i].shape[0], 1500)
+            torch.cuda.synchronize()
+            with torch.cuda.stream(st):
+                for _ in range(20):
+                    got[i] = (qlib.int8_matmul(xs[i], w), qlib.int8_matmul_backward(dy, w))
+            st.synchronize()
+        except Exception as e:   # noqa: BLE001
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    [t.start() for t in threads]
+    [t.join() for t in threads]
+    assert not errors
+    assert all(torch.equal(a, b) for g, v in zip(got, want) for a, b in zip(g, v))
+
+
+@pytest.mark.skipif(torch.cuda.device_count() < 2, reason="needs a second GPU")
+def test_other_device_than_the_current_one(qlib):
+    x, w0 = rand(1, 20, 128).to("cuda:1"), rand(2, 64, 128, dtype="fp32").to("cuda:1")
+    w = qlib.int8_quantize(w0)
+    assert w.device.index == 1 and torch.equal(qlib.int8_matmul(x, w).cpu(),
+                                               qlib.int8_matmul(x.to("cuda:0"), qlib.int8_quantize(w0.to("cuda:0"))).cpu())
+    with pytest.raises(ValueError):
+        qlib.int8_matmul(x.to("cuda:0"), w)
 
 
 def test_streams_graphs_and_repeats(qlib):
