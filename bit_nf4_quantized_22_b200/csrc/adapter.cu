@@ -10,7 +10,8 @@
 // hi/lo split of fp32 operands and the deterministic split-K reduce.  fp32
 // operands (T, G, pool(x)) are carried as two bf16 terms hi + lo,
 // hi = RN_bf16(v), lo = RN_bf16(v - hi), which keeps ~16 mantissa bits; the
-// GEMM multiplies both terms and the reduce kernel adds the two halves in fp32.
+// GEMM multiplies the terms and the reduce kernel adds their products in fp32.
+// (The backward from an 8-bit checkpoint carries T in a third term, to 24 bits.)
 #include "common.cuh"
 
 namespace qlora {
@@ -49,26 +50,24 @@ __global__ void k_pool_split(const uint16_t *__restrict__ X, int64_t M, int64_t 
     lo[i] = enc16(v - dec16(h, f16), f16);
 }
 
-// fp32 [rows][r] -> compute dtype [rows][2 rp] = [hi | lo] with zero padding
-__global__ void k_split_f32(const float *__restrict__ src, int64_t rows, int r, int rp,
+// fp32 [rows][r] -> compute dtype [rows][terms rp] = [hi | lo] (terms = 3: and
+// what is left of them, 24 bits in bf16) with zero padding
+__global__ void k_split_f32(const float *__restrict__ src, int64_t rows, int r, int rp, int terms,
                             uint16_t *__restrict__ dst, bool f16) {
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= rows * rp) return;
     const int64_t row = i / rp;
     const int j = (int)(i % rp);
-    uint16_t h = 0, l = 0;
-    if (j < r) {
-        const float v = src[row * r + j];
-        h = enc16(v, f16);
-        l = enc16(v - dec16(h, f16), f16);
+    float v = j < r ? src[row * r + j] : 0.f;
+    for (int t = 0; t < terms; ++t) {
+        const uint16_t h = enc16(v, f16);
+        dst[(row * terms + t) * rp + j] = h;
+        v -= dec16(h, f16);
     }
-    dst[row * 2 * rp + j] = h;
-    dst[row * 2 * rp + rp + j] = l;
 }
 
 // Deterministic split-K reduce (fixed summation order) with the adapter
-// epilogues.  v(p,q) = sum_z partial[z][p][q] (+ partial[z][p][q+H] when H>0),
-// for q < Qv:
+// epilogues.  v(p,q) = sum_z sum_{t < terms} partial[z][p][q + t H] for q < Qv:
 //   out_f32[p*fsp + q*fsq]  = f32_scale * v
 //   out_bf16[p*bsp + q]     = RN_bf16(bf_scale * v)          (row stride bsp)
 //   out_split[p*2*sp + q], [p*2*sp + sp + q] = hi/lo of v    (row stride 2 sp)
@@ -77,7 +76,7 @@ struct ReduceArgs {
     const float *partial;
     int splits;
     int64_t P, Qp;        // partial layout [splits][P][Qp]
-    int H;                // 0, or the offset of the second half to add
+    int H, terms;         // offset from one term of the split operand to the next
     int Qv;               // valid output columns
     float f32_scale; float *out_f32; int64_t fsp, fsq;
     float bf_scale; uint16_t *out_bf16; int64_t bsp;
@@ -102,7 +101,7 @@ __global__ void k_reduce_scalar(ReduceArgs a) {
     for (int z = 0; z < a.splits; ++z) {
         const float *base = a.partial + ((int64_t)z * a.P + p) * a.Qp;
         v += base[q];
-        if (a.H) v += base[q + a.H];
+        for (int t = 1; t < a.terms; ++t) v += base[q + t * a.H];
     }
     if (a.out_f32) a.out_f32[p * a.fsp + q * a.fsq] = a.f32_scale * v;
     if (a.out_bf16) a.out_bf16[p * a.bsp + q] = enc16(a.bf_scale * v, a.f16);
@@ -132,8 +131,8 @@ __global__ void __launch_bounds__(256) k_reduce(ReduceArgs a) {
     for (int z = 0; z < a.splits; ++z) {
         const float4 x = __ldg(reinterpret_cast<const float4 *>(base + z * zs));
         v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
-        if (a.H) {
-            const float4 y = __ldg(reinterpret_cast<const float4 *>(base + z * zs + a.H));
+        for (int t = 1; t < a.terms; ++t) {
+            const float4 y = __ldg(reinterpret_cast<const float4 *>(base + z * zs + t * a.H));
             v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
         }
     }
@@ -177,20 +176,20 @@ int launch_pool_split(const uint16_t *X, int64_t M, int64_t Din, int g, int64_t 
     return QLORA_OK;
 }
 
-int launch_split_f32(const float *src, int64_t rows, int r, int rp, uint16_t *dst, cudaStream_t st,
+int launch_split_f32(const float *src, int64_t rows, int r, int rp, int terms, uint16_t *dst, cudaStream_t st,
                      bool f16) {
     const int64_t n = rows * rp;
     if (n == 0) return QLORA_OK;
-    k_split_f32<<<blocks_for(n), 256, 0, st>>>(src, rows, r, rp, dst, f16);
+    k_split_f32<<<blocks_for(n), 256, 0, st>>>(src, rows, r, rp, terms, dst, f16);
     QLORA_LAUNCH_CHECK();
     return QLORA_OK;
 }
 
-int launch_reduce(const float *partial, int splits, int64_t P, int64_t Qp, int H, int Qv,
+int launch_reduce(const float *partial, int splits, int64_t P, int64_t Qp, int H, int terms, int Qv,
                   float f32_scale, float *out_f32, int64_t fsp, int64_t fsq, float bf_scale,
                   uint16_t *out_bf16, int64_t bsp, uint16_t *out_split, int64_t sp,
                   cudaStream_t st, bool f16) {
-    ReduceArgs a{partial, splits, P, Qp, H, Qv, f32_scale, out_f32, fsp, fsq,
+    ReduceArgs a{partial, splits, P, Qp, H, terms, Qv, f32_scale, out_f32, fsp, fsq,
                  bf_scale, out_bf16, bsp, out_split, sp, f16, Qv};
     if (P * Qv == 0) return QLORA_OK;
     if (out_bf16 && bsp > a.Qz) a.Qz = (int)bsp;

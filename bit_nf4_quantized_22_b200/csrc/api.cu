@@ -33,9 +33,9 @@ int launch_pad_rows(const uint16_t *src, int64_t rows, int r, int rp, int rep, f
                     uint16_t *dst, cudaStream_t st, bool f16);
 int launch_pool_split(const uint16_t *X, int64_t M, int64_t Din, int g, int64_t ld, uint16_t *hi,
                       uint16_t *lo, cudaStream_t st, bool f16);
-int launch_split_f32(const float *src, int64_t rows, int r, int rp, uint16_t *dst, cudaStream_t st,
+int launch_split_f32(const float *src, int64_t rows, int r, int rp, int terms, uint16_t *dst, cudaStream_t st,
                      bool f16);
-int launch_reduce(const float *partial, int splits, int64_t P, int64_t Qp, int H, int Qv,
+int launch_reduce(const float *partial, int splits, int64_t P, int64_t Qp, int H, int terms, int Qv,
                   float f32_scale, float *out_f32, int64_t fsp, int64_t fsq, float bf_scale,
                   uint16_t *out_bf16, int64_t bsp, uint16_t *out_split, int64_t sp, cudaStream_t st,
                   bool f16);
@@ -223,13 +223,13 @@ Prod prod_dA(const Dims &d, const uint16_t *X, const uint16_t *ph, const uint16_
     pr.Q = 2 * d.rp;
     return pr;
 }
-// dB^T-sum = dY^T . [T_hi | T_lo]
-Prod prod_dB(const Dims &d, const uint16_t *dY, const uint16_t *Tsplit) {
+// dB^T-sum = dY^T . [T_hi | T_lo]   (three terms of T from an 8-bit checkpoint)
+Prod prod_dB(const Dims &d, const uint16_t *dY, const uint16_t *Tsplit, int terms = 2) {
     Prod pr{};
-    pr.seg[0] = SkinnySeg{dY, d.Dout, 0, Tsplit, 2 * d.rp, 0, 2 * d.rp, d.M};
+    pr.seg[0] = SkinnySeg{dY, d.Dout, 0, Tsplit, terms * d.rp, 0, terms * d.rp, d.M};
     pr.nseg = 1;
     pr.P = d.Dout;
-    pr.Q = 2 * d.rp;
+    pr.Q = terms * d.rp;
     return pr;
 }
 
@@ -241,7 +241,7 @@ struct FwdWs {
 struct BwdWs {
     uint16_t *Apad, *ph, *pl, *sG, *Gsplit, *Tsplit, *Aext;
     float *G32, *Gpart, *T32, *Tpart, *dApart, *dBpart, *gemv_part;
-    // input in 8 bits, not pooled: the digits of s_m G's columns and of A's
+    // input in 8 bits: the digits of s_m G's columns and of A's
     int8_t *Gdig, *Adig;
     float *Gstep, *Astep;
 };
@@ -266,27 +266,30 @@ size_t layout_fwd(const Dims &d, bool have_tsave, void *base, FwdWs *w) {
     return b.off;
 }
 
-// x8: the layer's input is 8-bit rows; without pooling its products (dA, T)
-// are integer ones, which need digits instead of hi/lo halves and partials.
+// x8: the layer's input is 8-bit rows; its products (dA, T) are integer ones,
+// which need digits instead of hi/lo halves and partials.
+// Terms of the compute dtype that carry T in dB: two (16 bits in bf16, 22 in
+// fp16); three of bf16 from an 8-bit checkpoint, whose dA is good to 24 bits.
+int t_terms(const Dims &d, bool x8) { return x8 && !d.f16 ? 3 : 2; }
+
 size_t layout_bwd(const Dims &d, bool have_tsaved, bool want_dx, bool want_da, bool want_db, bool x8,
                   void *base, BwdWs *w) {
     Bump b(base);
     BwdWs x{};
-    const bool digits = x8 && d.g == 1;
     x.G32 = b.take<float>(d.M * d.r);
     x.Gpart = b.take<float>(prod_partial_floats(prod_G(d, 0, 0)));
-    if (want_da && !digits) x.Gsplit = b.take<uint16_t>(d.M * 2 * d.rp);
-    if (want_da && digits) {
+    if (want_da && !x8) x.Gsplit = b.take<uint16_t>(d.M * 2 * d.rp);
+    if (want_da && x8) {
         x.Gdig = b.take<int8_t>(3 * d.rp * round_up(d.M, 16));
         x.Gstep = b.take<float>(d.rp);
     }
-    if (d.g > 1 && (want_da || (want_db && !have_tsaved))) {
+    if (d.g > 1 && !x8 && (want_da || (want_db && !have_tsaved))) {
         x.ph = b.take<uint16_t>(d.M * d.Dap);
         x.pl = b.take<uint16_t>(d.M * d.Dap);
     }
     if (want_db) {
-        if (!have_tsaved && digits) {
-            x.Adig = b.take<int8_t>(3 * d.rp * round_up(d.Da, 16));
+        if (!have_tsaved && x8) {
+            x.Adig = b.take<int8_t>(3 * d.rp * d.Din);
             x.Astep = b.take<float>(d.rp);
             x.T32 = b.take<float>(d.M * d.r);
         } else if (!have_tsaved) {
@@ -294,10 +297,10 @@ size_t layout_bwd(const Dims &d, bool have_tsaved, bool want_dx, bool want_da, b
             x.T32 = b.take<float>(d.M * d.r);
             x.Tpart = b.take<float>(prod_partial_floats(prod_T(d, 0, 0, 0, 0)));
         }
-        x.Tsplit = b.take<uint16_t>(d.M * 2 * d.rp);
-        x.dBpart = b.take<float>(prod_partial_floats(prod_dB(d, 0, 0)));
+        x.Tsplit = b.take<uint16_t>(d.M * t_terms(d, x8) * d.rp);
+        x.dBpart = b.take<float>(prod_partial_floats(prod_dB(d, 0, 0, t_terms(d, x8))));
     }
-    if (want_da && !digits) x.dApart = b.take<float>(prod_partial_floats(prod_dA(d, 0, 0, 0, 0)));
+    if (want_da && !x8) x.dApart = b.take<float>(prod_partial_floats(prod_dA(d, 0, 0, 0, 0)));
     if (want_dx) {
         if (d.small) {
             x.gemv_part = b.take<float>(gemv_bwd_partial_bytes((int)d.M, d.Din, d.Dout) / 4 + 1);
@@ -348,7 +351,7 @@ int run_adapter_down(const Dims &d, const uint16_t *X, const uint16_t *A, uint16
     }
     ProdPlan plan;
     RC(run_prod(prod_T(d, X, Ause, ph, pl), Tpart, status, st, &plan, d.f16));
-    return launch_reduce(Tpart, plan.splits, d.M, plan.Qp, 0, d.r, 1.f, T32, d.r, 1, s, sT, d.rp64,
+    return launch_reduce(Tpart, plan.splits, d.M, plan.Qp, 0, 1, d.r, 1.f, T32, d.r, 1, s, sT, d.rp64,
                          nullptr, 0, st, d.f16);
 }
 
@@ -375,31 +378,31 @@ bool aligned_to(const void *p, int32_t dt) {
 }
 
 // dA = s u^T G from codes c and scales of the tokens: column j of (scale_m G[m][j]) in digits, then
-// dA[k][j] = s step_j sum_m c[m][k] digits.
+// dA[k][j] = s step_j sum_m c[m][k] digits.  Pooled: the sums of a group's 64 features, over 64.
 int run_dA_int8(const Dims &d, const int8_rows_t &x, const float *G, int8_t *dig, float *step, float s, float *dA,
                 uint32_t *status, cudaStream_t st) {
     const int64_t ld = round_up(d.M, 16);
-    RC(launch_int8_col_digits(G, QLORA_DTYPE_FP32, d.M, d.r, x.scales, dig, ld, d.rp, step, st));
+    RC(launch_int8_col_digits(G, QLORA_DTYPE_FP32, d.M, d.r, x.scales, dig, ld, d.rp, 1, step, st));
     Int8Product g{};
     g.a = x.codes, g.lda = x.ld, g.a_mn = 1;
     g.b = dig, g.ldb = ld, g.plane_rows = d.rp, g.planes = 3;
     g.P = d.Din, g.Q = d.r, g.R = d.M;
-    g.qscale = step, g.mul = s;
+    g.qscale = step, g.mul = s / (float)d.g, g.pool = d.g;
     g.out = dA, g.ldo = d.r, g.q_inner = 1, g.dtype = QLORA_DTYPE_FP32;
     return launch_int8_product(g, status, st);
 }
 
-// T[m][j] = scale_m step_j sum_k c[m][k] (digits of A's column j)
+// T[m][j] = scale_m step_j sum_k c[m][k] (digits of A's column j).  Pooled: every feature of a group
+// meets the group's row of A, over 64.
 int run_T_int8(const Dims &d, const int8_rows_t &x, const uint16_t *A, int8_t *dig, float *step, float *T,
                uint32_t *status, cudaStream_t st) {
-    const int64_t ld = round_up(d.Da, 16);
-    RC(launch_int8_col_digits(A, d.f16 ? QLORA_DTYPE_FP16 : QLORA_DTYPE_BF16, d.Da, d.r, nullptr, dig, ld, d.rp,
-                              step, st));
+    RC(launch_int8_col_digits(A, d.f16 ? QLORA_DTYPE_FP16 : QLORA_DTYPE_BF16, d.Da, d.r, nullptr, dig, d.Din, d.rp,
+                              d.g, step, st));
     Int8Product g{};
     g.a = x.codes, g.lda = x.ld;
-    g.b = dig, g.ldb = ld, g.plane_rows = d.rp, g.planes = 3;
+    g.b = dig, g.ldb = d.Din, g.plane_rows = d.rp, g.planes = 3;
     g.P = d.M, g.Q = d.r, g.R = d.Din;
-    g.qscale = step, g.pscale = x.scales, g.mul = 1.f;
+    g.qscale = step, g.pscale = x.scales, g.mul = 1.f / (float)d.g, g.pool = 1;
     g.out = T, g.ldo = d.r, g.q_inner = 1, g.dtype = QLORA_DTYPE_FP32;
     return launch_int8_product(g, status, st);
 }
@@ -579,11 +582,10 @@ static int backward_impl(const uint16_t *X, const int8_rows_t *X8, const uint16_
         ProdPlan pl;
         RC(run_prod(prod_G(d, dY, B), w.Gpart, d_status, st, &pl, d.f16));
         uint16_t *sG = (want_dx && !d.small) ? w.sG : nullptr;
-        RC(launch_reduce(w.Gpart, pl.splits, M, pl.Qp, 0, r, 1.f, w.G32, r, 1, s, sG, d.rp64,
+        RC(launch_reduce(w.Gpart, pl.splits, M, pl.Qp, 0, 1, r, 1.f, w.G32, r, 1, s, sG, d.rp64,
                          w.Gsplit, d.rp, st, d.f16));
     }
-    if (d.g > 1 && w.ph)
-        RC(X8 ? launch_int8_pool_split(*X8, d.Da, d.Dap, w.ph, w.pl, st, d.f16) : run_pool(d, X, w.ph, w.pl, st));
+    if (d.g > 1 && w.ph) RC(run_pool(d, X, w.ph, w.pl, st));
 
     // With the tensor-core dX GEMM, dA and dB go to the side stream (after
     // G): the GEMM is enqueued first, so its CTAs are placed first and the
@@ -619,30 +621,30 @@ static int backward_impl(const uint16_t *X, const int8_rows_t *X8, const uint16_
     }
     int rc = QLORA_OK;
     if (side && cudaStreamWaitEvent(side, ev_fork, 0) != cudaSuccess) rc = QLORA_ECUDA;
-    const bool digits = X8 && d.g == 1;
-    if (rc == QLORA_OK && want_da && digits) {
+    if (rc == QLORA_OK && want_da && X8) {
         rc = run_dA_int8(d, *X8, w.G32, w.Gdig, w.Gstep, s, dA, d_status, ast);
     } else if (rc == QLORA_OK && want_da) {
         ProdPlan pl;
         rc = run_prod(prod_dA(d, X, w.ph, w.pl, w.Gsplit), w.dApart, d_status, ast, &pl, d.f16);
         if (rc == QLORA_OK)
-            rc = launch_reduce(w.dApart, pl.splits, d.Da, pl.Qp, d.rp, r, s, dA, r, 1, 0.f, nullptr,
+            rc = launch_reduce(w.dApart, pl.splits, d.Da, pl.Qp, d.rp, 2, r, s, dA, r, 1, 0.f, nullptr,
                                0, nullptr, 0, ast, d.f16);
     }
     if (rc == QLORA_OK && want_db) {
         const float *T32 = T_saved;
         if (!T32) {
-            rc = digits ? run_T_int8(d, *X8, A, w.Adig, w.Astep, w.T32, d_status, ast)
-                        : run_adapter_down(d, X, A, w.Apad, w.ph, w.pl, w.Tpart, w.T32, s, nullptr,
-                                           d_status, ast);
+            rc = X8 ? run_T_int8(d, *X8, A, w.Adig, w.Astep, w.T32, d_status, ast)
+                    : run_adapter_down(d, X, A, w.Apad, w.ph, w.pl, w.Tpart, w.T32, s, nullptr, d_status,
+                                       ast);
             T32 = w.T32;
         }
-        if (rc == QLORA_OK) rc = launch_split_f32(T32, M, r, d.rp, w.Tsplit, ast, d.f16);
+        const int terms = t_terms(d, X8 != nullptr);
+        if (rc == QLORA_OK) rc = launch_split_f32(T32, M, r, d.rp, terms, w.Tsplit, ast, d.f16);
         ProdPlan pl;
         if (rc == QLORA_OK)
-            rc = run_prod(prod_dB(d, dY, w.Tsplit), w.dBpart, d_status, ast, &pl, d.f16);
+            rc = run_prod(prod_dB(d, dY, w.Tsplit, terms), w.dBpart, d_status, ast, &pl, d.f16);
         if (rc == QLORA_OK)
-            rc = launch_reduce(w.dBpart, pl.splits, d.Dout, pl.Qp, d.rp, r, s, dB, 1, d.Dout, 0.f,
+            rc = launch_reduce(w.dBpart, pl.splits, d.Dout, pl.Qp, d.rp, terms, r, s, dB, 1, d.Dout, 0.f,
                                nullptr, 0, nullptr, 0, ast, d.f16);
     }
     if (side) {

@@ -108,6 +108,7 @@ struct TallParams {
     void *out;
     int64_t ldo;
     int q_inner;           // out[p * ldo + q], else out[q * ldo + p]
+    int pool;              // q_inner: the 64 rows of each group summed
     int dtype, vec;
     int pdl;               // B and the scales come from the kernel before (programmatic launch)
     uint32_t *status;
@@ -294,6 +295,14 @@ k_int8_tall(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
                     t = column(d, c);
                     sum[0] = sum[0] * 256 + t.x, sum[1] = sum[1] * 256 + t.y;
                     sum[2] = sum[2] * 256 + t.z, sum[3] = sum[3] * 256 + t.w;
+                }
+                if (p.pool == 64) {
+                    int64_t all = sum[0] + sum[1] + sum[2] + sum[3];
+#pragma unroll
+                    for (int x = 8; x > 0; x /= 2) all += __shfl_xor_sync(0xffffffffu, all, x);
+                    if ((lane & 15) == 0 && prow < p.P)
+                        static_cast<float *>(p.out)[prow / 64 * p.ldo + q] = __fmul_rn(__ll2float_rn(all), qs[c]);
+                    continue;
                 }
 #pragma unroll
                 for (int e = 0; e < 4; ++e) v[e] = __ll2float_rn(sum[e]);
@@ -717,6 +726,7 @@ static int launch_int8_tall(const Int8Product &g, uint32_t *d_status, cudaStream
     p.out = g.out;
     p.ldo = g.ldo;
     p.q_inner = g.q_inner;
+    p.pool = g.pool;
     p.dtype = g.dtype;
     const int esize = g.dtype == QLORA_DTYPE_FP32 ? 4 : 2;
     p.vec = g.ldo % 4 == 0 && (reinterpret_cast<uintptr_t>(g.out) & (4 * esize - 1)) == 0;

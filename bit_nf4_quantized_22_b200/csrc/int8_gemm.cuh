@@ -21,6 +21,7 @@ struct Int8Product {
     void *out;             // q_inner: out[p * ldo + q] (fp32), else out[q * ldo + p]
     int64_t ldo;
     int q_inner;
+    int pool;              // q_inner: 64 sums the rows p of each run of 64 (out has P / 64 rows), else 1 or 0
     int dtype;             // QLORA_DTYPE_*
     int pdl;               // launch beside the kernel before, which writes B and the scales but not A
 };
@@ -44,9 +45,7 @@ int launch_int8_quantize(const void *X, int dtype, int64_t ldx, const int8_rows_
 int launch_int8_row_digits(const uint16_t *Y, bool f16, int64_t rows, int64_t cols, const float *cscale,
                            int8_t *planes, int64_t ld, float *steps, cudaStream_t st);
 int launch_int8_col_digits(const void *S, int dtype, int64_t R, int r, const float *f, int8_t *planes, int64_t ld,
-                           int rp, float *steps, cudaStream_t st);
-int launch_int8_pool_split(const int8_rows_t &q, int64_t Da, int64_t ld, uint16_t *hi, uint16_t *lo,
-                           cudaStream_t st, bool f16);
+                           int rp, int rep, float *steps, cudaStream_t st);
 int launch_int8_dequantize(const int8_rows_t &q, int dtype, void *out, cudaStream_t st);
 
 }  // namespace qlora

@@ -223,6 +223,7 @@ k_int8_row_digits(const void *Y, int64_t rows, int cols, const float *__restrict
 // times f[t], in 24-bit fixed point with one step per column, as three digit
 // planes transposed to planes[d][j][t] (rows of ld bytes, rp rows a plane).
 // A step is max / 8355711: half of it is 6e-8 of the column's largest value.
+// rep = 64 writes each row's digits 64 times over (t -> 64 t .. 64 t + 63).
 // A cluster of 8 CTAs shares 8 columns: each finds the maxima of its rows,
 // keeping the values in shared memory (up to kColKeep rows; past them they are
 // read again), and the cluster joins the maxima over distributed shared memory.
@@ -233,7 +234,7 @@ constexpr float kColMax = 8355711.f;   // 127 * (65536 + 256 + 1)
 template <int DT>
 __global__ void __cluster_dims__(1, kColCluster, 1) __launch_bounds__(kColThreads)
 k_int8_col_digits(const void *S, int64_t R, int r, const float *__restrict__ f, int64_t per,
-                  int8_t *planes, int64_t ld, int rp, float *steps) {
+                  int8_t *planes, int64_t ld, int rp, int rep, float *steps) {
     namespace cg = cooperative_groups;
     __shared__ uint32_t cmax[kColStrip];
     __shared__ float tile[kColStrip][kColKeep + 1];
@@ -318,39 +319,20 @@ k_int8_col_digits(const void *S, int64_t R, int r, const float *__restrict__ f, 
                 d[2][e / 4] |= (uint32_t)(uint8_t)b0 << (8 * (e & 3));
             }
 #pragma unroll
-            for (int p = 0; p < 3; ++p)
-                *reinterpret_cast<uint2 *>(planes + ((int64_t)p * rp + j0 + jc) * ld + tb + k) =
-                    make_uint2(d[p][0], d[p][1]);
+            for (int p = 0; p < 3; ++p) {
+                int8_t *row = planes + ((int64_t)p * rp + j0 + jc) * ld;
+                if (rep == 1) {
+                    *reinterpret_cast<uint2 *>(row + tb + k) = make_uint2(d[p][0], d[p][1]);
+                    continue;
+                }
+                for (int e = 0; e < 8 && tb + k + e < t1; ++e) {
+                    const uint32_t b = ((d[p][e / 4] >> (8 * (e & 3))) & 255u) * 0x01010101u;
+                    for (int i = 0; i < 4; ++i)
+                        reinterpret_cast<uint4 *>(row + (tb + k + e) * 64)[i] = make_uint4(b, b, b, b);
+                }
+            }
         }
     }
-}
-
-// Pooled checkpoint: u[m][k'] = s[m] * (sum of 64 codes) / 64 as hi/lo terms of
-// the compute dtype into [M][ld] buffers (columns past Da are zero).  The sum
-// of codes is exact (at most 14 bits); the product is rounded once in fp32.
-__global__ void k_int8_pool_split(const int8_t *__restrict__ codes, int64_t cld, const float *__restrict__ scales,
-                                  int64_t M, int64_t Da, int64_t ld, uint16_t *__restrict__ hi,
-                                  uint16_t *__restrict__ lo, bool f16) {
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= M * ld) return;
-    const int64_t m = i / ld, k = i % ld;
-    float v = 0.f;
-    if (k < Da) {
-        const uint4 *p = reinterpret_cast<const uint4 *>(codes + m * cld + k * 64);
-        int sum = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint4 w = __ldg(p + e);
-            sum = __dp4a((int)w.x, 0x01010101, sum);
-            sum = __dp4a((int)w.y, 0x01010101, sum);
-            sum = __dp4a((int)w.z, 0x01010101, sum);
-            sum = __dp4a((int)w.w, 0x01010101, sum);
-        }
-        v = __fmul_rn((float)sum * 0.015625f, __ldg(scales + m));
-    }
-    const uint16_t h = enc16(v, f16);
-    hi[i] = h;
-    lo[i] = enc16(v - dec16(h, f16), f16);
 }
 
 // out[m][k] = RN_dt(code * s): 8 values a thread.
@@ -470,25 +452,15 @@ int launch_int8_row_digits(const uint16_t *Y, bool f16, int64_t rows, int64_t co
 }
 
 int launch_int8_col_digits(const void *S, int dtype, int64_t R, int r, const float *f, int8_t *planes, int64_t ld,
-                           int rp, float *steps, cudaStream_t st) {
+                           int rp, int rep, float *steps, cudaStream_t st) {
     const int64_t per = ((R + kColCluster - 1) / kColCluster + 15) / 16 * 16;
     const dim3 grid((unsigned)((rp + kColStrip - 1) / kColStrip), kColCluster);
     if (dtype == QLORA_DTYPE_FP32)
-        k_int8_col_digits<QLORA_DTYPE_FP32><<<grid, kColThreads, 0, st>>>(S, R, r, f, per, planes, ld, rp, steps);
+        k_int8_col_digits<QLORA_DTYPE_FP32><<<grid, kColThreads, 0, st>>>(S, R, r, f, per, planes, ld, rp, rep, steps);
     else if (dtype == QLORA_DTYPE_FP16)
-        k_int8_col_digits<QLORA_DTYPE_FP16><<<grid, kColThreads, 0, st>>>(S, R, r, f, per, planes, ld, rp, steps);
+        k_int8_col_digits<QLORA_DTYPE_FP16><<<grid, kColThreads, 0, st>>>(S, R, r, f, per, planes, ld, rp, rep, steps);
     else
-        k_int8_col_digits<QLORA_DTYPE_BF16><<<grid, kColThreads, 0, st>>>(S, R, r, f, per, planes, ld, rp, steps);
-    QLORA_LAUNCH_CHECK();
-    return QLORA_OK;
-}
-
-int launch_int8_pool_split(const int8_rows_t &q, int64_t Da, int64_t ld, uint16_t *hi, uint16_t *lo,
-                           cudaStream_t st, bool f16) {
-    const int64_t n = q.rows * ld;
-    if (n == 0) return QLORA_OK;
-    k_int8_pool_split<<<(unsigned)((n + 255) / 256), 256, 0, st>>>(q.codes, q.ld, q.scales, q.rows, Da, ld, hi, lo,
-                                                                   f16);
+        k_int8_col_digits<QLORA_DTYPE_BF16><<<grid, kColThreads, 0, st>>>(S, R, r, f, per, planes, ld, rp, rep, steps);
     QLORA_LAUNCH_CHECK();
     return QLORA_OK;
 }

@@ -353,44 +353,44 @@ def layer_case(qlib, M, K, N, r, g, dtype, seed=0):
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
 @pytest.mark.parametrize("M,K,N,r,g", [(1, 64, 8, 1, 1), (5, 192, 200, 8, 1), (16, 256, 296, 16, 1), (17, 320, 72, 3, 1),
                                        (100, 1024, 264, 64, 1), (129, 128, 1000, 85, 1), (300, 704, 520, 256, 1),
-                                       (1000, 2048, 200, 24, 1), (33, 512, 136, 8, 64), (260, 4096, 88, 40, 64)])
+                                       (1000, 2048, 200, 24, 1), (33, 512, 136, 8, 64), (260, 4096, 88, 40, 64),
+                                       (2, 64, 8, 1, 64), (90, 192, 64, 256, 64), (700, 9024, 264, 17, 64)])
 def test_checkpoint_backward(qlib, M, K, N, r, g, dtype):
-    """dX and dB (with T saved) are qlora_backward's to the bit; dA and a recomputed T read the 8-bit
-    input.  Bounds: G's fp32 accumulation (N terms, 2^-23 each, of the sum of magnitudes); 0.51 of the
-    24-bit step of G's column (over a token's scale) or hi/lo terms good to 2^-16; fp32 roundings."""
+    """dX is qlora_backward's to the bit; dA, dB and a recomputed T against the formulas of the 8-bit
+    input.  Bounds: G's fp32 accumulation (N terms, 2^-23 each, of the sum of magnitudes), 0.51 of the
+    24-bit step of G's column (over a token's scale), fp32 roundings; in dB, T's terms (three of bf16,
+    two of fp16: 2^-22, or an fp16 subnormal's 2^-25) and the M fp32 terms of its sums."""
     alpha = 16.0
     w, x, A, B, dy = layer_case(qlib, M, K, N, r, g, dtype)
     x8 = qlib.int8_quantize(x)
     _, T = qlib.forward(x, w, A, B, alpha, g)
     status = torch.zeros(1, dtype=torch.int32, device="cuda")
-    dx0, _, db0 = qlib.backward(x, dy, w, A, B, alpha, g, T=T)
+    dx0, _, _ = qlib.backward(x, dy, w, A, B, alpha, g, T=T)
     dx, da, db = qlib.backward(x8, dy, w, A, B, alpha, g, T=T, status=status)
     assert int(status.item()) == 0
-    assert torch.equal(dx, dx0) and torch.equal(db, db0)
-    xh = x8.codes.double() * x8.scales.double()[:, None]
-    p = xh.reshape(M, K // g, g).mean(2)
+    assert torch.equal(dx, dx0)
+    pool = lambda z: z.reshape(M, K // g, g).mean(2)   # noqa: E731
+    xs = x8.scales.double()[:, None]
+    xh = x8.codes.double() * xs
+    p, pabs, pcodes = pool(xh), pool(xh.abs()), pool(x8.codes.double().abs())
     s = alpha / r
     G, Gabs = dy.double() @ B.double().t(), dy.double().abs() @ B.double().abs().t()
     want = s * p.t() @ G
-    eG = N * 2.0 ** -23 * Gabs
-    if g == 1:
-        D = x8.scales.double()[:, None] * G
-        step = (D.abs() + x8.scales.double()[:, None] * eG).amax(0, keepdim=True) / 8355711
-        tol = s * (p.abs().t() @ (eG + 2.0 ** -23 * G.abs()) + 0.51 * step * x8.codes.double().abs().sum(0)[:, None])
-    else:   # hi/lo of the pooled input and of G (2^-16 each), M terms in fp32
-        tol = s * (p.abs().t() @ (eG + (2.0 ** -15 + M * 2.0 ** -23) * G.abs()))
-    tol = tol + 2.0 ** -22 * want.abs() + 1e-30
+    eG = N * 2.0 ** -23 * Gabs + 2.0 ** -23 * G.abs()
+    step = (xs * (G.abs() + eG)).amax(0, keepdim=True) / 8355711
+    tol = s * (pabs.t() @ eG + 0.51 * step * pcodes.sum(0)[:, None]) + 2.0 ** -22 * want.abs() + 1e-30
     assert ((da.double() - want).abs() <= tol).all()
-    # T from the checkpoint
+
+    def check_db(db, T, eT):
+        wantB = s * T.t() @ dy.double()
+        eT = eT + (2.0 ** -22 + M * 2.0 ** -23) * T.abs() + (2.0 ** -25 if dtype == "fp16" else 0)
+        assert ((db.double() - wantB).abs() <= s * eT.t() @ dy.double().abs() + 2.0 ** -22 * wantB.abs() + 1e-30).all()
+
+    check_db(db, T.double(), 0)
+    # T from the checkpoint: exact sums of the codes with A's columns in 24 bits, and fp32 roundings
     _, _, db2 = qlib.backward(x8, dy, w, A, B, alpha, g, need_dx=False, need_dA=False)
-    Th, Tabs = p @ A.double(), p.abs() @ A.double().abs()
-    wantB = s * Th.t() @ dy.double()
-    # T: 0.51 of A's column step times the codes (or 2^-16 hi/lo), fp32 roundings; then T's own hi/lo
-    # terms (2^-16) and M fp32 terms
-    eT = 0.51 * A.double().abs().amax(0) / 8355711 * xh.abs().sum(1, keepdim=True) if g == 1 else \
-        (2.0 ** -16 + K // g * 2.0 ** -23) * Tabs
-    eT = eT + 2.0 ** -22 * Th.abs() + (2.0 ** -16 + M * 2.0 ** -23) * Tabs
-    assert ((db2.double() - wantB).abs() <= s * eT.t() @ dy.double().abs() + 1e-30).all()
+    Th = p @ A.double()
+    check_db(db2, Th, 0.51 * A.double().abs().amax(0) / 8355711 * pabs.sum(1, keepdim=True) + 2.0 ** -22 * Th.abs())
 
 
 def test_checkpoint_gradient_against_differences(qlib):
