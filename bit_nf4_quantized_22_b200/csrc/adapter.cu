@@ -50,24 +50,27 @@ __global__ void k_pool_split(const uint16_t *__restrict__ X, int64_t M, int64_t 
     lo[i] = enc16(v - dec16(h, f16), f16);
 }
 
-// fp32 [rows][r] -> compute dtype [rows][terms rp] = [hi | lo] (terms = 3: and
-// what is left of them, 24 bits in bf16) with zero padding
-__global__ void k_split_f32(const float *__restrict__ src, int64_t rows, int r, int rp, int terms,
+// fp32 [rows][r] -> the compute dtype's terms of it: v = t0 + t1 (+ t2), each the
+// rounding of what the ones before leave (two: 16 bits in bf16, 22 in fp16;
+// three of bf16: 24).  Columns in groups of gw, a group's terms one after
+// another, zero padding up to W = groups * gw columns: dst [rows][terms * W].
+__global__ void k_split_f32(const float *__restrict__ src, int64_t rows, int r, int W, int gw, int terms,
                             uint16_t *__restrict__ dst, bool f16) {
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= rows * rp) return;
-    const int64_t row = i / rp;
-    const int j = (int)(i % rp);
+    if (i >= rows * W) return;
+    const int64_t row = i / W;
+    const int j = (int)(i % W);
     float v = j < r ? src[row * r + j] : 0.f;
     for (int t = 0; t < terms; ++t) {
         const uint16_t h = enc16(v, f16);
-        dst[(row * terms + t) * rp + j] = h;
+        dst[row * terms * W + (int64_t)(j / gw) * terms * gw + t * gw + j % gw] = h;
         v -= dec16(h, f16);
     }
 }
 
 // Deterministic split-K reduce (fixed summation order) with the adapter
-// epilogues.  v(p,q) = sum_z sum_{t < terms} partial[z][p][q + t H] for q < Qv:
+// epilogues.  v(p,q) = sum_z partial[z][p][q] (+ partial[z][p][q+H] when H>0),
+// for q < Qv:
 //   out_f32[p*fsp + q*fsq]  = f32_scale * v
 //   out_bf16[p*bsp + q]     = RN_bf16(bf_scale * v)          (row stride bsp)
 //   out_split[p*2*sp + q], [p*2*sp + sp + q] = hi/lo of v    (row stride 2 sp)
@@ -76,7 +79,7 @@ struct ReduceArgs {
     const float *partial;
     int splits;
     int64_t P, Qp;        // partial layout [splits][P][Qp]
-    int H, terms;         // offset from one term of the split operand to the next
+    int H;                // 0, or the offset of the second half to add
     int Qv;               // valid output columns
     float f32_scale; float *out_f32; int64_t fsp, fsq;
     float bf_scale; uint16_t *out_bf16; int64_t bsp;
@@ -101,7 +104,7 @@ __global__ void k_reduce_scalar(ReduceArgs a) {
     for (int z = 0; z < a.splits; ++z) {
         const float *base = a.partial + ((int64_t)z * a.P + p) * a.Qp;
         v += base[q];
-        for (int t = 1; t < a.terms; ++t) v += base[q + t * a.H];
+        if (a.H) v += base[q + a.H];
     }
     if (a.out_f32) a.out_f32[p * a.fsp + q * a.fsq] = a.f32_scale * v;
     if (a.out_bf16) a.out_bf16[p * a.bsp + q] = enc16(a.bf_scale * v, a.f16);
@@ -131,8 +134,8 @@ __global__ void __launch_bounds__(256) k_reduce(ReduceArgs a) {
     for (int z = 0; z < a.splits; ++z) {
         const float4 x = __ldg(reinterpret_cast<const float4 *>(base + z * zs));
         v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
-        for (int t = 1; t < a.terms; ++t) {
-            const float4 y = __ldg(reinterpret_cast<const float4 *>(base + z * zs + t * a.H));
+        if (a.H) {
+            const float4 y = __ldg(reinterpret_cast<const float4 *>(base + z * zs + a.H));
             v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
         }
     }
@@ -176,20 +179,20 @@ int launch_pool_split(const uint16_t *X, int64_t M, int64_t Din, int g, int64_t 
     return QLORA_OK;
 }
 
-int launch_split_f32(const float *src, int64_t rows, int r, int rp, int terms, uint16_t *dst, cudaStream_t st,
+int launch_split_f32(const float *src, int64_t rows, int r, int W, int gw, int terms, uint16_t *dst, cudaStream_t st,
                      bool f16) {
-    const int64_t n = rows * rp;
+    const int64_t n = rows * W;
     if (n == 0) return QLORA_OK;
-    k_split_f32<<<blocks_for(n), 256, 0, st>>>(src, rows, r, rp, terms, dst, f16);
+    k_split_f32<<<blocks_for(n), 256, 0, st>>>(src, rows, r, W, gw, terms, dst, f16);
     QLORA_LAUNCH_CHECK();
     return QLORA_OK;
 }
 
-int launch_reduce(const float *partial, int splits, int64_t P, int64_t Qp, int H, int terms, int Qv,
+int launch_reduce(const float *partial, int splits, int64_t P, int64_t Qp, int H, int Qv,
                   float f32_scale, float *out_f32, int64_t fsp, int64_t fsq, float bf_scale,
                   uint16_t *out_bf16, int64_t bsp, uint16_t *out_split, int64_t sp,
                   cudaStream_t st, bool f16) {
-    ReduceArgs a{partial, splits, P, Qp, H, terms, Qv, f32_scale, out_f32, fsp, fsq,
+    ReduceArgs a{partial, splits, P, Qp, H, Qv, f32_scale, out_f32, fsp, fsq,
                  bf_scale, out_bf16, bsp, out_split, sp, f16, Qv};
     if (P * Qv == 0) return QLORA_OK;
     if (out_bf16 && bsp > a.Qz) a.Qz = (int)bsp;

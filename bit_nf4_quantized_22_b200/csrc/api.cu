@@ -33,9 +33,9 @@ int launch_pad_rows(const uint16_t *src, int64_t rows, int r, int rp, int rep, f
                     uint16_t *dst, cudaStream_t st, bool f16);
 int launch_pool_split(const uint16_t *X, int64_t M, int64_t Din, int g, int64_t ld, uint16_t *hi,
                       uint16_t *lo, cudaStream_t st, bool f16);
-int launch_split_f32(const float *src, int64_t rows, int r, int rp, int terms, uint16_t *dst, cudaStream_t st,
+int launch_split_f32(const float *src, int64_t rows, int r, int W, int gw, int terms, uint16_t *dst, cudaStream_t st,
                      bool f16);
-int launch_reduce(const float *partial, int splits, int64_t P, int64_t Qp, int H, int terms, int Qv,
+int launch_reduce(const float *partial, int splits, int64_t P, int64_t Qp, int H, int Qv,
                   float f32_scale, float *out_f32, int64_t fsp, int64_t fsq, float bf_scale,
                   uint16_t *out_bf16, int64_t bsp, uint16_t *out_split, int64_t sp, cudaStream_t st,
                   bool f16);
@@ -50,9 +50,12 @@ struct SkinnySeg {
     int64_t qext;
     int64_t R;
 };
+struct SkinnyFold {
+    int terms = 1, gw = 0, groups = 0, most = 0;
+};
 int skinny_k_tiles(const SkinnySeg *segs, int nseg);
-void skinny_splits(int64_t P, int64_t Q, int nk, int *splits, int *per);
-int launch_umma_skinny(const SkinnySeg *segs, int nseg, int64_t P, int64_t Q, int64_t Qp,
+void skinny_splits(int64_t P, int64_t Q, int nk, const SkinnyFold &f, int *splits, int *per);
+int launch_umma_skinny(const SkinnySeg *segs, int nseg, int64_t P, int64_t Q, int64_t Qp, const SkinnyFold &f,
                        float *partial, uint32_t *d_status, cudaStream_t st, bool f16);
 // umma_gemm.cu
 int launch_umma_qgemm(int mode, const uint16_t *X, int64_t M, const nf4_weight_t &q,
@@ -157,6 +160,7 @@ struct Prod {
     SkinnySeg seg[2];
     int nseg;
     int64_t P, Q;
+    SkinnyFold fold;
 };
 struct ProdPlan {
     int splits;
@@ -166,7 +170,7 @@ struct ProdPlan {
 ProdPlan plan_prod(const Prod &pr) {
     ProdPlan pl;
     int per = 1;
-    skinny_splits(pr.P, pr.Q, skinny_k_tiles(pr.seg, pr.nseg), &pl.splits, &per);
+    skinny_splits(pr.P, pr.Q, skinny_k_tiles(pr.seg, pr.nseg), pr.fold, &pl.splits, &per);
     pl.Qp = round_up(pr.Q, 4);
     return pl;
 }
@@ -179,7 +183,7 @@ size_t prod_partial_floats(const Prod &pr) {
 int run_prod(const Prod &pr, float *partial, uint32_t *status, cudaStream_t st, ProdPlan *plan,
              bool f16) {
     *plan = plan_prod(pr);
-    return launch_umma_skinny(pr.seg, pr.nseg, pr.P, pr.Q, plan->Qp, partial, status, st, f16);
+    return launch_umma_skinny(pr.seg, pr.nseg, pr.P, pr.Q, plan->Qp, pr.fold, partial, status, st, f16);
 }
 
 // T = u . A    (u = x [M, Din], or pooled hi/lo [M, Dap]; A padded [Da, rp])
@@ -198,13 +202,31 @@ Prod prod_T(const Dims &d, const uint16_t *X, const uint16_t *Apad, const uint16
     pr.Q = d.r;
     return pr;
 }
+// The backward from an 8-bit checkpoint gives its fp32 gradients to about 24
+// bits: at most 12 k-tiles (48 MMA steps) in an accumulator that rounds toward
+// zero, an error of 7e-7 (with the splits alone, 22 k-tiles at M = 4096, Dout =
+// 11008: 1.4e-6; 112 at M = 8192, Dout = 28672: 9e-6).  G and dB both have the
+// bound; ranks past 64, too wide for the epilogue's registers, in G by splits.
+constexpr int kInt8Most = 12;
+
+SkinnyFold fold_columns(int rp, int terms) {
+    SkinnyFold f;
+    f.terms = terms;
+    f.gw = rp < 64 ? rp : 64;
+    f.groups = (rp + f.gw - 1) / f.gw;
+    f.most = kInt8Most;
+    return f;
+}
+
 // G = dY . B^T   (B [r, Dout] is K-major for this product)
-Prod prod_G(const Dims &d, const uint16_t *dY, const uint16_t *B) {
+Prod prod_G(const Dims &d, const uint16_t *dY, const uint16_t *B, bool x8 = false) {
     Prod pr{};
+    if (x8 && d.rp <= 64) pr.fold = fold_columns(d.rp, 1);
+    else if (x8) pr.fold.most = kInt8Most;
     pr.seg[0] = SkinnySeg{dY, d.Dout, 1, B, d.Dout, 1, d.r, d.Dout};
     pr.nseg = 1;
     pr.P = d.M;
-    pr.Q = d.r;
+    pr.Q = pr.fold.gw ? d.rp : d.r;
     return pr;
 }
 // dA-sum = u^T . [G_hi | G_lo]   (reduction over tokens; both MN-major)
@@ -223,13 +245,25 @@ Prod prod_dA(const Dims &d, const uint16_t *X, const uint16_t *ph, const uint16_
     pr.Q = 2 * d.rp;
     return pr;
 }
-// dB^T-sum = dY^T . [T_hi | T_lo]   (three terms of T from an 8-bit checkpoint)
-Prod prod_dB(const Dims &d, const uint16_t *dY, const uint16_t *Tsplit, int terms = 2) {
+// dB^T-sum = dY^T . [T_hi | T_lo]
+Prod prod_dB(const Dims &d, const uint16_t *dY, const uint16_t *Tsplit) {
     Prod pr{};
-    pr.seg[0] = SkinnySeg{dY, d.Dout, 0, Tsplit, terms * d.rp, 0, terms * d.rp, d.M};
+    pr.seg[0] = SkinnySeg{dY, d.Dout, 0, Tsplit, 2 * d.rp, 0, 2 * d.rp, d.M};
     pr.nseg = 1;
     pr.P = d.Dout;
-    pr.Q = terms * d.rp;
+    pr.Q = 2 * d.rp;
+    return pr;
+}
+// The same from an 8-bit checkpoint: the terms of T (three of bf16, two of
+// fp16) in groups of up to 64 columns, their products added in the kernel.
+Prod prod_dB8(const Dims &d, const uint16_t *dY, const uint16_t *Tsplit) {
+    Prod pr{};
+    pr.fold = fold_columns(d.rp, d.f16 ? 2 : 3);
+    const int W = pr.fold.groups * pr.fold.gw, cols = pr.fold.terms * W;
+    pr.seg[0] = SkinnySeg{dY, d.Dout, 0, Tsplit, cols, 0, cols, d.M};
+    pr.nseg = 1;
+    pr.P = d.Dout;
+    pr.Q = W;
     return pr;
 }
 
@@ -268,16 +302,12 @@ size_t layout_fwd(const Dims &d, bool have_tsave, void *base, FwdWs *w) {
 
 // x8: the layer's input is 8-bit rows; its products (dA, T) are integer ones,
 // which need digits instead of hi/lo halves and partials.
-// Terms of the compute dtype that carry T in dB: two (16 bits in bf16, 22 in
-// fp16); three of bf16 from an 8-bit checkpoint, whose dA is good to 24 bits.
-int t_terms(const Dims &d, bool x8) { return x8 && !d.f16 ? 3 : 2; }
-
 size_t layout_bwd(const Dims &d, bool have_tsaved, bool want_dx, bool want_da, bool want_db, bool x8,
                   void *base, BwdWs *w) {
     Bump b(base);
     BwdWs x{};
     x.G32 = b.take<float>(d.M * d.r);
-    x.Gpart = b.take<float>(prod_partial_floats(prod_G(d, 0, 0)));
+    x.Gpart = b.take<float>(prod_partial_floats(prod_G(d, 0, 0, x8)));
     if (want_da && !x8) x.Gsplit = b.take<uint16_t>(d.M * 2 * d.rp);
     if (want_da && x8) {
         x.Gdig = b.take<int8_t>(3 * d.rp * round_up(d.M, 16));
@@ -297,8 +327,9 @@ size_t layout_bwd(const Dims &d, bool have_tsaved, bool want_dx, bool want_da, b
             x.T32 = b.take<float>(d.M * d.r);
             x.Tpart = b.take<float>(prod_partial_floats(prod_T(d, 0, 0, 0, 0)));
         }
-        x.Tsplit = b.take<uint16_t>(d.M * t_terms(d, x8) * d.rp);
-        x.dBpart = b.take<float>(prod_partial_floats(prod_dB(d, 0, 0, t_terms(d, x8))));
+        const Prod pr = x8 ? prod_dB8(d, 0, 0) : prod_dB(d, 0, 0);
+        x.Tsplit = b.take<uint16_t>(d.M * pr.seg[0].ldb);
+        x.dBpart = b.take<float>(prod_partial_floats(pr));
     }
     if (want_da && !x8) x.dApart = b.take<float>(prod_partial_floats(prod_dA(d, 0, 0, 0, 0)));
     if (want_dx) {
@@ -351,7 +382,7 @@ int run_adapter_down(const Dims &d, const uint16_t *X, const uint16_t *A, uint16
     }
     ProdPlan plan;
     RC(run_prod(prod_T(d, X, Ause, ph, pl), Tpart, status, st, &plan, d.f16));
-    return launch_reduce(Tpart, plan.splits, d.M, plan.Qp, 0, 1, d.r, 1.f, T32, d.r, 1, s, sT, d.rp64,
+    return launch_reduce(Tpart, plan.splits, d.M, plan.Qp, 0, d.r, 1.f, T32, d.r, 1, s, sT, d.rp64,
                          nullptr, 0, st, d.f16);
 }
 
@@ -580,9 +611,9 @@ static int backward_impl(const uint16_t *X, const int8_rows_t *X8, const uint16_
     // G = dY . B^T  (fp32), s*G (compute dtype, large M), hi/lo split (for dA)
     {
         ProdPlan pl;
-        RC(run_prod(prod_G(d, dY, B), w.Gpart, d_status, st, &pl, d.f16));
+        RC(run_prod(prod_G(d, dY, B, X8 != nullptr), w.Gpart, d_status, st, &pl, d.f16));
         uint16_t *sG = (want_dx && !d.small) ? w.sG : nullptr;
-        RC(launch_reduce(w.Gpart, pl.splits, M, pl.Qp, 0, 1, r, 1.f, w.G32, r, 1, s, sG, d.rp64,
+        RC(launch_reduce(w.Gpart, pl.splits, M, pl.Qp, 0, r, 1.f, w.G32, r, 1, s, sG, d.rp64,
                          w.Gsplit, d.rp, st, d.f16));
     }
     if (d.g > 1 && w.ph) RC(run_pool(d, X, w.ph, w.pl, st));
@@ -627,7 +658,7 @@ static int backward_impl(const uint16_t *X, const int8_rows_t *X8, const uint16_
         ProdPlan pl;
         rc = run_prod(prod_dA(d, X, w.ph, w.pl, w.Gsplit), w.dApart, d_status, ast, &pl, d.f16);
         if (rc == QLORA_OK)
-            rc = launch_reduce(w.dApart, pl.splits, d.Da, pl.Qp, d.rp, 2, r, s, dA, r, 1, 0.f, nullptr,
+            rc = launch_reduce(w.dApart, pl.splits, d.Da, pl.Qp, d.rp, r, s, dA, r, 1, 0.f, nullptr,
                                0, nullptr, 0, ast, d.f16);
     }
     if (rc == QLORA_OK && want_db) {
@@ -638,13 +669,14 @@ static int backward_impl(const uint16_t *X, const int8_rows_t *X8, const uint16_
                                        ast);
             T32 = w.T32;
         }
-        const int terms = t_terms(d, X8 != nullptr);
-        if (rc == QLORA_OK) rc = launch_split_f32(T32, M, r, d.rp, terms, w.Tsplit, ast, d.f16);
+        const Prod pr = X8 ? prod_dB8(d, dY, w.Tsplit) : prod_dB(d, dY, w.Tsplit);
+        if (rc == QLORA_OK)
+            rc = X8 ? launch_split_f32(T32, M, r, (int)pr.Q, pr.fold.gw, pr.fold.terms, w.Tsplit, ast, d.f16)
+                    : launch_split_f32(T32, M, r, d.rp, d.rp, 2, w.Tsplit, ast, d.f16);
         ProdPlan pl;
+        if (rc == QLORA_OK) rc = run_prod(pr, w.dBpart, d_status, ast, &pl, d.f16);
         if (rc == QLORA_OK)
-            rc = run_prod(prod_dB(d, dY, w.Tsplit, terms), w.dBpart, d_status, ast, &pl, d.f16);
-        if (rc == QLORA_OK)
-            rc = launch_reduce(w.dBpart, pl.splits, d.Dout, pl.Qp, d.rp, terms, r, s, dB, 1, d.Dout, 0.f,
+            rc = launch_reduce(w.dBpart, pl.splits, d.Dout, pl.Qp, X8 ? 0 : d.rp, r, s, dB, 1, d.Dout, 0.f,
                                nullptr, 0, nullptr, 0, ast, d.f16);
     }
     if (side) {

@@ -13,6 +13,13 @@
 // CTA: 128 rows of P x N columns (N = 64/128/192/256, one UMMA of
 // 128 x N x 16 per 16-deep step, accumulator in TMEM); warp 0 = TMA,
 // warp 1 = MMA issuer, warps 2..5 = epilogue.  4-stage mbarrier ring.
+//
+// The tensor cores' fp32 accumulators round toward zero (measured: sums come
+// out 1.3e-8 of themselves small for each 16-deep step).  A caller that wants
+// 24-bit results bounds the k-tiles that one accumulator takes (SkinnyFold):
+// the epilogue warps then take it out after so many and add it, and the terms
+// of a split operand with it, in registers with rounding to nearest, while the
+// SM's other CTA keeps the tensor core busy.
 #include "common.cuh"
 #include "tcgen05.cuh"
 
@@ -27,6 +34,12 @@ struct SkinnySeg {
     int b_kmajor;        // 1: B(t,q) at b[q*ldb + t]; 0: at b[t*ldb + q]
     int64_t qext;        // extent of B along q (rows if K-major, columns if MN-major)
     int64_t R;           // reduction length
+};
+// gw > 0 (16 .. 64): the columns of B come in groups of terms * gw, the terms of
+// gw output columns one after another, and C holds their sums ([P][groups * gw]).
+// most: k-tiles one accumulator takes (gw > 0), or a split has (gw == 0, 0: no bound).
+struct SkinnyFold {
+    int terms = 1, gw = 0, groups = 0, most = 0;
 };
 
 namespace {
@@ -46,6 +59,7 @@ inline int skinny_smem_bytes(int N) { return skinny_stages(N) * skinny_stage_byt
 struct SkinnyParams {
     int64_t P;
     int N;                 // UMMA N = columns per CTA tile
+    int terms, gw, most;   // as SkinnyFold
     int a_kmajor, b_kmajor;  // bit s: segment s's operand is K-major
     int nk0, nk1, per;     // k-tiles per segment, k-tiles per split
     int stages, stage_bytes;
@@ -67,13 +81,13 @@ k_umma_skinny(const __grid_constant__ CUtensorMap tA0, const __grid_constant__ C
     const uint32_t bar0 = base + kSStages * kSStageBytes;
     auto full_bar = [&](int s) { return bar0 + 8u * s; };
     auto empty_bar = [&](int s) { return bar0 + 8u * (kSMaxStages + s); };
-    const uint32_t acc_bar = bar0 + 8u * (2 * kSMaxStages);
+    const uint32_t acc_bar = bar0 + 8u * (2 * kSMaxStages), acc_free = acc_bar + 8u;
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(gen_base + kSStages * kSStageBytes + 160);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gen_base + kSStages * kSStageBytes + 192);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int64_t p0 = (int64_t)blockIdx.x * kSBM;
-    const int q0 = blockIdx.y * p.N;
+    const int q0 = blockIdx.y * (p.gw ? p.terms * p.gw : p.N);
     const int nk = p.nk0 + p.nk1;
     const int kbeg = blockIdx.z * p.per;
     const int kend = kbeg + p.per < nk ? kbeg + p.per : nk;
@@ -87,6 +101,7 @@ k_umma_skinny(const __grid_constant__ CUtensorMap tA0, const __grid_constant__ C
             mbar_init(empty_bar(s), 1);
         }
         mbar_init(acc_bar, 1);
+        mbar_init(acc_free, 4);
         *abort_flag = 0;
         asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
         fence_proxy_async();
@@ -133,8 +148,17 @@ k_umma_skinny(const __grid_constant__ CUtensorMap tA0, const __grid_constant__ C
         }
     } else if (warp == 1) {
         if (lane == 0) {
+            int turn = 0;                              // k-tiles in the accumulator
+            uint32_t taken = 0;                        // times it has been taken out, as a phase parity
             for (int i = 0; i < nloc && ok; ++i) {
                 const int s = i % kSStages;
+                if (p.gw && turn == p.most) {
+                    umma_commit(acc_bar);
+                    ok = mbar_wait(acc_free, taken, abort_flag);
+                    if (!ok) break;
+                    taken ^= 1;
+                    turn = 0;
+                }
                 ok = mbar_wait(full_bar(s), (i / kSStages) & 1, abort_flag);
                 if (!ok) break;
                 tc_fence_after();
@@ -152,14 +176,15 @@ k_umma_skinny(const __grid_constant__ CUtensorMap tA0, const __grid_constant__ C
                                             : sdesc(sa + kk * 2048, 8192, 1024);
                     const uint64_t bd = bkm ? sdesc(sb + kk * 32, 16, 1024)
                                             : sdesc(sb + kk * 2048, 8192, 1024);
-                    umma_bf16(tmem, ad, bd, idesc, (i > 0 || kk > 0) ? 1u : 0u);
+                    umma_bf16(tmem, ad, bd, idesc, (turn > 0 || kk > 0) ? 1u : 0u);
                 }
+                ++turn;
                 umma_commit(empty_bar(s));
             }
             if (ok) umma_commit(acc_bar);
             else *abort_flag = 1;
         }
-    } else {
+    } else if (!p.gw) {
         ok = __all_sync(0xffffffffu, mbar_wait(acc_bar, 0, abort_flag));
         if (ok) {
             tc_fence_after();
@@ -183,6 +208,42 @@ k_umma_skinny(const __grid_constant__ CUtensorMap tA0, const __grid_constant__ C
                     }
                 }
             }
+        } else {
+            *abort_flag = 1;
+        }
+    } else {
+        // the accumulator, p.most k-tiles at a time: its terms, added in registers
+        const int q = warp & 3;
+        const uint32_t at = tmem + ((uint32_t)(32 * q) << 16);
+        float sum[64];
+#pragma unroll
+        for (int i = 0; i < 64; ++i) sum[i] = 0.f;
+        const int turns = (nloc + p.most - 1) / p.most;
+        for (int n = 0; n < turns && ok; ++n) {
+            ok = __all_sync(0xffffffffu, mbar_wait(acc_bar, n & 1, abort_flag));
+            if (!ok) break;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < 64; c += 16) {
+                if (c >= p.gw) break;
+                for (int t = 0; t < p.terms; ++t) {
+                    uint32_t v[16];
+                    tmem_ld16(at + t * p.gw + c, v);
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) sum[c + i] += __uint_as_float(v[i]);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(acc_free);
+        }
+        if (ok) {
+            const int64_t prow = p0 + 32 * q + lane;
+            float *dst = p.partial + ((int64_t)blockIdx.z * p.P + prow) * p.Qp + blockIdx.y * p.gw;
+#pragma unroll
+            for (int c = 0; c < 64; c += 4)
+                if (c < p.gw && prow < p.P)
+                    *reinterpret_cast<float4 *>(dst + c) = make_float4(sum[c], sum[c + 1], sum[c + 2], sum[c + 3]);
         } else {
             *abort_flag = 1;
         }
@@ -224,8 +285,8 @@ int skinny_n(int64_t Q) { return Q <= 64 ? 64 : (Q <= 128 ? 128 : (Q <= 192 ? 19
 
 // Split count and k-tiles per split for a (P, Q, total k-tiles) problem:
 // about one CTA per SM, at least 4 k-tiles per split, no empty split.
-void skinny_splits(int64_t P, int64_t Q, int nk, int *splits, int *per) {
-    const int64_t tiles = ((P + kSBM - 1) / kSBM) * ((Q + 255) / 256);
+void skinny_splits(int64_t P, int64_t Q, int nk, const SkinnyFold &f, int *splits, int *per) {
+    const int64_t tiles = ((P + kSBM - 1) / kSBM) * (f.gw ? f.groups : (Q + 255) / 256);
     // two resident CTAs per SM; round down so that the grid is one wave
     // (a few CTAs over the slots would cost a whole second round)
     int64_t s = 2 * device_sms() / tiles;
@@ -233,6 +294,10 @@ void skinny_splits(int64_t P, int64_t Q, int nk, int *splits, int *per) {
     if (s > cap) s = cap;
     if (s < 1) s = 1;
     int pr = (int)((nk + s - 1) / s);
+    if (!f.gw && f.most && pr > f.most) {
+        const int n = (nk + f.most - 1) / f.most;
+        pr = (nk + n - 1) / n;
+    }
     *per = pr;
     *splits = (nk + pr - 1) / pr;
 }
@@ -244,10 +309,10 @@ int skinny_k_tiles(const SkinnySeg *segs, int nseg) {
 }
 
 // C[P, Q] partial sums into partial[splits][P][Qp] (Qp >= Q, multiple of 4).
-int launch_umma_skinny(const SkinnySeg *segs, int nseg, int64_t P, int64_t Q, int64_t Qp,
+int launch_umma_skinny(const SkinnySeg *segs, int nseg, int64_t P, int64_t Q, int64_t Qp, const SkinnyFold &f,
                        float *partial, uint32_t *d_status, cudaStream_t st, bool f16) {
     if (P <= 0 || Q <= 0) return QLORA_OK;
-    const int N = skinny_n(Q < 256 ? Q : 256);
+    const int N = f.gw ? (f.terms * f.gw + 63) / 64 * 64 : skinny_n(Q < 256 ? Q : 256);
     CUtensorMap tA[2], tB[2];
     SkinnyParams prm{};
     for (int i = 0; i < 2; ++i) {
@@ -261,9 +326,12 @@ int launch_umma_skinny(const SkinnySeg *segs, int nseg, int64_t P, int64_t Q, in
     prm.nk0 = (int)((segs[0].R + kSBK - 1) / kSBK);
     prm.nk1 = nseg > 1 ? (int)((segs[1].R + kSBK - 1) / kSBK) : 0;
     int splits = 1, per = 1;
-    skinny_splits(P, Q, prm.nk0 + prm.nk1, &splits, &per);
+    skinny_splits(P, Q, prm.nk0 + prm.nk1, f, &splits, &per);
     prm.P = P;
     prm.N = N;
+    prm.terms = f.terms;
+    prm.gw = f.gw;
+    prm.most = f.most;
     prm.stages = skinny_stages(N);
     prm.stage_bytes = skinny_stage_bytes(N);
     const int smem = skinny_smem_bytes(N);
@@ -273,7 +341,8 @@ int launch_umma_skinny(const SkinnySeg *segs, int nseg, int64_t P, int64_t Q, in
     prm.status = d_status;
     prm.f16 = f16 ? 1 : 0;
     if (set_max_smem(reinterpret_cast<const void *>(k_umma_skinny), (int)smem) != cudaSuccess) return QLORA_ECUDA;
-    dim3 grid((unsigned)((P + kSBM - 1) / kSBM), (unsigned)((Q + N - 1) / N), (unsigned)splits);
+    dim3 grid((unsigned)((P + kSBM - 1) / kSBM), (unsigned)(f.gw ? f.groups : (Q + N - 1) / N),
+              (unsigned)splits);
     k_umma_skinny<<<grid, kSThreads, smem, st>>>(tA[0], tA[1], tB[0], tB[1], prm);
     QLORA_LAUNCH_CHECK();
     return QLORA_OK;
