@@ -349,7 +349,9 @@ constexpr int kWStages = 4;
 constexpr int kWSlab = 128 * kTK;                  // 16 KB: 128 rows of one operand
 constexpr int kWStageBytes = 3 * kWSlab;           // two token slabs, one weight slab
 constexpr int kWThreads = 320, kWEpiThreads = 256;
-constexpr int kWSmemBytes = kWStages * kWStageBytes + 1024 + 256 + 2 * 2 * 256 * 4;
+constexpr int kWTurnPitch = 17;                    // words: 32 rows of 16 words a warp, without bank conflicts
+constexpr int kWTurnWords = 32 * kWTurnPitch;
+constexpr int kWSmemBytes = kWStages * kWStageBytes + 1024 + 256 + 2 * 2 * 256 * 4 + (kWEpiThreads / 32) * kWTurnWords * 4;
 constexpr int kWGroup = 8;                         // row tiles that share a column tile's pass through L2
 
 struct WideParams {
@@ -405,12 +407,21 @@ __device__ __forceinline__ void tile_at(const WideParams &p, int t, int &tm, int
     tn = in / rows;
 }
 
-// 32 finished values of one row, columns [n, n + 32)
-__device__ __forceinline__ void store32(const WideParams &p, int64_t m, int64_t n, const float (&v)[32]) {
-    if (m >= p.M || n >= p.N) return;
+// A warp's 32 x 32 block of finished values: lane l has columns [n, n + 32) of
+// row m0 + l.  Rows on 16-byte borders are stored by their lanes, 32 bytes at a
+// time.  Others are turned in shared memory (`turn`, the warp's own), so that
+// a store covers consecutive values of a row: a lane's two-byte stores to 32
+// rows at once took longer than the product (2143 x 10158 x 2222 of an input gradient: 289 us, turned 117).
+__device__ __forceinline__ void store_block(const WideParams &p, int64_t m0, int64_t n, const float (&v)[32],
+                                            uint32_t *turn) {
+    const int lane = threadIdx.x & 31;
+    const int64_t m = m0 + lane;
+    if (n >= p.N || m0 >= p.M) return;               // the same for all lanes
+    const bool whole = n + 32 <= p.N;
     if (p.dtype == QLORA_DTYPE_FP32) {
-        float *o = static_cast<float *>(p.out) + m * p.ldo + n;
-        if (p.align >= 32 && n + 32 <= p.N) {
+        if (p.align >= 32 && whole) {
+            if (m >= p.M) return;
+            float *o = static_cast<float *>(p.out) + m * p.ldo + n;
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 uint32_t w[8];
@@ -418,30 +429,50 @@ __device__ __forceinline__ void store32(const WideParams &p, int64_t m, int64_t 
                 for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[8 * i + j]);
                 stg256(o + 8 * i, w);
             }
-        } else {
+            return;
+        }
 #pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (n + i < p.N) o[i] = v[i];
+        for (int half = 0; half < 2; ++half) {       // 16 columns, two rows a store
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) turn[lane * kWTurnPitch + j] = __float_as_uint(v[16 * half + j]);
+            __syncwarp();
+            const int64_t c = n + 16 * half + (lane & 15);
+#pragma unroll 8
+            for (int r = lane >> 4; r < 32; r += 2)
+                if (m0 + r < p.M && c < p.N)
+                    static_cast<float *>(p.out)[(m0 + r) * p.ldo + c] =
+                        __uint_as_float(turn[r * kWTurnPitch + (lane & 15)]);
         }
         return;
     }
     const bool f16 = p.dtype == QLORA_DTYPE_FP16;
-    uint16_t *o = static_cast<uint16_t *>(p.out) + m * p.ldo + n;
     uint32_t w[16];
 #pragma unroll
     for (int i = 0; i < 16; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1], f16);
-    if (p.align >= 32 && n + 32 <= p.N) {
-        stg256(o, w);
-        stg256(o + 16, w + 8);
-    } else if (p.align >= 16 && n + 32 <= p.N) {
+    if (p.align >= 16 && whole) {
+        if (m >= p.M) return;
+        uint16_t *o = static_cast<uint16_t *>(p.out) + m * p.ldo + n;
+        if (p.align >= 32) {
+            stg256(o, w);
+            stg256(o + 16, w + 8);
+        } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            reinterpret_cast<uint4 *>(o)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-            if (n + i < p.N) o[i] = (uint16_t)(w[i / 2] >> (16 * (i & 1)));
+            for (int i = 0; i < 4; ++i)
+                reinterpret_cast<uint4 *>(o)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        }
+        return;
     }
+    __syncwarp();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) turn[lane * kWTurnPitch + i] = w[i];
+    __syncwarp();
+    const int64_t c = n + lane;
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r)
+        if (m0 + r < p.M && c < p.N)
+            static_cast<uint16_t *>(p.out)[(m0 + r) * p.ldo + c] =
+                (uint16_t)(turn[r * kWTurnPitch + (lane >> 1)] >> (16 * (lane & 1)));
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWThreads, 1)
@@ -458,6 +489,7 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(gen_base + kWStages * kWStageBytes + 208);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gen_base + kWStages * kWStageBytes + 240);
     float *cbuf = reinterpret_cast<float *>(gen_base + kWStages * kWStageBytes + 256);   // [2][2][256]
+    uint32_t *turns = reinterpret_cast<uint32_t *>(cbuf + 2 * 2 * 256);
 
     const int warp = warp_index(), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -586,7 +618,8 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
             ok = __all_sync(0xffffffffu, mbar_wait_cluster(acc_full, i & 1, abort_flag));
             if (!ok) break;
             tc_fence_after();
-            const int64_t mrow = (int64_t)tm * mrows + 128 * rank + 32 * qt + lane;
+            const int64_t mblk = (int64_t)tm * mrows + 128 * rank + 32 * qt, mrow = mblk + lane;
+            uint32_t *turn = turns + (warp - 2) * kWTurnWords;
             float rs[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -609,7 +642,7 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                     for (int j = 0; j < 32; ++j)
                         v[j] = __fmaf_rn(__fmul_rn(join_digits((float)(int)a[j], (int)b[j]), rs[0]),
                                          cs[col + j], cb[col + j]);
-                    store32(p, mrow, n0 + col, v);
+                    store_block(p, mblk, n0 + col, v, turn);
                 }
             } else {
 #pragma unroll
@@ -627,7 +660,7 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
 #pragma unroll
                         for (int j = 0; j < 32; ++j)
                             v[j] = __fmaf_rn(__fmul_rn((float)(int)a[j], rs[h]), cs[col + j], cb[col + j]);
-                        store32(p, mrow + 256 * h, n0 + col, v);
+                        store_block(p, mblk + 256 * h, n0 + col, v, turn);
                     }
             }
         }
@@ -661,13 +694,13 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
 // once (8 splits of N = 176 took twice the time of 6).
 struct TallPlan {
     int nt, splits, per;
+    double us;
 };
 static TallPlan plan_tall(const Int8Product &g, int nk) {
     const int sms = device_sms();
     const int cap = 256 / g.planes / 16 * 16;
     const int64_t pt = (g.P + kTP - 1) / kTP, least = (g.Q + cap - 1) / cap;
     TallPlan best{};
-    double best_us = 0;
     int last = 0;
     for (int64_t tq = least; tq <= 16 * least; ++tq) {
         const int nt = (int)(((g.Q + tq - 1) / tq + 15) / 16 * 16);
@@ -681,9 +714,8 @@ static TallPlan plan_tall(const Int8Product &g, int nk) {
             const int64_t units = tiles * s, waves = (units + slots - 1) / slots;
             const double tile = (0.17 + 0.0018 * N) * (units > sms && N <= kTTwoN ? 1.25 : 1.0);
             const double us = 2.0 + (double)waves * (3.0 + per * tile) + (s > 1 ? 1.2 + 0.2 * s : 0.0) + 0.004 * N;
-            if (best.nt == 0 || us < best_us) {
-                best = TallPlan{nt, s, per};
-                best_us = us;
+            if (best.nt == 0 || us < best.us) {
+                best = TallPlan{nt, s, per, us};
             }
         }
         if (nt == 16) break;
@@ -691,7 +723,7 @@ static TallPlan plan_tall(const Int8Product &g, int nk) {
     return best;
 }
 
-static int launch_int8_tall(const Int8Product &g, uint32_t *d_status, cudaStream_t st) {
+static int launch_int8_tall(const Int8Product &g, const TallPlan &plan, uint32_t *d_status, cudaStream_t st) {
     if (g.P <= 0 || g.Q <= 0) return QLORA_OK;
     TallParams p{};
     p.P = g.P;
@@ -700,7 +732,6 @@ static int launch_int8_tall(const Int8Product &g, uint32_t *d_status, cudaStream
     p.plane_rows = g.plane_rows;
     p.nk = (int)((g.R + kTK - 1) / kTK);
     p.a_mn = g.a_mn;
-    const TallPlan plan = plan_tall(g, p.nk);
     p.nt = plan.nt;
     p.per = plan.per;
     const int N = p.planes * p.nt;
@@ -803,12 +834,19 @@ static int launch_int8_wide(const Int8Product &g, uint32_t *d_status, cudaStream
     return QLORA_OK;
 }
 
+// The wide kernel takes a k-tile in about 0.76 us (512 x 256 outputs, or 256 x
+// 256 of two digits), each of its CTA pairs a tile after the other: 29 us at
+// 1024 x 4096 x 4096, 54 at 1024 x 4096 x 11008, by the model 30 and 55.
 int launch_int8_product(const Int8Product &g, uint32_t *d_status, cudaStream_t st) {
     if (g.P <= 0 || g.Q <= 0) return QLORA_OK;
-    const int64_t mrows = g.planes == 2 ? 256 : 512;
-    const int64_t tiles = ((g.Q + mrows - 1) / mrows) * ((g.P + 255) / 256);
-    if (!g.q_inner && g.planes <= 2 && g.Q > 128 && tiles >= device_sms() / 4) return launch_int8_wide(g, d_status, st);
-    return launch_int8_tall(g, d_status, st);
+    const int nk = (int)((g.R + kTK - 1) / kTK);
+    const TallPlan plan = plan_tall(g, nk);
+    if (!g.q_inner && g.planes <= 2) {
+        const int64_t mrows = g.planes == 2 ? 256 : 512, pairs = device_sms() / 2;
+        const int64_t tiles = ((g.Q + mrows - 1) / mrows) * ((g.P + 255) / 256);
+        if (6.0 + 0.76 * nk * (double)((tiles + pairs - 1) / pairs) < plan.us) return launch_int8_wide(g, d_status, st);
+    }
+    return launch_int8_tall(g, plan, d_status, st);
 }
 
 }  // namespace qlora

@@ -16,9 +16,9 @@ struct Raw8 {
 };
 
 // Values [8 v, 8 v + 8) of a row, zeros past its end.  FULL: rows start on
-// 16-byte borders and hold a multiple of 8 values.  Otherwise a 16-bit row that
-// starts off a border is read in the two aligned pieces around the values,
-// where both lie inside the row, and shifted into place; what is left, at the
+// 16-byte borders and hold a multiple of 8 values.  Otherwise a row that starts
+// off a border is read in the aligned pieces around the values, where all lie
+// inside the row, and shifted into place; what is left, at the
 // row's ends, comes value by value (the addresses clamped, so that the eight
 // loads do not wait for one another).
 template <int DT, bool FULL>
@@ -37,20 +37,24 @@ __device__ __forceinline__ Raw8<DT> load8(const void *row, int v, int cols) {
         }
         return r;
     }
-    if (DT != QLORA_DTYPE_FP32 && v > 0 && e0 + 2 * kVec <= cols) {
-        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(at - off));
-        const uint4 y = __ldg(reinterpret_cast<const uint4 *>(at - off) + 1);
-        const uint32_t in[8] = {x.x, x.y, x.z, x.w, y.x, y.y, y.z, y.w};
-        uint32_t t[5];
+    if (v > 0 && e0 + kVec + 16 / kSize <= cols) {
+        uint32_t in[kWords + 4];
 #pragma unroll
-        for (int i = 0; i < 5; ++i) {
+        for (int i = 0; i < kWords / 4 + 1; ++i) {
+            const uint4 x = __ldg(reinterpret_cast<const uint4 *>(at - off) + i);
+            in[4 * i] = x.x, in[4 * i + 1] = x.y, in[4 * i + 2] = x.z, in[4 * i + 3] = x.w;
+        }
+        uint32_t t[kWords + 1];
+#pragma unroll
+        for (int i = 0; i < kWords + 1; ++i) {
             t[i] = in[i];
-            if (off >= 4 && i + 1 < 8) t[i] = in[i + 1];
-            if (off >= 8 && i + 2 < 8) t[i] = in[i + 2];
-            if (off >= 12 && i + 3 < 8) t[i] = in[i + 3];
+            if (off >= 4 && i + 1 < kWords + 4) t[i] = in[i + 1];
+            if (off >= 8 && i + 2 < kWords + 4) t[i] = in[i + 2];
+            if (off >= 12 && i + 3 < kWords + 4) t[i] = in[i + 3];
         }
 #pragma unroll
-        for (int i = 0; i < kWords; ++i) r.w[i] = __funnelshift_r(t[i % 4], t[i % 4 + 1], 8 * (off & 3u));
+        for (int i = 0; i < kWords; ++i)
+            r.w[i] = DT == QLORA_DTYPE_FP32 ? t[i] : __funnelshift_r(t[i], t[i + 1], 8 * (off & 3u));
         return r;
     }
     uint32_t one[kVec];

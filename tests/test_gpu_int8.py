@@ -81,7 +81,7 @@ def test_quantize_extremes(qlib):
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("rows,cols,stride", [(2000, 2048, 2048), (1000, 4099, 4104), (700, 20000, 20000),
                                               (900, 3001, 3001), (3000, 1000, 1000), (400, 300, 301), (901, 1024, 2048),
-                                              (641, 9000, 9008)])
+                                              (641, 9000, 9008), (1200, 2055, 2055), (50, 20001, 20001)])
 def test_quantize_many_rows(qlib, rows, cols, stride, dtype):
     """Persistent CTAs, a warp a row and a CTA a row; among the rows: zero, tiny, huge and non-finite
     ones, scales that a / 127 gives exactly (a = 127 m 2^e, quotients of k + 1/2 among them), ties."""
@@ -148,7 +148,8 @@ MATMUL = [(1, 1, 1), (1, 64, 8), (1, 4096, 256), (2, 100, 130), (16, 4096, 1000)
           # many tokens: one tile a CTA pair and several, reductions shorter and longer than the ring
           (1100, 200, 5000), (2600, 1500, 2504), (513, 96, 9999), (700, 5000, 333), (2100, 2053, 40),
           (1200, 40, 3000), (1000, 24, 2504), (600, 16, 11008), (950, 33, 2500), (620, 200, 25000), (1501, 8, 8192),
-          (3001, 16, 11001),
+          (3001, 16, 11001), (1500, 2000, 3001), (900, 6000, 5001), (1600, 3001, 2000), (2100, 3010, 1500),
+          (1030, 2500, 4100),
           (4100, 640, 3000), (4100, 200, 3001), (2100, 3000, 700), (9300, 130, 1000),
           # a few tokens: quantized by the product's own CTAs or before it, rows in one wave and several
           (3, 1000, 2500), (8, 2048, 9500), (4, 513, 5000), (7, 12000, 33), (1, 28672, 100), (2, 8192, 5003),
