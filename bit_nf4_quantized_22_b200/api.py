@@ -116,6 +116,12 @@ class NF4Weight:
         return n
 
 
+def _pitch(cols: int) -> int:
+    """Row pitch of new codes: whole 128-byte lines, which the products read fastest; short rows 16."""
+    unit = 128 if cols >= 128 else 16
+    return (cols + unit - 1) // unit * unit
+
+
 @dataclass
 class Int8Rows:
     """A matrix in 8-bit rows: row m stands for codes[m] * scales[m].  The rows are
@@ -125,7 +131,7 @@ class Int8Rows:
 
     @staticmethod
     def empty(rows: int, cols: int, device="cuda") -> "Int8Rows":
-        codes = torch.empty_strided((rows, cols), ((cols + 15) // 16 * 16, 1), dtype=torch.int8, device=device)
+        codes = torch.empty_strided((rows, cols), (_pitch(cols), 1), dtype=torch.int8, device=device)
         return Int8Rows(codes, torch.empty(rows, dtype=torch.float32, device=device))
 
     @property
@@ -412,7 +418,7 @@ def int8_matmul(x: torch.Tensor | Int8Rows, w: Int8Rows, bias: torch.Tensor | No
             if (xc.rows, xc.cols) != (M, K):
                 raise ValueError(f"x8_out: [{M}, {K}] is needed")
         else:   # codes and scales in one scratch tensor
-            ld = (K + 15) // 16 * 16
+            ld = _pitch(K)
             scratch = torch.empty(M * (ld + 4), dtype=torch.uint8, device=x.device)
             xc = _lib.Int8RowsC(M, K, ld, scratch.data_ptr(), scratch.data_ptr() + M * ld)
     if K != wc.cols:

@@ -310,7 +310,7 @@ size_t layout_bwd(const Dims &d, bool have_tsaved, bool want_dx, bool want_da, b
     x.Gpart = b.take<float>(prod_partial_floats(prod_G(d, 0, 0, x8)));
     if (want_da && !x8) x.Gsplit = b.take<uint16_t>(d.M * 2 * d.rp);
     if (want_da && x8) {
-        x.Gdig = b.take<int8_t>(3 * d.rp * round_up(d.M, 16));
+        x.Gdig = b.take<int8_t>(3 * d.rp * round_up(d.M, 128));
         x.Gstep = b.take<float>(d.rp);
     }
     if (d.g > 1 && !x8 && (want_da || (want_db && !have_tsaved))) {
@@ -412,7 +412,7 @@ bool aligned_to(const void *p, int32_t dt) {
 // dA[k][j] = s step_j sum_m c[m][k] digits.  Pooled: the sums of a group's 64 features, over 64.
 int run_dA_int8(const Dims &d, const int8_rows_t &x, const float *G, int8_t *dig, float *step, float s, float *dA,
                 uint32_t *status, cudaStream_t st) {
-    const int64_t ld = round_up(d.M, 16);
+    const int64_t ld = round_up(d.M, 128);
     RC(launch_int8_col_digits(G, QLORA_DTYPE_FP32, d.M, d.r, x.scales, dig, ld, d.rp, 1, step, st));
     Int8Product g{};
     g.a = x.codes, g.lda = x.ld, g.a_mn = 1;
@@ -447,7 +447,7 @@ struct GradWs {
 size_t layout_grad8(int64_t M, const int8_rows_t &w, void *base, GradWs *out) {
     Bump b(base);
     GradWs x{};
-    x.ld = round_up(w.rows, 16);
+    x.ld = round_up(w.rows, 128);   // whole lines: a TMA row off them takes two
     x.planes = b.take<int8_t>(2 * M * x.ld);
     x.steps = b.take<float>(M);
     if (out) *out = x;

@@ -27,7 +27,7 @@ constexpr int kTABytes = kTP * kTK;            // 16 KB
 constexpr int kTThreads = 192;
 constexpr int kTMaxStages = 8;
 constexpr int kTMaxSplits = 8;                 // portable cluster size
-constexpr int kTTwoN = 64;                     // UMMA N up to which two CTAs share an SM
+constexpr int kTTwoN = 128;                    // UMMA N up to which two CTAs share an SM
 constexpr int kTSmemTwo = 110 * 1024;
 constexpr int kTSmemOne = 220 * 1024;
 
@@ -686,12 +686,14 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
 }  // namespace
 
 // How a product is cut: columns of B a tile, splits of the reduction.  The
-// least of a model of the measured times (4096 x 4096 and 4096 x 11008 weights,
-// 16 to 1024 tokens, within 10%): about 5 us whatever the size, 0.17 us + 1.8 ns
-// a column of the MMA for each k-tile of a CTA (a quarter more where two CTAs
-// share the SM, which N <= 64 lets them), 1.2 us + 0.2 us a split for a
-// cluster's exchange.  Clusters of big CTAs past 6 do not all find a place at
-// once (8 splits of N = 176 took twice the time of 6).
+// least of a model of the measured times (16 to 2300 tokens on weights of 900 to
+// 11008 channels, reductions of 4096 to 26112; within 15% there): 6 us, 3 us a
+// wave of CTAs, for each k-tile of a CTA 0.17 us + 1.8 ns a column alone on its
+// SM, 0.16 us + 2.4 ns where two share it (as N <= 128 lets them: 1024 x 4096 x
+// 4096 takes 27 us in 128 columns, 33 in 256), 1.2 us + 0.2 us a split for a
+// cluster's exchange, half as much again for rows off 128-byte borders (their
+// pieces straddle two lines).  Clusters of big CTAs past 6 do not all find a
+// place at once (8 splits of N = 176 took twice the time of 6).
 struct TallPlan {
     int nt, splits, per;
     double us;
@@ -700,20 +702,21 @@ static TallPlan plan_tall(const Int8Product &g, int nk) {
     const int sms = device_sms();
     const int cap = 256 / g.planes / 16 * 16;
     const int64_t pt = (g.P + kTP - 1) / kTP, least = (g.Q + cap - 1) / cap;
+    const double lines = g.lda % 128 || g.ldb % 128 ? 1.5 : 1.0;
     TallPlan best{};
     int last = 0;
     for (int64_t tq = least; tq <= 16 * least; ++tq) {
         const int nt = (int)(((g.Q + tq - 1) / tq + 15) / 16 * 16);
         if (nt == last) continue;
         last = nt;
-        const int N = nt * g.planes, most = N <= kTTwoN ? kTMaxSplits : 6;
+        const int N = nt * g.planes, most = N <= 64 ? kTMaxSplits : 6;
         const int64_t slots = (N <= kTTwoN ? 2 : 1) * (int64_t)sms, tiles = pt * ((g.Q + nt - 1) / nt);
         for (int s = 1; s <= most && (s == 1 || 2 * s <= nk); ++s) {
             const int per = (nk + s - 1) / s;
             if ((nk + per - 1) / per != s) continue;
             const int64_t units = tiles * s, waves = (units + slots - 1) / slots;
-            const double tile = (0.17 + 0.0018 * N) * (units > sms && N <= kTTwoN ? 1.25 : 1.0);
-            const double us = 2.0 + (double)waves * (3.0 + per * tile) + (s > 1 ? 1.2 + 0.2 * s : 0.0) + 0.004 * N;
+            const double tile = (units > sms && N <= kTTwoN ? 0.16 + 0.0024 * N : 0.17 + 0.0018 * N) * lines;
+            const double us = 6.0 + (double)waves * (3.0 + per * tile) + (s > 1 ? 1.2 + 0.2 * s : 0.0) + 0.004 * N;
             if (best.nt == 0 || us < best.us) {
                 best = TallPlan{nt, s, per, us};
             }

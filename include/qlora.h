@@ -263,7 +263,8 @@ int qlora_backward(const uint16_t *X, const uint16_t *dY, int64_t M, const nf4_w
  * input and each output channel of the weight).  One matrix of 8-bit rows:
  *   codes    [rows][ld] int8, the first cols of a row valid; 16-byte aligned
  *   scales   [rows] fp32
- *   ld       bytes from one row to the next: >= cols, a multiple of 16
+ *   ld       bytes from one row to the next: >= cols, a multiple of 16 (of 128
+ *            is read fastest)
  *   rows     up to 2^30;  cols  1 .. 2^30
  * Row m stands for codes[m][k] * scales[m].  The rows are tokens for an
  * activation, output channels for a weight Wt:[Dout, Din]. */
