@@ -14,6 +14,8 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <type_traits>
+
 #include "int8_gemm.cuh"
 #include "tcgen05.cuh"
 
@@ -32,9 +34,7 @@ constexpr int kTSmemTwo = 110 * 1024;
 constexpr int kTSmemOne = 220 * 1024;
 
 // 256 * (a rounded upper sum) + the lower sum, in fp32: off by 2^-23 of the larger of the two terms
-__device__ __forceinline__ float join_digits(float upper, int lower) {
-    return __fmaf_rn(upper, 256.f, (float)lower);
-}
+__device__ __forceinline__ float join_digits(float upper, float lower) { return __fmaf_rn(upper, 256.f, lower); }
 
 // kind::i8 instruction descriptor: signed 8-bit A and B, s32 accumulator.
 __host__ __device__ constexpr uint32_t idesc_i8(uint32_t m, uint32_t n, uint32_t a_mn, uint32_t b_mn) {
@@ -77,6 +77,31 @@ __device__ __forceinline__ void umma_commit_elect(uint32_t bar) {
         "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar)
         : "memory");
 }
+// 32 TMEM columns without the wait, and the wait for all loads before it, which
+// the values pass through so that nothing reads them earlier.
+__device__ __forceinline__ void tmem_ld32_issue(uint32_t taddr, uint32_t *v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+        "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr));
+}
+#define QLORA_TIE16(v, o)                                                                                          \
+    "+r"((v)[o]), "+r"((v)[(o) + 1]), "+r"((v)[(o) + 2]), "+r"((v)[(o) + 3]), "+r"((v)[(o) + 4]),                  \
+        "+r"((v)[(o) + 5]), "+r"((v)[(o) + 6]), "+r"((v)[(o) + 7]), "+r"((v)[(o) + 8]), "+r"((v)[(o) + 9]),        \
+        "+r"((v)[(o) + 10]), "+r"((v)[(o) + 11]), "+r"((v)[(o) + 12]), "+r"((v)[(o) + 13]), "+r"((v)[(o) + 14]),   \
+        "+r"((v)[(o) + 15])
+template <int N>
+__device__ __forceinline__ void tmem_wait(uint32_t (&v)[N]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;\n" ::: "memory");
+#pragma unroll
+    for (int o = 0; o < N; o += 16) asm volatile("" : QLORA_TIE16(v, o));
+}
+#undef QLORA_TIE16
 __device__ __forceinline__ int4 ld_cluster_int4(uint32_t addr) {
     int4 v;
     asm volatile("ld.shared::cluster.v4.s32 {%0,%1,%2,%3}, [%4];\n"
@@ -281,8 +306,8 @@ k_int8_tall(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             if (p.planes == 2) {
                 // as k_int8_wide does, so that a token's gradient does not depend on its batch
                 t = column(1, c);
-                v[0] = join_digits(v[0], t.x), v[1] = join_digits(v[1], t.y);
-                v[2] = join_digits(v[2], t.z), v[3] = join_digits(v[3], t.w);
+                v[0] = join_digits(v[0], (float)t.x), v[1] = join_digits(v[1], (float)t.y);
+                v[2] = join_digits(v[2], (float)t.z), v[3] = join_digits(v[3], (float)t.w);
             } else if (p.planes > 2) {
                 int64_t sum[4] = {t.x, t.y, t.z, t.w};
                 for (int d = 1; d < p.planes; ++d) {
@@ -356,9 +381,9 @@ k_int8_tall(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 constexpr int kWStages = 4;
 constexpr int kWSlab = 128 * kTK;                  // 16 KB: 128 rows of one operand
 constexpr int kWStageBytes = 3 * kWSlab;           // two token slabs, one weight slab
-constexpr int kWThreads = 320, kWEpiThreads = 256;
+constexpr int kWThreads = 384, kWEpiThreads = 256;   // warps: loads, MMAs, two idle; eight for the sums
 constexpr int kWTurnPitch = 17;                    // words: 32 rows of 16 words a warp, without bank conflicts
-constexpr int kWTurnWords = 32 * kWTurnPitch;
+constexpr int kWTurnWords = 32 * kWTurnPitch;      // or 16 rows of 32 words in swizzled 16-byte pieces
 constexpr int kWSmemBytes = kWStages * kWStageBytes + 1024 + 256 + 2 * 2 * 256 * 4 + (kWEpiThreads / 32) * kWTurnWords * 4;
 constexpr int kWGroup = 8;                         // row tiles that share a column tile's pass through L2
 
@@ -373,7 +398,7 @@ struct WideParams {
     const void *bias;
     void *out;
     int64_t ldo;
-    int dtype, align;          // bytes that every row of a tile starts on: 32, 16 or less
+    int dtype, aligned;        // rows of the output start on 16-byte borders
     int pdl;
     uint32_t *status;
 };
@@ -401,12 +426,6 @@ __device__ __forceinline__ void umma_commit_pair_elect(uint32_t bar, uint16_t ma
         "h"(mask)
         : "memory");
 }
-__device__ __forceinline__ void stg256(void *p, const uint32_t *v) {
-    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"l"(p), "r"(v[0]), "r"(v[1]), "r"(v[2]),
-                 "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
-                 : "memory");
-}
-
 // Row and column tile of tile t: groups of kWGroup row tiles, columns within a group.
 __device__ __forceinline__ void tile_at(const WideParams &p, int t, int &tm, int &tn) {
     const int per = kWGroup * p.nt, g = t / per, in = t % per;
@@ -415,72 +434,59 @@ __device__ __forceinline__ void tile_at(const WideParams &p, int t, int &tm, int
     tn = in / rows;
 }
 
-// A warp's 32 x 32 block of finished values: lane l has columns [n, n + 32) of
-// row m0 + l.  Rows on 16-byte borders are stored by their lanes, 32 bytes at a
-// time.  Others are turned in shared memory (`turn`, the warp's own), so that
-// a store covers consecutive values of a row: a lane's two-byte stores to 32
-// rows at once took longer than the product (2143 x 10158 x 2222 of an input gradient: 289 us, turned 117).
-__device__ __forceinline__ void store_block(const WideParams &p, int64_t m0, int64_t n, const float (&v)[32],
+// A warp's block of 32 rows of finished values: lane l has 128 bytes of row
+// m0 + l from column n on, 64 16-bit values in pairs or 32 fp32 values.  They
+// are turned in shared memory (`turn`, the warp's own, XXX), so that a store
+// covers whole lines or, off 16-byte borders, consecutive values of a row.
+template <bool F32>
+__device__ __forceinline__ void store_block(const WideParams &p, int64_t m0, int64_t n, const uint32_t *w,
                                             uint32_t *turn) {
+    constexpr int kPer = F32 ? 1 : 2, kCols = 32 * kPer;
     const int lane = threadIdx.x & 31;
-    const int64_t m = m0 + lane;
     if (n >= p.N || m0 >= p.M) return;               // the same for all lanes
-    const bool whole = n + 32 <= p.N;
-    if (p.dtype == QLORA_DTYPE_FP32) {
-        if (p.align >= 32 && whole) {
-            if (m >= p.M) return;
-            float *o = static_cast<float *>(p.out) + m * p.ldo + n;
+    if (p.aligned && n + kCols <= p.N) {
+        uint4 *t4 = reinterpret_cast<uint4 *>(turn);
+        const int at = lane >> 3, piece = lane & 7;
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {       // 16 rows, 4 in a store
+            __syncwarp();
+            if (lane >> 4 == half)
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    t4[(lane & 15) * 8 + (i ^ (lane & 7))] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            __syncwarp();
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                uint32_t w[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[8 * i + j]);
-                stg256(o + 8 * i, w);
+                const int r = 4 * i + at;
+                const int64_t m = m0 + 16 * half + r;
+                const uint4 v = t4[r * 8 + (piece ^ (r & 7))];
+                if (m < p.M)
+                    *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + (m * p.ldo + n) * (4 / kPer) + 16 * piece) = v;
             }
-            return;
         }
+        return;
+    }
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {       // 16 columns, two rows a store
-            __syncwarp();
+    for (int half = 0; half < 2; ++half) {           // 16 words of each row
+        __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) turn[lane * kWTurnPitch + j] = __float_as_uint(v[16 * half + j]);
-            __syncwarp();
+        for (int j = 0; j < 16; ++j) turn[lane * kWTurnPitch + j] = w[16 * half + j];
+        __syncwarp();
+        if constexpr (F32) {                         // two rows a store
             const int64_t c = n + 16 * half + (lane & 15);
 #pragma unroll 8
             for (int r = lane >> 4; r < 32; r += 2)
                 if (m0 + r < p.M && c < p.N)
-                    static_cast<float *>(p.out)[(m0 + r) * p.ldo + c] =
-                        __uint_as_float(turn[r * kWTurnPitch + (lane & 15)]);
-        }
-        return;
-    }
-    const bool f16 = p.dtype == QLORA_DTYPE_FP16;
-    uint32_t w[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) w[i] = pack2(v[2 * i], v[2 * i + 1], f16);
-    if (p.align >= 16 && whole) {
-        if (m >= p.M) return;
-        uint16_t *o = static_cast<uint16_t *>(p.out) + m * p.ldo + n;
-        if (p.align >= 32) {
-            stg256(o, w);
-            stg256(o + 16, w + 8);
+                    static_cast<uint32_t *>(p.out)[(m0 + r) * p.ldo + c] = turn[r * kWTurnPitch + (lane & 15)];
         } else {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                reinterpret_cast<uint4 *>(o)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-        }
-        return;
-    }
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 16; ++i) turn[lane * kWTurnPitch + i] = w[i];
-    __syncwarp();
-    const int64_t c = n + lane;
+            const int64_t c = n + 32 * half + lane;
 #pragma unroll 8
-    for (int r = 0; r < 32; ++r)
-        if (m0 + r < p.M && c < p.N)
-            static_cast<uint16_t *>(p.out)[(m0 + r) * p.ldo + c] =
-                (uint16_t)(turn[r * kWTurnPitch + (lane >> 1)] >> (16 * (lane & 1)));
+            for (int r = 0; r < 32; ++r)
+                if (m0 + r < p.M && c < p.N)
+                    static_cast<uint16_t *>(p.out)[(m0 + r) * p.ldo + c] =
+                        (uint16_t)(turn[r * kWTurnPitch + (lane >> 1)] >> (16 * (lane & 1)));
+        }
+    }
 }
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWThreads, 1)
@@ -527,91 +533,95 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
     bool ok = true;
-
-    if (warp == 0) {
-        if (elect_one()) {
-            auto load_w = [&](int s, int t0, int tn) {
-                const uint32_t fa0 = mapa_shared(full(s), 0);
-                const int c0 = tn * 256 + 128 * (int)rank;
-                if (rank == 0) mbar_expect_tx(full(s), 2 * kWStageBytes);
-                const uint32_t sb = base + s * kWStageBytes + 2 * kWSlab;
-                if (p.b_mn) tma_load_2d_pair(sb, &tmW, c0, t0, fa0);
-                else tma_load_2d_pair(sb, &tmW, t0, c0, fa0);
-            };
-            auto load_x = [&](int s, int t0, int tm) {
-                const uint32_t fa0 = mapa_shared(full(s), 0);
-                const uint32_t sa = base + s * kWStageBytes;
-                const int r0 = tm * mrows + 128 * (int)rank;
-                tma_load_2d_pair(sa, &tmX, t0, r0, fa0);
-                tma_load_2d_pair(sa + kWSlab, &tmX, t0, r0 + (p.digits ? (int)p.plane_rows : 256), fa0);
-            };
-            int it = 0, head = 0;
-            for (int t = pair; t < tiles && ok; t += pairs) {
-                int tm, tn;
-                tile_at(p, t, tm, tn);
-                if (it == 0 && p.pdl) {
-                    // the weight does not depend on the kernel before
-                    head = p.nk < kWStages ? p.nk : kWStages;
-                    for (int k = 0; k < head; ++k) load_w(k, k * kTK, tn);
-                    asm volatile("griddepcontrol.wait;\n" ::: "memory");
+    // 384 x 168 registers at launch = 128 x 40 + 256 x 232
+    if (warp < 4) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
+        if (warp == 0) {
+            if (elect_one()) {
+                auto load_w = [&](int s, int t0, int tn) {
+                    const uint32_t fa0 = mapa_shared(full(s), 0);
+                    const int c0 = tn * 256 + 128 * (int)rank;
+                    if (rank == 0) mbar_expect_tx(full(s), 2 * kWStageBytes);
+                    const uint32_t sb = base + s * kWStageBytes + 2 * kWSlab;
+                    if (p.b_mn) tma_load_2d_pair(sb, &tmW, c0, t0, fa0);
+                    else tma_load_2d_pair(sb, &tmW, t0, c0, fa0);
+                };
+                auto load_x = [&](int s, int t0, int tm) {
+                    const uint32_t fa0 = mapa_shared(full(s), 0);
+                    const uint32_t sa = base + s * kWStageBytes;
+                    const int r0 = tm * mrows + 128 * (int)rank;
+                    tma_load_2d_pair(sa, &tmX, t0, r0, fa0);
+                    tma_load_2d_pair(sa + kWSlab, &tmX, t0, r0 + (p.digits ? (int)p.plane_rows : 256), fa0);
+                };
+                int it = 0, head = 0;
+                for (int t = pair; t < tiles && ok; t += pairs) {
+                    int tm, tn;
+                    tile_at(p, t, tm, tn);
+                    if (it == 0 && p.pdl) {
+                        // the weight does not depend on the kernel before
+                        head = p.nk < kWStages ? p.nk : kWStages;
+                        for (int k = 0; k < head; ++k) load_w(k, k * kTK, tn);
+                        asm volatile("griddepcontrol.wait;\n" ::: "memory");
+                    }
+                    for (int k = 0; k < p.nk && ok; ++k, ++it) {
+                        const int s = it % kWStages;
+                        if (it >= kWStages) ok = mbar_wait(empty(s), ((it / kWStages) & 1) ^ 1, abort_flag);
+                        if (!ok) break;
+                        if (it >= head) load_w(s, k * kTK, tn);
+                        load_x(s, k * kTK, tm);
+                    }
                 }
-                for (int k = 0; k < p.nk && ok; ++k, ++it) {
-                    const int s = it % kWStages;
-                    if (it >= kWStages) ok = mbar_wait(empty(s), ((it / kWStages) & 1) ^ 1, abort_flag);
-                    if (!ok) break;
-                    if (it >= head) load_w(s, k * kTK, tn);
-                    load_x(s, k * kTK, tm);
-                }
+                if (!ok) *abort_flag = 1;
             }
-            if (!ok) *abort_flag = 1;
-        }
-    } else if (warp == 1) {
-        if (rank == 0) {
-            const uint32_t idesc = idesc_i8(256, 256, 0, p.b_mn ? 1u : 0u);
-            const uint64_t bstep = p.b_mn ? 256u : 2u;
-            const uint64_t dX = sdesc(base, 16, 1024), dW = sdesc(base + 2 * kWSlab, 16, 1024);
-            constexpr uint32_t kStageD = kWStageBytes >> 4, kSlabD = kWSlab >> 4;
-            auto mma = [&](uint32_t s, uint32_t h, uint32_t acc) {
-                umma_i8_pair_ktile(tmem + h * 256, dX + s * kStageD + h * kSlabD, dW + s * kStageD, bstep, idesc, acc);
-            };
-            static_assert((kWStages & (kWStages - 1)) == 0, "stage and parity from the running k-tile's bits");
-            uint32_t it = 0, i = 0;
-            for (int t = pair; t < tiles && ok; t += pairs, ++i) {
-                const uint32_t nk = p.nk, lead = nk < kWStages ? nk : kWStages;
-                if (i > 0) ok = __all_sync(0xffffffffu, mbar_wait_cluster(acc_free(0), (i - 1) & 1, abort_flag));
-                for (uint32_t k = 0; k < lead && ok; ++k) {
-                    const uint32_t s = (it + k) % kWStages;
-                    ok = __all_sync(0xffffffffu, mbar_wait_cluster(full(s), ((it + k) / kWStages) & 1, abort_flag));
+        } else if (warp == 1) {
+            if (rank == 0) {
+                const uint32_t idesc = idesc_i8(256, 256, 0, p.b_mn ? 1u : 0u);
+                const uint64_t bstep = p.b_mn ? 256u : 2u;
+                const uint64_t dX = sdesc(base, 16, 1024), dW = sdesc(base + 2 * kWSlab, 16, 1024);
+                constexpr uint32_t kStageD = kWStageBytes >> 4, kSlabD = kWSlab >> 4;
+                auto mma = [&](uint32_t s, uint32_t h, uint32_t acc) {
+                    umma_i8_pair_ktile(tmem + h * 256, dX + s * kStageD + h * kSlabD, dW + s * kStageD, bstep, idesc, acc);
+                };
+                static_assert((kWStages & (kWStages - 1)) == 0, "stage and parity from the running k-tile's bits");
+                uint32_t it = 0, i = 0;
+                for (int t = pair; t < tiles && ok; t += pairs, ++i) {
+                    const uint32_t nk = p.nk, lead = nk < kWStages ? nk : kWStages;
+                    if (i > 0) ok = __all_sync(0xffffffffu, mbar_wait_cluster(acc_free(0), (i - 1) & 1, abort_flag));
+                    for (uint32_t k = 0; k < lead && ok; ++k) {
+                        const uint32_t s = (it + k) % kWStages;
+                        ok = __all_sync(0xffffffffu, mbar_wait_cluster(full(s), ((it + k) / kWStages) & 1, abort_flag));
+                        if (!ok) break;
+                        tc_fence_after();
+                        mma(s, 0, k > 0 ? 1u : 0u);
+                    }
+                    if (ok && i > 0) ok = __all_sync(0xffffffffu, mbar_wait_cluster(acc_free(1), (i - 1) & 1, abort_flag));
                     if (!ok) break;
                     tc_fence_after();
-                    mma(s, 0, k > 0 ? 1u : 0u);
+                    for (uint32_t k = 0; k < lead; ++k) {
+                        const uint32_t s = (it + k) % kWStages;
+                        mma(s, 1, k > 0 ? 1u : 0u);
+                        umma_commit_pair_elect(empty(s), 0x3);
+                    }
+                    for (uint32_t k = lead; k < nk; ++k) {
+                        const uint32_t s = (it + k) % kWStages;
+                        ok = __all_sync(0xffffffffu, mbar_wait_cluster(full(s), ((it + k) / kWStages) & 1, abort_flag));
+                        if (!ok) break;
+                        tc_fence_after();
+                        mma(s, 0, 1u);
+                        mma(s, 1, 1u);
+                        umma_commit_pair_elect(empty(s), 0x3);
+                    }
+                    if (ok) umma_commit_pair_elect(acc_full, 0x3);
+                    it += nk;
                 }
-                if (ok && i > 0) ok = __all_sync(0xffffffffu, mbar_wait_cluster(acc_free(1), (i - 1) & 1, abort_flag));
-                if (!ok) break;
-                tc_fence_after();
-                for (uint32_t k = 0; k < lead; ++k) {
-                    const uint32_t s = (it + k) % kWStages;
-                    mma(s, 1, k > 0 ? 1u : 0u);
-                    umma_commit_pair_elect(empty(s), 0x3);
-                }
-                for (uint32_t k = lead; k < nk; ++k) {
-                    const uint32_t s = (it + k) % kWStages;
-                    ok = __all_sync(0xffffffffu, mbar_wait_cluster(full(s), ((it + k) / kWStages) & 1, abort_flag));
-                    if (!ok) break;
-                    tc_fence_after();
-                    mma(s, 0, 1u);
-                    mma(s, 1, 1u);
-                    umma_commit_pair_elect(empty(s), 0x3);
-                }
-                if (ok) umma_commit_pair_elect(acc_full, 0x3);
-                it += nk;
+                if (!ok) *abort_flag = 1;
             }
-            if (!ok) *abort_flag = 1;
         }
     } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 232;\n");
         if (p.pdl) asm volatile("griddepcontrol.wait;\n" ::: "memory");
-        const int e = threadIdx.x - 64;
-        const int qt = warp & 3, cg = (warp - 2) >> 2;     // TMEM lane quarter, column half
+        const int e = threadIdx.x - 128;
+        const int qt = warp & 3, cg = (warp - 4) >> 2;     // TMEM lane quarter, column half
         const uint32_t lanes = (uint32_t)(32 * qt) << 16;
         const uint32_t free0 = mapa_shared(acc_free(0), 0);
         int i = 0;
@@ -622,55 +632,109 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
             float *cs = cbuf + (i & 1) * 512, *cb = cs + 256;
             cs[e] = p.cscale && n0 + e < p.N ? __ldg(p.cscale + n0 + e) : 1.f;
             cb[e] = p.bias && n0 + e < p.N ? load_any(p.bias, n0 + e, p.dtype) : 0.f;
-            asm volatile("bar.sync 1, 256;\n" ::: "memory");
-            ok = __all_sync(0xffffffffu, mbar_wait_cluster(acc_full, i & 1, abort_flag));
-            if (!ok) break;
-            tc_fence_after();
             const int64_t mblk = (int64_t)tm * mrows + 128 * rank + 32 * qt, mrow = mblk + lane;
-            uint32_t *turn = turns + (warp - 2) * kWTurnWords;
+            uint32_t *turn = turns + (warp - 4) * kWTurnWords;
             float rs[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int64_t m = mrow + 256 * h;
                 rs[h] = m < p.M && (h == 0 || !p.digits) ? __ldcg(p.rscale + m) * p.mul : 0.f;
             }
-            if (p.digits) {
-                for (int c = 0; c < 4; ++c) {
-                    const int col = cg * 128 + c * 32;
-                    uint32_t a[32], b[32];
-                    float v[32];
-                    tmem_ld32(tmem + lanes + col, a);
-                    tmem_ld32(tmem + lanes + 256 + col, b);
-                    if (c == 3) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_cluster(free0), mbar_arrive_cluster(free0 + 8);
-                    }
-#pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        v[j] = __fmaf_rn(__fmul_rn(join_digits((float)(int)a[j], (int)b[j]), rs[0]),
-                                         cs[col + j], cb[col + j]);
-                    store_block(p, mblk, n0 + col, v, turn);
+            asm volatile("bar.sync 1, 256;\n" ::: "memory");
+            ok = __all_sync(0xffffffffu, mbar_wait_cluster(acc_full, i & 1, abort_flag));
+            if (!ok) break;
+            tc_fence_after();
+            // The next tile's MMAs wait for the accumulators: a warp takes its 128
+            // columns of one out at once and frees it before it scales, packs and
+            // stores them.
+            const int c0 = cg * 128;
+            auto release = [&](int h) {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive_cluster(free0 + 8 * h);
+            };
+            auto scaled = [&](int c, float4 x, float r) {   // columns c .. c + 3
+                const float4 s4 = *reinterpret_cast<const float4 *>(cs + c);
+                const float4 b4 = *reinterpret_cast<const float4 *>(cb + c);
+                return make_float4(__fmaf_rn(__fmul_rn(x.x, r), s4.x, b4.x), __fmaf_rn(__fmul_rn(x.y, r), s4.y, b4.y),
+                                   __fmaf_rn(__fmul_rn(x.z, r), s4.z, b4.z), __fmaf_rn(__fmul_rn(x.w, r), s4.w, b4.w));
+            };
+            auto sums4 = [](const uint32_t *v) {
+                return make_float4((float)(int)v[0], (float)(int)v[1], (float)(int)v[2], (float)(int)v[3]);
+            };
+            auto put4 = [](uint32_t *to, float4 v, auto dt) {
+                if constexpr (dt == QLORA_DTYPE_FP32) {
+                    to[0] = __float_as_uint(v.x), to[1] = __float_as_uint(v.y);
+                    to[2] = __float_as_uint(v.z), to[3] = __float_as_uint(v.w);
+                } else {
+                    to[0] = pack2(v.x, v.y, dt == QLORA_DTYPE_FP16);
+                    to[1] = pack2(v.z, v.w, dt == QLORA_DTYPE_FP16);
                 }
-            } else {
+            };
+            auto finish = [&](auto dt) {
+                constexpr bool f32 = dt == QLORA_DTYPE_FP32;
+                constexpr int per = f32 ? 1 : 2, cols = 32 * per;    // values a word, columns a stored block
+                if (p.digits) {
+                    uint32_t out[128 / cols][32];
 #pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    for (int c = 0; c < 4; ++c) {
-                        const int col = cg * 128 + c * 32;
-                        uint32_t a[32];
-                        float v[32];
-                        tmem_ld32(tmem + lanes + h * 256 + col, a);
-                        if (c == 3) {
-                            tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) mbar_arrive_cluster(free0 + 8 * h);
+                    for (int b = 0; b < 128 / cols; ++b) {
+#pragma unroll
+                        for (int g = 0; g < per; ++g) {
+                            const int c = c0 + cols * b + 32 * g;
+                            uint32_t raw[64];
+                            tmem_ld32_issue(tmem + lanes + c, raw);
+                            tmem_ld32_issue(tmem + lanes + 256 + c, raw + 32);
+                            tmem_wait(raw);
+                            if (c == c0 + 96) release(0), release(1);
+#pragma unroll
+                            for (int j = 0; j < 32; j += 4) {
+                                const float4 u = sums4(raw + j), l = sums4(raw + 32 + j);
+                                const float4 x = make_float4(join_digits(u.x, l.x), join_digits(u.y, l.y),
+                                                             join_digits(u.z, l.z), join_digits(u.w, l.w));
+                                put4(out[b] + (32 * g + j) / per, scaled(c + j, x, rs[0]), dt);
+                            }
                         }
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            v[j] = __fmaf_rn(__fmul_rn((float)(int)a[j], rs[h]), cs[col + j], cb[col + j]);
-                        store_block(p, mblk + 256 * h, n0 + col, v, turn);
                     }
-            }
+#pragma unroll
+                    for (int b = 0; b < 128 / cols; ++b)
+                        store_block<f32>(p, mblk, n0 + c0 + cols * b, out[b], turn);
+                } else {
+                    uint32_t raw[128], out[128 / cols][32];
+                    auto take = [&](int h) {
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) tmem_ld32_issue(tmem + lanes + 256 * h + c0 + 32 * c, raw + 32 * c);
+                        tmem_wait(raw);
+                        release(h);
+                    };
+                    auto convert = [&](int h, int b) {
+#pragma unroll
+                        for (int j = 0; j < cols; j += 4)
+                            put4(out[b] + j / per, scaled(c0 + cols * b + j, sums4(raw + cols * b + j), rs[h]), dt);
+                    };
+                    auto store = [&](int h, int b) {
+                        store_block<f32>(p, mblk + 256 * h, n0 + c0 + cols * b, out[b], turn);
+                    };
+                    take(0);
+                    if constexpr (f32) {
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) convert(0, b), store(0, b);
+                        take(1);
+#pragma unroll
+                        for (int b = 0; b < 4; ++b) convert(1, b), store(1, b);
+                    } else {                         // packed, so that the registers hold both
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) convert(0, b);
+                        take(1);
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) store(0, b), convert(1, b);
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) store(1, b);
+                    }
+                }
+            };
+            if (p.dtype == QLORA_DTYPE_BF16) finish(std::integral_constant<int, QLORA_DTYPE_BF16>{});
+            else if (p.dtype == QLORA_DTYPE_FP16) finish(std::integral_constant<int, QLORA_DTYPE_FP16>{});
+            else finish(std::integral_constant<int, QLORA_DTYPE_FP32>{});
         }
         if (!ok) *abort_flag = 1;
     }
@@ -816,7 +880,7 @@ static int launch_int8_wide(const Int8Product &g, uint32_t *d_status, cudaStream
     p.ldo = g.ldo;
     p.dtype = g.dtype;
     const uintptr_t at = reinterpret_cast<uintptr_t>(g.out) | (uintptr_t)(g.ldo * (g.dtype == QLORA_DTYPE_FP32 ? 4 : 2));
-    p.align = at % 32 == 0 ? 32 : (at % 16 == 0 ? 16 : 1);
+    p.aligned = at % 16 == 0;
     p.pdl = g.pdl;
     p.status = d_status;
     const int64_t xrows = g.plane_rows * (g.planes - 1) + g.Q;
