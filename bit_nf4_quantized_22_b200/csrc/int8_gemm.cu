@@ -370,14 +370,14 @@ k_int8_tall(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 // 512 x 256 tile, with two the digits of one 256 x 256 tile.
 // CTA r of the pair holds rows [128 r, +128) of each block and 128 of the
 // columns.  Warp 0 loads (its ring runs on into the next tile), warp 1 of CTA
-// 0 issues the MMAs, warps 2..9 take the sums out of TMEM, scale and store.
+// 0 issues the MMAs, warps 4..11 take the sums out of TMEM, scale and store.
 // The MMAs of the next tile start on an accumulator as soon as it is read:
 // its first four k-tiles go to accumulator 0 before accumulator 1 is needed.
-// 4096 x 4096 x 11008: 128 us (2.9e15 op/s), two digits of it 234 us (3.2e15, with
-// 256 tiles on 74 pairs).  A k-tile brings 48 KB into each SM in about 0.75 us:
-// 9.4 TB/s out of L2 for all of them, which bounds it (the MMAs alone: 0.55 us);
-// a 512 x 256 tile is the most that TMEM holds, so only fewer tiles than pairs in
-// the last round (4.65 rounds there) could be won back.
+// 4096 x 4096 x 11008: 118 us (3.1e15 op/s), two digits of it 232 us (3.2e15).
+// The MMAs bound it: 1024 cycles a k-tile at the full rate of the tensor cores,
+// 164000 of the 182000 cycles of the pairs with five tiles (344 tiles on 74 pairs);
+// a change of tiles idles them for about 3000, the last tile's 256 KB of results
+// take 10000 to leave the pair.  L2 and its links are a third busy.
 constexpr int kWStages = 4;
 constexpr int kWSlab = 128 * kTK;                  // 16 KB: 128 rows of one operand
 constexpr int kWStageBytes = 3 * kWSlab;           // two token slabs, one weight slab
@@ -436,8 +436,10 @@ __device__ __forceinline__ void tile_at(const WideParams &p, int t, int &tm, int
 
 // A warp's block of 32 rows of finished values: lane l has 128 bytes of row
 // m0 + l from column n on, 64 16-bit values in pairs or 32 fp32 values.  They
-// are turned in shared memory (`turn`, the warp's own, XXX), so that a store
-// covers whole lines or, off 16-byte borders, consecutive values of a row.
+// are turned in shared memory (`turn`, the warp's own), so that a store covers
+// whole lines or, off 16-byte borders, consecutive values of a row: two-byte
+// stores to 32 rows at once took longer than the product (an input gradient of
+// 2143 x 10158 x 2222: 289 us, turned 112).
 template <bool F32>
 __device__ __forceinline__ void store_block(const WideParams &p, int64_t m0, int64_t n, const uint32_t *w,
                                             uint32_t *turn) {
@@ -646,7 +648,8 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
             tc_fence_after();
             // The next tile's MMAs wait for the accumulators: a warp takes its 128
             // columns of one out at once and frees it before it scales, packs and
-            // stores them.
+            // stores them, and takes the other before it stores the first (freed
+            // between blocks of 32 columns, 4096 x 4096 x 11008 took 128 us for 118).
             const int c0 = cg * 128;
             auto release = [&](int h) {
                 tc_fence_before();
@@ -763,8 +766,8 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
 // wave of CTAs, for each k-tile of a CTA 0.17 us + 1.8 ns a column alone on its
 // SM, 0.16 us + 2.4 ns where two share it (as N <= 128 lets them: 1024 x 4096 x
 // 4096 takes 27 us in 128 columns, 33 in 256), 1.2 us + 0.2 us a split for a
-// cluster's exchange, half as much again for rows off 128-byte borders (their
-// pieces straddle two lines).  Clusters of big CTAs past 6 do not all find a
+// cluster's exchange, 4 ns a column for its results or 24 where two share the SM,
+// half as much again for rows off 128-byte borders (their pieces straddle two lines).  Clusters of big CTAs past 6 do not all find a
 // place at once (8 splits of N = 176 took twice the time of 6).
 struct TallPlan {
     int nt, splits, per;
@@ -788,7 +791,8 @@ static TallPlan plan_tall(const Int8Product &g, int nk) {
             if ((nk + per - 1) / per != s) continue;
             const int64_t units = tiles * s, waves = (units + slots - 1) / slots;
             const double tile = (units > sms && N <= kTTwoN ? 0.16 + 0.0024 * N : 0.17 + 0.0018 * N) * lines;
-            const double us = 6.0 + (double)waves * (3.0 + per * tile) + (s > 1 ? 1.2 + 0.2 * s : 0.0) + 0.004 * N;
+            const double us = 6.0 + (double)waves * (3.0 + per * tile) + (s > 1 ? 1.2 + 0.2 * s : 0.0) +
+                              (units > sms ? 0.024 : 0.004) * N;
             if (best.nt == 0 || us < best.us) {
                 best = TallPlan{nt, s, per, us};
             }
@@ -909,9 +913,10 @@ static int launch_int8_wide(const Int8Product &g, uint32_t *d_status, cudaStream
     return QLORA_OK;
 }
 
-// The wide kernel takes a k-tile in about 0.76 us (512 x 256 outputs, or 256 x
-// 256 of two digits), each of its CTA pairs a tile after the other: 29 us at
-// 1024 x 4096 x 4096, 54 at 1024 x 4096 x 11008, by the model 30 and 55.
+// The wide kernel: 8.5 us of start and end, and for each of a pair's tiles 1 us and
+// 0.575 us a k-tile (512 x 256 outputs, or 256 x 256 of two digits).  4096 tokens on
+// 1024 x 1024: 14.1 us wide, 16.4 tall; 512 on 11008 x 4096: 29 and 45; 1024 on 4096 x
+// 4096: 28 and 27; 512 on 8192 x 8192: 46 and 41, as the model has them in order.
 int launch_int8_product(const Int8Product &g, uint32_t *d_status, cudaStream_t st) {
     if (g.P <= 0 || g.Q <= 0) return QLORA_OK;
     const int nk = (int)((g.R + kTK - 1) / kTK);
@@ -919,7 +924,7 @@ int launch_int8_product(const Int8Product &g, uint32_t *d_status, cudaStream_t s
     if (!g.q_inner && g.planes <= 2) {
         const int64_t mrows = g.planes == 2 ? 256 : 512, pairs = device_sms() / 2;
         const int64_t tiles = ((g.Q + mrows - 1) / mrows) * ((g.P + 255) / 256);
-        if (6.0 + 0.76 * nk * (double)((tiles + pairs - 1) / pairs) < plan.us) return launch_int8_wide(g, d_status, st);
+        if (8.5 + (1.0 + 0.575 * nk) * (double)((tiles + pairs - 1) / pairs) < plan.us) return launch_int8_wide(g, d_status, st);
     }
     return launch_int8_tall(g, plan, d_status, st);
 }
