@@ -35,20 +35,26 @@ k_int8_quantize(const void *X, int64_t ldx, int64_t rows, int cols, int8_t *code
                 uint32_t *status) {
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     constexpr int esize = DT == QLORA_DTYPE_FP32 ? 4 : 2;
-    const int nv = (cols + kVec - 1) / kVec;
     const int64_t m = WARP ? (int64_t)blockIdx.x * 8 + threadIdx.x / 32 : blockIdx.x;
     if (WARP && m >= rows) return;
     const int tid = WARP ? threadIdx.x & 31 : threadIdx.x, threads = WARP ? 32 : blockDim.x;
     const char *row = static_cast<const char *>(X) + m * ldx * esize;
-    Raw8<DT> keep[STEPS];
+    const uint32_t off = row_offset<FULL>(row);
+    const RowSpan span = row_span<DT, FULL>(off, cols);
+    const int first = span.v0 + tid;
+    Raw8<DT> keep[STEPS], edge{};
     uint32_t am = 0;
+    if (!FULL && tid < span.edges) edge = edge8<DT>(row, span.edge(tid));
+    load_steps<DT, FULL, STEPS>(row, off, first, threads, span.v1, keep);
 #pragma unroll
     for (int i = 0; i < STEPS; ++i)
-        if (i * threads + tid < nv) keep[i] = load8<DT, FULL>(row, i * threads + tid, cols);
-#pragma unroll
-    for (int i = 0; i < STEPS; ++i)
-        if (i * threads + tid < nv) am = absmax8<DT>(keep[i], am);
-    for (int v = STEPS * threads + tid; v < nv; v += threads) am = absmax8<DT>(load8<DT, FULL>(row, v, cols), am);
+        if (first + i * threads < span.v1) am = absmax8<DT>(keep[i], am);
+    for (int v = first + STEPS * threads; v < span.v1; v += threads) {
+        Raw8<DT> x;
+        load_steps<DT, FULL, 1>(row, off, v, threads, span.v1, &x);
+        am = absmax8<DT>(x, am);
+    }
+    if (!FULL) am = absmax8<DT>(edge, am);
     am = absmax_bits<DT>(am);
     am = WARP ? __reduce_max_sync(0xffffffffu, am) : block_max(am);
     const RowCode rc = row_code<DT>(am);
@@ -60,17 +66,23 @@ k_int8_quantize(const void *X, int64_t ldx, int64_t rows, int cols, int8_t *code
     float far = 0.f;
 #pragma unroll
     for (int i = 0; i < STEPS; ++i) {
-        const int v = i * threads + tid;
-        if (v < nv) {
+        const int v = first + i * threads;
+        if (v < span.v1) {
             const uint2 c = encode8<DT>(keep[i], rc, far);
-            store8<FULL>(dst, v * kVec, cols, c.x, c.y);
+            store8<true>(dst, v * kVec, cols, c.x, c.y);
         }
     }
-    for (int v = STEPS * threads + tid; v < nv; v += threads) {
-        const uint2 c = encode8<DT>(load8<DT, FULL>(row, v, cols), rc, far);
-        store8<FULL>(dst, v * kVec, cols, c.x, c.y);
+    for (int v = first + STEPS * threads; v < span.v1; v += threads) {
+        Raw8<DT> x;
+        load_steps<DT, FULL, 1>(row, off, v, threads, span.v1, &x);
+        const uint2 c = encode8<DT>(x, rc, far);
+        store8<true>(dst, v * kVec, cols, c.x, c.y);
     }
-    if (rc.exact || far > kFar) encode_exact<DT>(row, tid, threads, cols, rc.s, dst, nullptr);
+    if (!FULL && tid < span.edges) dst[span.edge(tid)] = (int8_t)(uint8_t)(encode8<DT>(edge, rc, far).x & 255u);
+    if (rc.exact || far > kFar) {
+        encode_exact<DT>(row, first, threads, cols, rc.s, dst, nullptr);
+        if (!FULL && tid < span.edges) dst[span.edge(tid)] = (int8_t)code_exact<DT>(val8(edge, 0), rc.s);
+    }
 }
 
 // Rows of D = dY * scale[column] (RN32) in 16-bit fixed point, q = RN(D / step),
@@ -80,14 +92,14 @@ k_int8_quantize(const void *X, int64_t ldx, int64_t rows, int cols, int8_t *code
 //
 // The scales of one vector's columns (from L1 the second time).
 template <bool FULL>
-__device__ __forceinline__ void digit_scales(const float *__restrict__ cscale, int v, int cols, float (&f)[kVec]) {
-    if (FULL) {
+__device__ __forceinline__ void digit_scales(const float *__restrict__ cscale, int v, float (&f)[kVec]) {
+    if (FULL || (reinterpret_cast<uintptr_t>(cscale) & 15u) == 0) {
         const float4 x = __ldg(reinterpret_cast<const float4 *>(cscale + v * kVec));
         const float4 y = __ldg(reinterpret_cast<const float4 *>(cscale + v * kVec) + 1);
         f[0] = x.x, f[1] = x.y, f[2] = x.z, f[3] = x.w, f[4] = y.x, f[5] = y.y, f[6] = y.z, f[7] = y.w;
     } else {
 #pragma unroll
-        for (int e = 0; e < kVec; ++e) f[e] = __ldg(cscale + (v * kVec + e < cols ? v * kVec + e : cols - 1));
+        for (int e = 0; e < kVec; ++e) f[e] = __ldg(cscale + v * kVec + e);
     }
 }
 template <int DT>
@@ -119,9 +131,7 @@ __device__ __forceinline__ RowDigits row_digits(uint32_t am) {
 // q in +-32639.  With 32768 + 128 in the magic number, the sum's 16 low bits are
 // 256 (d1 + 128) + (d0 + 128): both digits with their top bit flipped, each in
 // a byte of its own.
-template <bool FULL>
-__device__ __forceinline__ void put_digits(float (&d)[kVec], const RowDigits &r, int8_t *hi, int8_t *lo, int e0,
-                                           int cols) {
+__device__ __forceinline__ void put_digits(float (&d)[kVec], const RowDigits &r, int8_t *hi, int8_t *lo) {
     uint32_t q[kVec / 2];
     if (r.up != 1.f) {
 #pragma unroll
@@ -133,8 +143,14 @@ __device__ __forceinline__ void put_digits(float (&d)[kVec], const RowDigits &r,
 #pragma unroll
     for (int i = 0; i < kVec / 2; ++i)
         q[i] = (__byte_perm(__float_as_uint(d[2 * i]), __float_as_uint(d[2 * i + 1]), 0x5410) ^ 0x80808080u) & keep;
-    store8<FULL>(hi, e0, cols, __byte_perm(q[0], q[1], 0x7531), __byte_perm(q[2], q[3], 0x7531));
-    store8<FULL>(lo, e0, cols, __byte_perm(q[0], q[1], 0x6420), __byte_perm(q[2], q[3], 0x6420));
+    *reinterpret_cast<uint2 *>(hi) = make_uint2(__byte_perm(q[0], q[1], 0x7531), __byte_perm(q[2], q[3], 0x7531));
+    *reinterpret_cast<uint2 *>(lo) = make_uint2(__byte_perm(q[0], q[1], 0x6420), __byte_perm(q[2], q[3], 0x6420));
+}
+__device__ __forceinline__ void put_digit(float d, const RowDigits &r, int8_t *hi, int8_t *lo) {
+    const uint32_t q = (__float_as_uint(__fmaf_rn(__fmul_rn(d, r.up), r.inv, kMagic + 32896.f)) ^ 0x8080u) &
+                       (r.fin ? 0xffffu : 0u);
+    *hi = (int8_t)(uint8_t)(q >> 8);
+    *lo = (int8_t)(uint8_t)(q & 255u);
 }
 
 // ROWS rows a CTA: the scales, read for the maxima and again for the digits, are
@@ -146,46 +162,61 @@ k_int8_row_digits(const void *Y, int64_t rows, int cols, const float *__restrict
                   int8_t *planes, int64_t ld, float *steps) {
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
     __shared__ uint32_t part[ROWS][32];
-    const int nv = (cols + kVec - 1) / kVec;
     const int64_t m0 = (int64_t)blockIdx.x * ROWS;
+    const int threads = blockDim.x;
     const char *row[ROWS];
+    uint32_t off[ROWS];
+    RowSpan span{0, 0x7fffffff, 0};     // the rows' common one: they share the scales of a vector
 #pragma unroll
-    for (int i = 0; i < ROWS; ++i)   // a last odd row stands in for its missing neighbour too
+    for (int i = 0; i < ROWS; ++i) {    // a last odd row stands in for its missing neighbour too
         row[i] = static_cast<const char *>(Y) + (m0 + i < rows ? m0 + i : m0) * (int64_t)cols * 2;
-    Raw8<DT> keep[STEPS][ROWS];
-    float top[ROWS] = {}, d[kVec];
+        off[i] = row_offset<FULL>(row[i]);
+        const RowSpan one = row_span<DT, FULL>(off[i], cols);
+        span.v0 = one.v0 > span.v0 ? one.v0 : span.v0;
+        span.v1 = one.v1 < span.v1 ? one.v1 : span.v1;
+    }
+    if (span.v1 <= span.v0) span.v0 = span.v1 = 0;
+    span.edges = cols - (span.v1 - span.v0) * kVec;
+    const int first = span.v0 + threadIdx.x;
+    const bool ends = !FULL && (int)threadIdx.x < span.edges;
+    const int at = ends ? span.edge(threadIdx.x) : 0;
+    Raw8<DT> keep[ROWS][STEPS];
+    float top[ROWS] = {}, d[kVec], edge[ROWS] = {};
+    if (ends) {
+        const float f = __ldg(cscale + at);
 #pragma unroll
-    for (int j = 0; j < STEPS; ++j) {
-        const int v = j * blockDim.x + threadIdx.x;
-#pragma unroll
-        for (int i = 0; i < ROWS; ++i)
-            if (v < nv) keep[j][i] = load8<DT, FULL>(row[i], v, cols);
+        for (int i = 0; i < ROWS; ++i) edge[i] = __fmul_rn(val8(edge8<DT>(row[i], at), 0), f);
     }
 #pragma unroll
+    for (int i = 0; i < ROWS; ++i) load_steps<DT, FULL, STEPS>(row[i], off[i], first, threads, span.v1, keep[i]);
+#pragma unroll
     for (int j = 0; j < STEPS; ++j) {
-        const int v = j * blockDim.x + threadIdx.x;
-        if (v < nv) {
+        const int v = first + j * threads;
+        if (v < span.v1) {
             float f[kVec];
-            digit_scales<FULL>(cscale, v, cols, f);
+            digit_scales<FULL>(cscale, v, f);
 #pragma unroll
             for (int i = 0; i < ROWS; ++i) {
-                digit_products<DT>(keep[j][i], f, d);
+                digit_products<DT>(keep[i][j], f, d);
                 top[i] = digit_max(d, top[i]);
             }
         }
     }
-    for (int v = STEPS * blockDim.x + threadIdx.x; v < nv; v += blockDim.x) {
+    for (int v = first + STEPS * threads; v < span.v1; v += threads) {
         float f[kVec];
-        digit_scales<FULL>(cscale, v, cols, f);
+        digit_scales<FULL>(cscale, v, f);
 #pragma unroll
         for (int i = 0; i < ROWS; ++i) {
-            digit_products<DT>(load8<DT, FULL>(row[i], v, cols), f, d);
+            Raw8<DT> x;
+            load_steps<DT, FULL, 1>(row[i], off[i], v, threads, span.v1, &x);
+            digit_products<DT>(x, f, d);
             top[i] = digit_max(d, top[i]);
         }
     }
     RowDigits r[ROWS];
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
+        if (!FULL) asm("max.NaN.xorsign.abs.f32 %0, %0, %1;\n" : "+f"(top[i]) : "f"(edge[i]));
         const uint32_t m = __reduce_max_sync(0xffffffffu, __float_as_uint(top[i]) & 0x7fffffffu);
         if ((threadIdx.x & 31) == 0) part[i][threadIdx.x >> 5] = m;
     }
@@ -199,23 +230,33 @@ k_int8_row_digits(const void *Y, int64_t rows, int cols, const float *__restrict
     auto put = [&](const Raw8<DT> &x, int i, int v, const float (&f)[kVec]) {
         if (m0 + i >= rows) return;
         digit_products<DT>(x, f, d);
-        put_digits<FULL>(d, r[i], planes + (m0 + i) * ld, planes + (rows + m0 + i) * ld, v * kVec, cols);
+        put_digits(d, r[i], planes + (m0 + i) * ld + v * kVec, planes + (rows + m0 + i) * ld + v * kVec);
     };
 #pragma unroll
     for (int j = 0; j < STEPS; ++j) {
-        const int v = j * blockDim.x + threadIdx.x;
-        if (v < nv) {
+        const int v = first + j * threads;
+        if (v < span.v1) {
             float f[kVec];
-            digit_scales<FULL>(cscale, v, cols, f);
+            digit_scales<FULL>(cscale, v, f);
 #pragma unroll
-            for (int i = 0; i < ROWS; ++i) put(keep[j][i], i, v, f);
+            for (int i = 0; i < ROWS; ++i) put(keep[i][j], i, v, f);
         }
     }
-    for (int v = STEPS * blockDim.x + threadIdx.x; v < nv; v += blockDim.x) {
+    for (int v = first + STEPS * threads; v < span.v1; v += threads) {
         float f[kVec];
-        digit_scales<FULL>(cscale, v, cols, f);
+        digit_scales<FULL>(cscale, v, f);
 #pragma unroll
-        for (int i = 0; i < ROWS; ++i) put(load8<DT, FULL>(row[i], v, cols), i, v, f);
+        for (int i = 0; i < ROWS; ++i) {
+            Raw8<DT> x;
+            load_steps<DT, FULL, 1>(row[i], off[i], v, threads, span.v1, &x);
+            put(x, i, v, f);
+        }
+    }
+    if (ends) {
+#pragma unroll
+        for (int i = 0; i < ROWS; ++i)
+            if (m0 + i < rows)
+                put_digit(edge[i], r[i], planes + (m0 + i) * ld + at, planes + (rows + m0 + i) * ld + at);
     }
 }
 

@@ -15,6 +15,23 @@ struct Raw8 {
     uint32_t w[DT == QLORA_DTYPE_FP32 ? 8 : 4];
 };
 
+// The 8 values that start off bytes into a run of words.
+template <int DT>
+__device__ __forceinline__ void shift8(const uint32_t *in, uint32_t off, Raw8<DT> &r) {
+    constexpr int kWords = sizeof(r.w) / 4;
+    uint32_t t[kWords + 1];
+#pragma unroll
+    for (int i = 0; i < kWords + 1; ++i) {
+        t[i] = in[i];
+        if (off >= 4 && i + 1 < kWords + 4) t[i] = in[i + 1];
+        if (off >= 8 && i + 2 < kWords + 4) t[i] = in[i + 2];
+        if (off >= 12 && i + 3 < kWords + 4) t[i] = in[i + 3];
+    }
+#pragma unroll
+    for (int i = 0; i < kWords; ++i)
+        r.w[i] = DT == QLORA_DTYPE_FP32 ? t[i] : __funnelshift_r(t[i], t[i + 1], 8 * (off & 3u));
+}
+
 // Values [8 v, 8 v + 8) of a row, zeros past its end.  FULL: rows start on
 // 16-byte borders and hold a multiple of 8 values.  Otherwise a row that starts
 // off a border is read in the aligned pieces around the values, where all lie
@@ -44,17 +61,7 @@ __device__ __forceinline__ Raw8<DT> load8(const void *row, int v, int cols) {
             const uint4 x = __ldg(reinterpret_cast<const uint4 *>(at - off) + i);
             in[4 * i] = x.x, in[4 * i + 1] = x.y, in[4 * i + 2] = x.z, in[4 * i + 3] = x.w;
         }
-        uint32_t t[kWords + 1];
-#pragma unroll
-        for (int i = 0; i < kWords + 1; ++i) {
-            t[i] = in[i];
-            if (off >= 4 && i + 1 < kWords + 4) t[i] = in[i + 1];
-            if (off >= 8 && i + 2 < kWords + 4) t[i] = in[i + 2];
-            if (off >= 12 && i + 3 < kWords + 4) t[i] = in[i + 3];
-        }
-#pragma unroll
-        for (int i = 0; i < kWords; ++i)
-            r.w[i] = DT == QLORA_DTYPE_FP32 ? t[i] : __funnelshift_r(t[i], t[i + 1], 8 * (off & 3u));
+        shift8<DT>(in, off, r);
         return r;
     }
     uint32_t one[kVec];
@@ -70,6 +77,66 @@ __device__ __forceinline__ Raw8<DT> load8(const void *row, int v, int cols) {
     for (int i = 0; i < kWords; ++i)
         r.w[i] = DT == QLORA_DTYPE_FP32 ? one[i % kVec] : one[2 * i % kVec] | (one[(2 * i + 1) % kVec] << 16);
     return r;
+}
+
+// A row as the whole vectors [v0, v1) whose (aligned) pieces lie inside it and
+// `edges` <= 32 values around them, one a thread: so no load of a vector waits in
+// a branch for another (bf16 of 8192 x 8191, rows on 16-byte borders: 32 us, with
+// the ends among the vectors 41).
+struct RowSpan {
+    int v0, v1, edges;
+    __device__ __forceinline__ int edge(int i) const { return i < v0 * kVec ? i : i + (v1 - v0) * kVec; }
+};
+template <int DT, bool FULL>
+__device__ __forceinline__ RowSpan row_span(uint32_t off, int cols) {
+    if (FULL) return RowSpan{0, cols / kVec, 0};
+    constexpr int size = DT == QLORA_DTYPE_FP32 ? 4 : 2;
+    RowSpan r{0, cols / kVec, 0};
+    if (off) r.v0 = 1, r.v1 = (cols - (int)(16 - off) / size) / kVec;
+    if (r.v1 <= r.v0) r.v0 = r.v1 = 0;
+    r.edges = cols - (r.v1 - r.v0) * kVec;
+    return r;
+}
+template <bool FULL>
+__device__ __forceinline__ uint32_t row_offset(const void *row) {
+    return FULL ? 0u : (uint32_t)(reinterpret_cast<uintptr_t>(row) & 15u);
+}
+template <int DT>
+__device__ __forceinline__ Raw8<DT> edge8(const void *row, int e) {   // value e, then zeros
+    Raw8<DT> r{};
+    r.w[0] = DT == QLORA_DTYPE_FP32 ? __ldg(static_cast<const uint32_t *>(row) + e)
+                                    : (uint32_t)__ldg(static_cast<const uint16_t *>(row) + e);
+    return r;
+}
+// Vectors v, v + stride, .. of a row whose start lies off bytes past a border.
+// Shifted ones are loaded four at a time: 8192 x 8192 in rows of 8196 take 33 us,
+// two at a time 36, eight at a time (104 registers) 39, one by one 46.
+constexpr int kShiftGroup = 4;
+template <int DT, bool FULL, int STEPS>
+__device__ __forceinline__ void load_steps(const char *row, uint32_t off, int v, int stride, int v1, Raw8<DT> *to) {
+    if (FULL || off == 0) {
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i)
+            if (v + i * stride < v1) to[i] = load8<DT, true>(row, v + i * stride, 0);
+        return;
+    }
+    constexpr int kWords = sizeof(Raw8<DT>) / 4, kGroup = STEPS < kShiftGroup ? STEPS : kShiftGroup;
+#pragma unroll
+    for (int g = 0; g < STEPS; g += kGroup) {
+        uint32_t w[kGroup][kWords + 4];
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i)
+            if (v + (g + i) * stride < v1) {
+                const uint4 *at = reinterpret_cast<const uint4 *>(row + (int64_t)(v + (g + i) * stride) * (kWords * 4) - off);
+#pragma unroll
+                for (int j = 0; j < kWords / 4 + 1; ++j) {
+                    const uint4 t = __ldg(at + j);
+                    w[i][4 * j] = t.x, w[i][4 * j + 1] = t.y, w[i][4 * j + 2] = t.z, w[i][4 * j + 3] = t.w;
+                }
+            }
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) shift8<DT>(w[i], off, to[g + i]);
+    }
 }
 
 template <int DT>
