@@ -133,6 +133,30 @@ def test_quantize_strided_and_out(qlib, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("rows", [3, 600])
+def test_rows_at_every_offset(qlib, dtype, rows):
+    """Rows that start anywhere between two 16-byte borders, from none to several whole vectors inside
+    them, the largest value at either end; the input gradient's rows likewise."""
+    size = 4 if dtype == "fp32" else 2
+    for lo in range(16 // size):
+        for cols in (1, 2, 7, 8, 9, 15, 16, 17, 22, 23, 24, 25, 31, 33, 40, 263, 1030):
+            x = rand(lo + cols, rows * cols + lo + 1, dtype=dtype)[lo:lo + rows * cols].view(rows, cols)
+            x[0, 0], x[1, cols - 1] = 9.0, -9.0
+            check_rows(qlib.int8_quantize(x), x)
+            if dtype == "fp32" or rows > 3 and cols not in (23, 1030):
+                continue
+            w = qlib.Int8Rows(torch.zeros(cols, 16, dtype=torch.int8, device="cuda"), torch.ones(cols, device="cuda"))
+            w.codes[0, 0] = w.codes[cols - 1, 1] = w.codes[cols // 2, 2] = 1
+            dx = qlib.int8_matmul_backward(x, w)
+            want = torch.zeros(rows, 16, dtype=torch.float64, device="cuda")
+            for j, c in enumerate((0, cols - 1, cols // 2)):
+                want[:, j] += x[:, c].double()
+            # 0.51 of a step of the row's fixed point, then the type's own rounding
+            step = x.double().abs().amax(1, keepdim=True) / 32639
+            assert ((dx.double() - want).abs() <= 0.51 * step + (HALF[DT[dtype]] + 2.0 ** -23) * want.abs()).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("rows,cols", [(1, 1), (3, 17), (64, 4096), (5, 1003)])
 def test_dequantize_exact(qlib, rows, cols, dtype):
     q8 = qlib.int8_quantize(rand(rows + cols, rows, cols, dtype="fp32"))
