@@ -382,8 +382,8 @@ constexpr int kWStages = 4;
 constexpr int kWSlab = 128 * kTK;                  // 16 KB: 128 rows of one operand
 constexpr int kWStageBytes = 3 * kWSlab;           // two token slabs, one weight slab
 constexpr int kWThreads = 384, kWEpiThreads = 256;   // warps: loads, MMAs, two idle; eight for the sums
-constexpr int kWTurnPitch = 17;                    // words: 32 rows of 16 words a warp, without bank conflicts
-constexpr int kWTurnWords = 32 * kWTurnPitch;      // or 16 rows of 32 words in swizzled 16-byte pieces
+constexpr int kWTurnPitch = 66;                    // words: 8 rows of 64 words a warp
+constexpr int kWTurnWords = 8 * kWTurnPitch;       // or 16 rows of 32 words in swizzled 16-byte pieces
 constexpr int kWSmemBytes = kWStages * kWStageBytes + 1024 + 256 + 2 * 2 * 256 * 4 + (kWEpiThreads / 32) * kWTurnWords * 4;
 constexpr int kWGroup = 8;                         // row tiles that share a column tile's pass through L2
 
@@ -434,60 +434,96 @@ __device__ __forceinline__ void tile_at(const WideParams &p, int t, int &tm, int
     tn = in / rows;
 }
 
-// A warp's block of 32 rows of finished values: lane l has 128 bytes of row
-// m0 + l from column n on, 64 16-bit values in pairs or 32 fp32 values.  They
+// A warp's block of 32 rows of finished values: lane l has 256 bytes of row
+// m0 + l from column n on, 128 16-bit values in pairs or 64 fp32 values, in w.  They
 // are turned in shared memory (`turn`, the warp's own), so that a store covers
-// whole lines or, off 16-byte borders, consecutive values of a row: two-byte
-// stores to 32 rows at once took longer than the product (an input gradient of
-// 2143 x 10158 x 2222: 289 us, turned 112).
+// whole 16-byte pieces of several rows.
+__device__ __forceinline__ void store_aligned(const WideParams &p, int64_t m0, int64_t byte0, int size, const uint32_t *w,
+                                              uint32_t *turn) {
+    const int lane = threadIdx.x & 31, piece = lane & 7;
+    uint4 *t4 = reinterpret_cast<uint4 *>(turn);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {           // 16 rows of 128 bytes
+        __syncwarp();
+        if (lane >> 4 == half)
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                t4[(lane & 15) * 8 + (i ^ (lane & 7))] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 4 * i + (lane >> 3);
+            const int64_t m = m0 + 16 * half + r;
+            const uint4 v = t4[r * 8 + (piece ^ (r & 7))];
+            if (m < p.M)
+                *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + m * p.ldo * size + byte0 + 16 * piece) = v;
+        }
+    }
+}
+// Rows off 16-byte borders, and ends of rows: 16-byte pieces from the offset in
+// shared memory that makes their stores aligned, then the values around them.
+// Two-byte stores to 32 rows at once took longer than the product (an input
+// gradient of 2143 x 10158 x 2222: 289 us, so 77); 1131 x 1429 x 27441 takes 68 us,
+// two bytes a lane along a row 101, and 1131 x 1429 x 27440, on borders, 58.
+template <bool F32>
+__device__ __forceinline__ void store_ragged(const WideParams &p, int64_t m0, int64_t n, const uint32_t *w,
+                                             uint32_t *turn) {
+    constexpr int kSize = F32 ? 4 : 2;
+    constexpr int kLanes = F32 ? 8 : 16, kRows = 32 / kLanes;      // a row's values around its pieces, rows a store
+    const int lane = threadIdx.x & 31;
+    const int bytes = p.N - n < 256 / kSize ? (int)(p.N - n) * kSize : 256;
+    const int64_t pitch = p.ldo * kSize;
+    const int rows = p.M - m0 < 32 ? (int)(p.M - m0) : 32;
+    uint8_t *const out = static_cast<uint8_t *>(p.out) + m0 * pitch + n * kSize;
+#pragma unroll 1
+    for (int g = 0; g < 32; g += 8) {
+        __syncwarp();
+        if ((lane & 24) == g)
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+                *reinterpret_cast<uint2 *>(turn + (lane & 7) * kWTurnPitch + 2 * j) = make_uint2(w[2 * j], w[2 * j + 1]);
+        __syncwarp();
+        int r = lane >> 4;
+        uint8_t *o = out + (g + r) * pitch;
+#pragma unroll
+        for (int i = 0; i < 4; ++i, r += 2, o += 2 * pitch) {
+            const int b = (int)(-reinterpret_cast<uintptr_t>(o) & 15u) + 16 * (lane & 15);
+            if (g + r < rows && b + 16 <= bytes) {
+                const uint32_t *from = turn + r * kWTurnPitch + (b >> 2);
+                uint32_t v[5];
+#pragma unroll
+                for (int j = 0; j < 5; ++j) v[j] = from[j];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v[j] = F32 ? v[j] : __funnelshift_r(v[j], v[j + 1], 8 * (b & 3));
+                *reinterpret_cast<uint4 *>(o + b) = make_uint4(v[0], v[1], v[2], v[3]);
+            }
+        }
+        r = lane / kLanes;
+        o = out + (g + r) * pitch;
+#pragma unroll
+        for (int i = 0; i < 8 / kRows; ++i, r += kRows, o += kRows * pitch) {
+            const int head = (int)(-reinterpret_cast<uintptr_t>(o) & 15u);
+            const int around = head < bytes ? (bytes - head) & ~15 : bytes;      // bytes of pieces from head on
+            int b = (lane & (kLanes - 1)) * kSize;
+            if (b >= head) b += around;
+            if (g + r < rows && b < bytes) {
+                const uint8_t *from = reinterpret_cast<const uint8_t *>(turn + r * kWTurnPitch) + b;
+                if (F32) *reinterpret_cast<uint32_t *>(o + b) = *reinterpret_cast<const uint32_t *>(from);
+                else *reinterpret_cast<uint16_t *>(o + b) = *reinterpret_cast<const uint16_t *>(from);
+            }
+        }
+    }
+}
 template <bool F32>
 __device__ __forceinline__ void store_block(const WideParams &p, int64_t m0, int64_t n, const uint32_t *w,
                                             uint32_t *turn) {
-    constexpr int kPer = F32 ? 1 : 2, kCols = 32 * kPer;
-    const int lane = threadIdx.x & 31;
+    constexpr int kSize = F32 ? 4 : 2;
     if (n >= p.N || m0 >= p.M) return;               // the same for all lanes
-    if (p.aligned && n + kCols <= p.N) {
-        uint4 *t4 = reinterpret_cast<uint4 *>(turn);
-        const int at = lane >> 3, piece = lane & 7;
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {       // 16 rows, 4 in a store
-            __syncwarp();
-            if (lane >> 4 == half)
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    t4[(lane & 15) * 8 + (i ^ (lane & 7))] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-            __syncwarp();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int r = 4 * i + at;
-                const int64_t m = m0 + 16 * half + r;
-                const uint4 v = t4[r * 8 + (piece ^ (r & 7))];
-                if (m < p.M)
-                    *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + (m * p.ldo + n) * (4 / kPer) + 16 * piece) = v;
-            }
-        }
-        return;
-    }
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {           // 16 words of each row
-        __syncwarp();
-#pragma unroll
-        for (int j = 0; j < 16; ++j) turn[lane * kWTurnPitch + j] = w[16 * half + j];
-        __syncwarp();
-        if constexpr (F32) {                         // two rows a store
-            const int64_t c = n + 16 * half + (lane & 15);
-#pragma unroll 8
-            for (int r = lane >> 4; r < 32; r += 2)
-                if (m0 + r < p.M && c < p.N)
-                    static_cast<uint32_t *>(p.out)[(m0 + r) * p.ldo + c] = turn[r * kWTurnPitch + (lane & 15)];
-        } else {
-            const int64_t c = n + 32 * half + lane;
-#pragma unroll 8
-            for (int r = 0; r < 32; ++r)
-                if (m0 + r < p.M && c < p.N)
-                    static_cast<uint16_t *>(p.out)[(m0 + r) * p.ldo + c] =
-                        (uint16_t)(turn[r * kWTurnPitch + (lane >> 1)] >> (16 * (lane & 1)));
-        }
+    if (p.aligned && n + 256 / kSize <= p.N) {
+        store_aligned(p, m0, n * kSize, kSize, w, turn);
+        store_aligned(p, m0, n * kSize + 128, kSize, w + 32, turn);
+    } else {
+        store_ragged<F32>(p, m0, n, w, turn);
     }
 }
 
@@ -676,33 +712,29 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
             };
             auto finish = [&](auto dt) {
                 constexpr bool f32 = dt == QLORA_DTYPE_FP32;
-                constexpr int per = f32 ? 1 : 2, cols = 32 * per;    // values a word, columns a stored block
+                constexpr int per = f32 ? 1 : 2, cols = 64 * per, blocks = 128 / cols;   // a stored block's columns
+                uint32_t out[blocks][64];
                 if (p.digits) {
-                    uint32_t out[128 / cols][32];
 #pragma unroll
-                    for (int b = 0; b < 128 / cols; ++b) {
+                    for (int g = 0; g < 4; ++g) {
+                        const int c = c0 + 32 * g;
+                        uint32_t raw[64];
+                        tmem_ld32_issue(tmem + lanes + c, raw);
+                        tmem_ld32_issue(tmem + lanes + 256 + c, raw + 32);
+                        tmem_wait(raw);
+                        if (g == 3) release(0), release(1);
 #pragma unroll
-                        for (int g = 0; g < per; ++g) {
-                            const int c = c0 + cols * b + 32 * g;
-                            uint32_t raw[64];
-                            tmem_ld32_issue(tmem + lanes + c, raw);
-                            tmem_ld32_issue(tmem + lanes + 256 + c, raw + 32);
-                            tmem_wait(raw);
-                            if (c == c0 + 96) release(0), release(1);
-#pragma unroll
-                            for (int j = 0; j < 32; j += 4) {
-                                const float4 u = sums4(raw + j), l = sums4(raw + 32 + j);
-                                const float4 x = make_float4(join_digits(u.x, l.x), join_digits(u.y, l.y),
-                                                             join_digits(u.z, l.z), join_digits(u.w, l.w));
-                                put4(out[b] + (32 * g + j) / per, scaled(c + j, x, rs[0]), dt);
-                            }
+                        for (int j = 0; j < 32; j += 4) {
+                            const float4 u = sums4(raw + j), l = sums4(raw + 32 + j);
+                            const float4 x = make_float4(join_digits(u.x, l.x), join_digits(u.y, l.y),
+                                                         join_digits(u.z, l.z), join_digits(u.w, l.w));
+                            put4(out[32 * g / cols] + (32 * g % cols + j) / per, scaled(c + j, x, rs[0]), dt);
                         }
                     }
 #pragma unroll
-                    for (int b = 0; b < 128 / cols; ++b)
-                        store_block<f32>(p, mblk, n0 + c0 + cols * b, out[b], turn);
+                    for (int b = 0; b < blocks; ++b) store_block<f32>(p, mblk, n0 + c0 + cols * b, out[b], turn);
                 } else {
-                    uint32_t raw[128], out[128 / cols][32];
+                    uint32_t raw[128];
                     auto take = [&](int h) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c) tmem_ld32_issue(tmem + lanes + 256 * h + c0 + 32 * c, raw + 32 * c);
@@ -720,18 +752,16 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                     take(0);
                     if constexpr (f32) {
 #pragma unroll
-                        for (int b = 0; b < 4; ++b) convert(0, b), store(0, b);
+                        for (int b = 0; b < 2; ++b) convert(0, b), store(0, b);
                         take(1);
 #pragma unroll
-                        for (int b = 0; b < 4; ++b) convert(1, b), store(1, b);
+                        for (int b = 0; b < 2; ++b) convert(1, b), store(1, b);
                     } else {                         // packed, so that the registers hold both
-#pragma unroll
-                        for (int b = 0; b < 2; ++b) convert(0, b);
+                        convert(0, 0);
                         take(1);
-#pragma unroll
-                        for (int b = 0; b < 2; ++b) store(0, b), convert(1, b);
-#pragma unroll
-                        for (int b = 0; b < 2; ++b) store(1, b);
+                        store(0, 0);
+                        convert(1, 0);
+                        store(1, 0);
                     }
                 }
             };

@@ -155,9 +155,10 @@ __device__ __forceinline__ void put_digit(float d, const RowDigits &r, int8_t *h
 
 // ROWS rows a CTA: the scales, read for the maxima and again for the digits, are
 // most of the traffic inside the SM, and two rows share them (4096 x 11008: 37 us,
-// one row 41 us).
+// one row 41).  64 registers, for two CTAs an SM of long rows too (4258 x 14856: 46
+// us, with 78 registers 67).
 template <int DT, bool FULL, int STEPS, int ROWS>
-__global__ void __launch_bounds__(STEPS == 4 ? 512 : 1024)
+__global__ void __launch_bounds__(STEPS == 4 ? 512 : 1024, STEPS == 4 ? 2 : 1)
 k_int8_row_digits(const void *Y, int64_t rows, int cols, const float *__restrict__ cscale,
                   int8_t *planes, int64_t ld, float *steps) {
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
