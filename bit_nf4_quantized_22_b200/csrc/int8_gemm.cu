@@ -383,8 +383,8 @@ constexpr int kWSlab = 128 * kTK;                  // 16 KB: 128 rows of one ope
 constexpr int kWStageBytes = 3 * kWSlab;           // two token slabs, one weight slab
 constexpr int kWThreads = 384, kWEpiThreads = 256;   // warps: loads, MMAs, two idle; eight for the sums
 constexpr int kWTurnPitch = 66;                    // words: 8 rows of 64 words a warp
-constexpr int kWTurnWords = 8 * kWTurnPitch;       // or 16 rows of 32 words in swizzled 16-byte pieces
-constexpr int kWSmemBytes = kWStages * kWStageBytes + 1024 + 256 + 2 * 2 * 256 * 4 + (kWEpiThreads / 32) * kWTurnWords * 4;
+constexpr int kWTurnBytes = 2560;                  // or a 2 KB block for TMA; a multiple of the swizzle's 512
+constexpr int kWSmemBytes = kWStages * kWStageBytes + 1024 + (kWEpiThreads / 32) * kWTurnBytes + 256 + 2 * 2 * 256 * 4;
 constexpr int kWGroup = 8;                         // row tiles that share a column tile's pass through L2
 
 struct WideParams {
@@ -398,7 +398,7 @@ struct WideParams {
     const void *bias;
     void *out;
     int64_t ldo;
-    int dtype, aligned;        // rows of the output start on 16-byte borders
+    int dtype, aligned;        // rows of the output start on 16-byte borders: TMA stores
     int pdl;
     uint32_t *status;
 };
@@ -434,40 +434,35 @@ __device__ __forceinline__ void tile_at(const WideParams &p, int t, int &tm, int
     tn = in / rows;
 }
 
-// A warp's block of 32 rows of finished values: lane l has 256 bytes of row
-// m0 + l from column n on, 128 16-bit values in pairs or 64 fp32 values, in w.  They
-// are turned in shared memory (`turn`, the warp's own), so that a store covers
-// whole 16-byte pieces of several rows.
-__device__ __forceinline__ void store_aligned(const WideParams &p, int64_t m0, int64_t byte0, int size, const uint32_t *w,
-                                              uint32_t *turn) {
-    const int lane = threadIdx.x & 31, piece = lane & 7;
-    uint4 *t4 = reinterpret_cast<uint4 *>(turn);
+// A warp's block of 32 rows x 64 bytes of finished values, lane l with 16 words of
+// row l, goes out as a TMA store from `turn` (the warp's own 2 KB, swizzled): it
+// leaves while the next block is converted (XXX).
+__device__ __forceinline__ void store_tile(const CUtensorMap *tm, int x, int y, const uint32_t *w, uint32_t turn) {
+    const int lane = threadIdx.x & 31;
+    if (lane == 0) bulk_wait_read();                 // the block before is out of `turn`
+    __syncwarp();
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {           // 16 rows of 128 bytes
-        __syncwarp();
-        if (lane >> 4 == half)
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                t4[(lane & 15) * 8 + (i ^ (lane & 7))] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = 4 * i + (lane >> 3);
-            const int64_t m = m0 + 16 * half + r;
-            const uint4 v = t4[r * 8 + (piece ^ (r & 7))];
-            if (m < p.M)
-                *reinterpret_cast<uint4 *>(static_cast<uint8_t *>(p.out) + m * p.ldo * size + byte0 + 16 * piece) = v;
-        }
+    for (int i = 0; i < 4; ++i)
+        asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};\n" ::"r"(turn + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4)),
+                     "r"(w[4 * i]), "r"(w[4 * i + 1]), "r"(w[4 * i + 2]), "r"(w[4 * i + 3])
+                     : "memory");
+    fence_proxy_async();
+    __syncwarp();
+    if (lane == 0) {
+        tma_store_2d(tm, turn, x, y);
+        bulk_commit();
     }
 }
-// Rows off 16-byte borders, and ends of rows: 16-byte pieces from the offset in
-// shared memory that makes their stores aligned, then the values around them.
+// 32 rows x 256 bytes, 64 words a lane, of rows off 16-byte borders: turned in
+// shared memory, 16-byte pieces from the offset there that makes their stores
+// aligned, then the values around them.
 // Two-byte stores to 32 rows at once took longer than the product (an input
 // gradient of 2143 x 10158 x 2222: 289 us, so 77); 1131 x 1429 x 27441 takes 68 us,
 // two bytes a lane along a row 101, and 1131 x 1429 x 27440, on borders, 58.
 template <bool F32>
 __device__ __forceinline__ void store_ragged(const WideParams &p, int64_t m0, int64_t n, const uint32_t *w,
                                              uint32_t *turn) {
+    if (n >= p.N || m0 >= p.M) return;               // the same for all lanes
     constexpr int kSize = F32 ? 4 : 2;
     constexpr int kLanes = F32 ? 8 : 16, kRows = 32 / kLanes;      // a row's values around its pieces, rows a store
     const int lane = threadIdx.x & 31;
@@ -514,34 +509,22 @@ __device__ __forceinline__ void store_ragged(const WideParams &p, int64_t m0, in
         }
     }
 }
-template <bool F32>
-__device__ __forceinline__ void store_block(const WideParams &p, int64_t m0, int64_t n, const uint32_t *w,
-                                            uint32_t *turn) {
-    constexpr int kSize = F32 ? 4 : 2;
-    if (n >= p.N || m0 >= p.M) return;               // the same for all lanes
-    if (p.aligned && n + 256 / kSize <= p.N) {
-        store_aligned(p, m0, n * kSize, kSize, w, turn);
-        store_aligned(p, m0, n * kSize + 128, kSize, w + 32, turn);
-    } else {
-        store_ragged<F32>(p, m0, n, w, turn);
-    }
-}
-
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWThreads, 1)
-k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW, const WideParams p) {
+k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
+            const __grid_constant__ CUtensorMap tmY, const WideParams p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     const uint32_t raw_addr = smem_u32(smem_raw);
     const uint32_t base = (raw_addr + 1023u) & ~1023u;
     uint8_t *gen_base = smem_raw + (base - raw_addr);
-    const uint32_t bar0 = base + kWStages * kWStageBytes;
+    const uint32_t turns = base + kWStages * kWStageBytes, bar0 = turns + (kWEpiThreads / 32) * kWTurnBytes;
+    uint8_t *bars = gen_base + (bar0 - base);
     auto full = [&](int s) { return bar0 + 8u * s; };                   // CTA 0: both CTAs' bytes landed
     auto empty = [&](int s) { return bar0 + 8u * (kWStages + s); };     // stage free (in both CTAs)
     const uint32_t acc_full = bar0 + 8u * (2 * kWStages);               // a tile's sums are complete (both)
     auto acc_free = [&](int h) { return bar0 + 8u * (2 * kWStages + 1 + h); };   // CTA 0: accumulator h read
-    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(gen_base + kWStages * kWStageBytes + 208);
-    volatile int *abort_flag = reinterpret_cast<volatile int *>(gen_base + kWStages * kWStageBytes + 240);
-    float *cbuf = reinterpret_cast<float *>(gen_base + kWStages * kWStageBytes + 256);   // [2][2][256]
-    uint32_t *turns = reinterpret_cast<uint32_t *>(cbuf + 2 * 2 * 256);
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(bars + 208);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(bars + 240);
+    float *cbuf = reinterpret_cast<float *>(bars + 256);   // [2][2][256]
 
     const int warp = warp_index(), lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
@@ -671,7 +654,8 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
             cs[e] = p.cscale && n0 + e < p.N ? __ldg(p.cscale + n0 + e) : 1.f;
             cb[e] = p.bias && n0 + e < p.N ? load_any(p.bias, n0 + e, p.dtype) : 0.f;
             const int64_t mblk = (int64_t)tm * mrows + 128 * rank + 32 * qt, mrow = mblk + lane;
-            uint32_t *turn = turns + (warp - 4) * kWTurnWords;
+            const uint32_t turn = turns + (warp - 4) * kWTurnBytes;
+            uint32_t *turn_words = reinterpret_cast<uint32_t *>(gen_base + (turn - base));
             float rs[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
@@ -712,8 +696,17 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
             };
             auto finish = [&](auto dt) {
                 constexpr bool f32 = dt == QLORA_DTYPE_FP32;
-                constexpr int per = f32 ? 1 : 2, cols = 64 * per, blocks = 128 / cols;   // a stored block's columns
-                uint32_t out[blocks][64];
+                constexpr int per = f32 ? 1 : 2, cols = 16 * per, count = 128 / cols;   // a block's columns
+                uint32_t out[64 * 2 / per];                                             // a row block's 128 columns
+                auto store = [&](int h, int b) {
+                    if (p.aligned) {
+                        const int64_t n = n0 + c0 + cols * b;
+                        if (n < p.N && mblk + 256 * h < p.M)
+                            store_tile(&tmY, (int)(n * (4 / per)), (int)(mblk + 256 * h), out + 16 * b, turn);
+                    } else if (b % 4 == 3) {
+                        store_ragged<f32>(p, mblk + 256 * h, n0 + c0 + cols * (b - 3), out + 16 * (b - 3), turn_words);
+                    }
+                };
                 if (p.digits) {
 #pragma unroll
                     for (int g = 0; g < 4; ++g) {
@@ -728,11 +721,11 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                             const float4 u = sums4(raw + j), l = sums4(raw + 32 + j);
                             const float4 x = make_float4(join_digits(u.x, l.x), join_digits(u.y, l.y),
                                                          join_digits(u.z, l.z), join_digits(u.w, l.w));
-                            put4(out[32 * g / cols] + (32 * g % cols + j) / per, scaled(c + j, x, rs[0]), dt);
+                            put4(out + (32 * g + j) / per, scaled(c + j, x, rs[0]), dt);
                         }
                     }
 #pragma unroll
-                    for (int b = 0; b < blocks; ++b) store_block<f32>(p, mblk, n0 + c0 + cols * b, out[b], turn);
+                    for (int b = 0; b < count; ++b) store(0, b);
                 } else {
                     uint32_t raw[128];
                     auto take = [&](int h) {
@@ -744,24 +737,29 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                     auto convert = [&](int h, int b) {
 #pragma unroll
                         for (int j = 0; j < cols; j += 4)
-                            put4(out[b] + j / per, scaled(c0 + cols * b + j, sums4(raw + cols * b + j), rs[h]), dt);
-                    };
-                    auto store = [&](int h, int b) {
-                        store_block<f32>(p, mblk + 256 * h, n0 + c0 + cols * b, out[b], turn);
+                            put4(out + 16 * b + j / per, scaled(c0 + cols * b + j, sums4(raw + cols * b + j), rs[h]), dt);
                     };
                     take(0);
                     if constexpr (f32) {
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) convert(0, b), store(0, b);
+                        for (int b = 0; b < count; ++b) convert(0, b), store(0, b);
                         take(1);
 #pragma unroll
-                        for (int b = 0; b < 2; ++b) convert(1, b), store(1, b);
+                        for (int b = 0; b < count; ++b) convert(1, b), store(1, b);
                     } else {                         // packed, so that the registers hold both
-                        convert(0, 0);
+#pragma unroll
+                        for (int b = 0; b < count; ++b) convert(0, b);
                         take(1);
-                        store(0, 0);
-                        convert(1, 0);
-                        store(1, 0);
+                        if (p.aligned) {
+#pragma unroll
+                            for (int b = 0; b < count; ++b) store(0, b), convert(1, b);
+                        } else {
+                            store(0, 3);
+#pragma unroll
+                            for (int b = 0; b < count; ++b) convert(1, b);
+                        }
+#pragma unroll
+                        for (int b = 0; b < count; ++b) store(1, b);
                     }
                 }
             };
@@ -769,6 +767,7 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
             else if (p.dtype == QLORA_DTYPE_FP16) finish(std::integral_constant<int, QLORA_DTYPE_FP16>{});
             else finish(std::integral_constant<int, QLORA_DTYPE_FP32>{});
         }
+        if (lane == 0) bulk_wait_all();              // no memory of this CTA is read behind its end
         if (!ok) *abort_flag = 1;
     }
 
@@ -914,7 +913,7 @@ static int launch_int8_wide(const Int8Product &g, uint32_t *d_status, cudaStream
     p.ldo = g.ldo;
     p.dtype = g.dtype;
     const uintptr_t at = reinterpret_cast<uintptr_t>(g.out) | (uintptr_t)(g.ldo * (g.dtype == QLORA_DTYPE_FP32 ? 4 : 2));
-    p.aligned = at % 16 == 0;
+    p.aligned = at % 16 == 0 && p.N < (1 << 29);          // a TMA coordinate in bytes
     p.pdl = g.pdl;
     p.status = d_status;
     const int64_t xrows = g.plane_rows * (g.planes - 1) + g.Q;
@@ -925,6 +924,11 @@ static int launch_int8_wide(const Int8Product &g, uint32_t *d_status, cudaStream
                                   CU_TENSOR_MAP_SWIZZLE_128B)
                        : make_map(&tW, g.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.R, g.P, g.lda, kTK, 128,
                                   CU_TENSOR_MAP_SWIZZLE_128B));
+    const int size = g.dtype == QLORA_DTYPE_FP32 ? 4 : 2;
+    CUtensorMap tY = tX;                                   // unused for rows off 16-byte borders
+    if (p.aligned)
+        ok = ok && make_map(&tY, g.out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.N * size, p.M, g.ldo * size, 64, 32,
+                            CU_TENSOR_MAP_SWIZZLE_64B);
     if (!ok) return QLORA_EUNSUPPORTED;
     if (set_max_smem(reinterpret_cast<const void *>(k_int8_wide), kWSmemBytes) != cudaSuccess) return QLORA_ECUDA;
     const int64_t tiles = (int64_t)p.mt * p.nt, pairs = device_sms() / 2;
@@ -938,7 +942,7 @@ static int launch_int8_wide(const Int8Product &g, uint32_t *d_status, cudaStream
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = g.pdl ? 1 : 0;
-    if (cudaLaunchKernelEx(&cfg, k_int8_wide, tX, tW, p) != cudaSuccess) return QLORA_ECUDA;
+    if (cudaLaunchKernelEx(&cfg, k_int8_wide, tX, tW, tY, p) != cudaSuccess) return QLORA_ECUDA;
     QLORA_LAUNCH_CHECK();
     return QLORA_OK;
 }
