@@ -347,12 +347,15 @@ def int8_quantize(x: torch.Tensor, out: Int8Rows | None = None,
     one scale a row: a token's activation, or an output channel of a weight Wt."""
     dtype = _any_float(x, "x")
     rows, cols, ldx = _row_stride(x, "x")
-    q = out if out is not None else Int8Rows.empty(rows, cols, x.device)
-    if out is not None and (q.rows, q.cols) != (rows, cols):
-        raise ValueError(f"out: [{rows}, {cols}] is needed")
+    if out is None:
+        q = Int8Rows.empty(rows, cols, x.device)
+        qc = _lib.Int8RowsC(rows, cols, _pitch(cols), q.codes.data_ptr(), q.scales.data_ptr())
+    else:
+        q, qc = out, out.c_struct()
+        if (q.rows, q.cols) != (rows, cols):
+            raise ValueError(f"out: [{rows}, {cols}] is needed")
     with _on(x, q.codes, status):
-        rc = load().int8_quantize(x.data_ptr(), dtype, ldx, ctypes.byref(q.c_struct()), _at(status),
-                                  _raw_stream(x))
+        rc = load().int8_quantize(x.data_ptr(), dtype, ldx, ctypes.byref(qc), _at(status), _raw_stream(x))
         _lib.check(rc, "int8_quantize")
     return q
 
