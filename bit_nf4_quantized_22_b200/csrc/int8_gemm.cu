@@ -792,14 +792,18 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
 }  // namespace
 
 // How a product is cut: columns of B a tile, splits of the reduction.  The
-// least of a model of the measured times (16 to 2300 tokens on weights of 900 to
-// 11008 channels, reductions of 4096 to 26112; within 15% there): 6 us, 3 us a
-// wave of CTAs, for each k-tile of a CTA 0.17 us + 1.8 ns a column alone on its
-// SM, 0.16 us + 2.4 ns where two share it (as N <= 128 lets them: 1024 x 4096 x
-// 4096 takes 27 us in 128 columns, 33 in 256), 1.2 us + 0.2 us a split for a
-// cluster's exchange, 4 ns a column for its results or 24 where two share the SM,
-// half as much again for rows off 128-byte borders (their pieces straddle two lines).  Clusters of big CTAs past 6 do not all find a
-// place at once (8 splits of N = 176 took twice the time of 6).
+// least of a model of the measured times (900 of them: 16 to 4300 tokens on weights
+// of 700 to 11008 channels, reductions of 500 to 28638, 16 to 256 columns, 1 to 8
+// splits; off by 10%, and the plan it finds takes 0.6% longer than the fastest of
+// them): 0.2 us, 4.5 us a wave of CTAs, for each k-tile of a CTA 0.18 us + 0.5 ns a
+// column alone on its SM (0.085 us more where the ring has only four stages: 192
+// columns beat 256), 2 ns a column where two share it (as N <= 128 lets them), 69 ns
+// a column for the results, which the splits divide, 0.7 us + 0.27 us a split for the
+// exchange, the k-tiles half as much again for rows off 128-byte borders (their
+// pieces straddle two lines).  Clusters past 2 leave places free: a wave of them is
+// counted as 0.92 of the SMs' (288 CTAs in clusters of 6 took two waves), and
+// clusters of big CTAs past 6 do not all find a place at once (8 splits of N = 176
+// took twice the time of 6).
 struct TallPlan {
     int nt, splits, per;
     double us;
@@ -820,10 +824,11 @@ static TallPlan plan_tall(const Int8Product &g, int nk) {
         for (int s = 1; s <= most && (s == 1 || 2 * s <= nk); ++s) {
             const int per = (nk + s - 1) / s;
             if ((nk + per - 1) / per != s) continue;
-            const int64_t units = tiles * s, waves = (units + slots - 1) / slots;
-            const double tile = (units > sms && N <= kTTwoN ? 0.16 + 0.0024 * N : 0.17 + 0.0018 * N) * lines;
-            const double us = 6.0 + (double)waves * (3.0 + per * tile) + (s > 1 ? 1.2 + 0.2 * s : 0.0) +
-                              (units > sms ? 0.024 : 0.004) * N;
+            const int64_t units = tiles * s, places = s > 2 ? slots * 23 / 25 : slots;
+            const double waves = (double)((units + places - 1) / places);
+            const double column = units > sms && N <= kTTwoN ? 0.002 : 0.0005;
+            const double tile = (0.18 + column * N + (N > 224 ? 0.085 : 0.0)) * lines;
+            const double us = 0.2 + waves * (4.5 + per * tile + 0.069 * N / s) + (s > 1 ? 0.7 + 0.27 * s : 0.0);
             if (best.nt == 0 || us < best.us) {
                 best = TallPlan{nt, s, per, us};
             }
