@@ -395,7 +395,8 @@ int check_rows8(const int8_rows_t *q) {
         return QLORA_EINVAL;
     if (q->ld < q->cols || q->ld % 16 != 0) return QLORA_EINVAL;
     if (q->rows == 0) return QLORA_OK;
-    if (!q->codes || !aligned16(q->codes) || !q->scales) return QLORA_EINVAL;
+    if (!q->codes || !aligned16(q->codes)) return QLORA_EINVAL;
+    if (!q->scales || (reinterpret_cast<uintptr_t>(q->scales) & 3u) != 0) return QLORA_EINVAL;
     return QLORA_OK;
 }
 
@@ -706,6 +707,7 @@ int qlora_backward_int8(const int8_rows_t *X8, const uint16_t *dY, int64_t M, co
     RC(check_rows8(X8));
     if (X8->rows != M || X8->cols != q->cols) return QLORA_EINVAL;
     if (M > kInt8MaxTerms || q->cols > kInt8MaxTerms) return QLORA_EUNSUPPORTED;
+    if (!aligned16(workspace)) return QLORA_EINVAL;
     return backward_impl(nullptr, X8, dY, M, q, codebook, A, B, r, alpha, pool_group, T_saved, dX, dA, dB, workspace,
                          ws_bytes, d_status, stream);
 }
@@ -769,6 +771,7 @@ int int8_matmul_backward(const uint16_t *dY, int32_t dtype, int64_t M, const int
     if (W->rows > kInt8MaxTerms) return QLORA_EUNSUPPORTED;
     if (M == 0) return QLORA_OK;
     if (!dY || !dX || !aligned_to(dY, dtype) || !aligned_to(dX, dtype)) return QLORA_EINVAL;
+    if (!aligned16(workspace)) return QLORA_EINVAL;
     if (!workspace || layout_grad8(M, *W, nullptr, nullptr) > ws_bytes) return QLORA_EWORKSPACE;
     GradWs ws;
     layout_grad8(M, *W, workspace, &ws);

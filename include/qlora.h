@@ -318,7 +318,8 @@ int int8_matmul(const void *X, int32_t x_dtype, int64_t ldx, const int8_rows_t *
  * rounding to dtype.  A token of dY with a NaN or an infinity gets NaN.  The
  * frozen weight and the bias get no gradient here.
  *   dY    device [M, N] dense, dtype BF16 or FP16;  dX  device [M, K]
- *   workspace/ws_bytes  at least int8_matmul_backward_workspace_size(M, W)
+ *   workspace/ws_bytes  at least int8_matmul_backward_workspace_size(M, W),
+ *                       16-byte aligned
  * Errors: as int8_matmul; EUNSUPPORTED for N > 131072; EWORKSPACE. */
 size_t int8_matmul_backward_workspace_size(int64_t M, const int8_rows_t *W);
 int int8_matmul_backward(const uint16_t *dY, int32_t dtype, int64_t M, const int8_rows_t *W, uint16_t *dX,
@@ -333,7 +334,8 @@ int int8_matmul_backward(const uint16_t *dY, int32_t dtype, int64_t M, const int
  *         by every layer that reads the same x.
  * The other arguments and results are qlora_backward's, dX among them.
  * Errors: as qlora_backward; EINVAL when X8 is not [M, Din]; EUNSUPPORTED for
- * M or Din > 131072.  Workspace: qlora_backward_int8_workspace_size(). */
+ * M or Din > 131072.  Workspace: qlora_backward_int8_workspace_size(),
+ * 16-byte aligned. */
 size_t qlora_backward_int8_workspace_size(int64_t M, const nf4_weight_t *q, int32_t r, int32_t pool_group);
 int qlora_backward_int8(const int8_rows_t *X8, const uint16_t *dY, int64_t M, const nf4_weight_t *q,
                         const float codebook[16], const uint16_t *A, const uint16_t *B, int32_t r, float alpha,

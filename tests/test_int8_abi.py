@@ -27,7 +27,7 @@ def rows(rows=4, cols=100, ld=112, codes=1 << 20, scales=1 << 20):
 
 
 BAD_ROWS = [dict(rows=-1), dict(rows=1 << 31), dict(cols=0), dict(cols=1 << 31, ld=1 << 32), dict(ld=96), dict(ld=100),
-            dict(codes=None), dict(codes=(1 << 20) + 8), dict(scales=None)]
+            dict(codes=None), dict(codes=(1 << 20) + 8), dict(scales=None), dict(scales=(1 << 20) + 2)]
 
 
 def weight(n=64, k=128):
@@ -135,3 +135,10 @@ def test_binding_refusals(lib):
         q.int8_dequantize(r8)
     with pytest.raises(TypeError):
         r8.c_struct()
+
+
+def test_unaligned_workspaces(lib):
+    for n in (1, 4, 8):
+        assert lib.int8_matmul_backward(P, 0, 4, rows(), P, odd(n), 1 << 40, None, None) == QLORA_EINVAL
+        assert lib.qlora_backward_int8(rows(4, 128, 128), P, 4, weight(), codebook(), P, P, 8, 16.0, 1, None, P, P, P,
+                                       odd(n), 1 << 40, None, None) == QLORA_EINVAL
