@@ -811,12 +811,13 @@ struct TallPlan {
 static TallPlan plan_tall(const Int8Product &g, int nk) {
     const int sms = device_sms();
     const int cap = 256 / g.planes / 16 * 16;
-    const int64_t pt = (g.P + kTP - 1) / kTP, least = (g.Q + cap - 1) / cap;
+    const int64_t pt = (g.P + kTP - 1) / kTP;
     const double lines = g.lda % 128 || g.ldb % 128 ? 1.5 : 1.0;
     TallPlan best{};
     int last = 0;
-    for (int64_t tq = least; tq <= 16 * least; ++tq) {
-        const int nt = (int)(((g.Q + tq - 1) / tq + 15) / 16 * 16);
+    for (int at_most = cap; at_most >= 16; at_most -= 16) {
+        const int64_t tq = (g.Q + at_most - 1) / at_most;
+        const int nt = (int)(((g.Q + tq - 1) / tq + 15) / 16 * 16);      // as even as that many tiles can be
         if (nt == last) continue;
         last = nt;
         const int N = nt * g.planes, most = N <= 64 ? kTMaxSplits : 6;
@@ -833,7 +834,6 @@ static TallPlan plan_tall(const Int8Product &g, int nk) {
                 best = TallPlan{nt, s, per, us};
             }
         }
-        if (nt == 16) break;
     }
     return best;
 }
@@ -965,7 +965,9 @@ int launch_int8_product(const Int8Product &g, uint32_t *d_status, cudaStream_t s
     if (!g.q_inner && g.planes <= 2) {
         const int64_t mrows = g.planes == 2 ? 256 : 512, pairs = device_sms() / 2;
         const int64_t tiles = ((g.Q + mrows - 1) / mrows) * ((g.P + 255) / 256);
-        if (8.5 + (1.0 + 0.575 * nk) * (double)((tiles + pairs - 1) / pairs) < plan.us) return launch_int8_wide(g, d_status, st);
+        const bool grid = (g.Q + plan.nt - 1) / plan.nt <= 65535;          // the tall kernel's grid
+        if (!grid || 8.5 + (1.0 + 0.575 * nk) * (double)((tiles + pairs - 1) / pairs) < plan.us)
+            return launch_int8_wide(g, d_status, st);
     }
     return launch_int8_tall(g, plan, d_status, st);
 }
