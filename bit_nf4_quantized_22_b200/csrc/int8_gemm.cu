@@ -955,9 +955,11 @@ static int launch_int8_wide(const Int8Product &g, uint32_t *d_status, cudaStream
 }
 
 // The wide kernel: 8.5 us of start and end, and for each of a pair's tiles 1 us and
-// 0.575 us a k-tile (512 x 256 outputs, or 256 x 256 of two digits).  4096 tokens on
-// 1024 x 1024: 14.1 us wide, 16.4 tall; 512 on 11008 x 4096: 29 and 45; 1024 on 4096 x
-// 4096: 28 and 27; 512 on 8192 x 8192: 46 and 41, as the model has them in order.
+// 0.575 us a k-tile (512 x 256 outputs, or 256 x 256 of two digits), though no less
+// than its results take where another tile follows: 3.5 us and as much for full
+// rows.  4096 tokens on 1024 x 1024: 14.1 us wide, 16.4 tall; 512 on 11008 x 4096: 29
+// and 45; 5 on 131072 x 128: 34 and 18; 384 on 11008 x 8192: 46 and 41; 4096 on 512 x
+// 4096: 26 and 17, as the model has them in order.
 int launch_int8_product(const Int8Product &g, uint32_t *d_status, cudaStream_t st) {
     if (g.P <= 0 || g.Q <= 0) return QLORA_OK;
     const int nk = (int)((g.R + kTK - 1) / kTK);
@@ -965,8 +967,12 @@ int launch_int8_product(const Int8Product &g, uint32_t *d_status, cudaStream_t s
     if (!g.q_inner && g.planes <= 2) {
         const int64_t mrows = g.planes == 2 ? 256 : 512, pairs = device_sms() / 2;
         const int64_t tiles = ((g.Q + mrows - 1) / mrows) * ((g.P + 255) / 256);
+        const int64_t rounds = (tiles + pairs - 1) / pairs;
+        const double tile = 1.0 + 0.575 * nk, rows = g.Q < mrows ? (double)g.Q / mrows : 1.0;
+        const double results = 3.5 + 3.5 * rows;
+        const double us = 8.5 + tile + (double)(rounds - 1) * (tile > results ? tile : results);
         const bool grid = (g.Q + plan.nt - 1) / plan.nt <= 65535;          // the tall kernel's grid
-        if (!grid || 8.5 + (1.0 + 0.575 * nk) * (double)((tiles + pairs - 1) / pairs) < plan.us)
+        if (!grid || us < plan.us)
             return launch_int8_wide(g, d_status, st);
     }
     return launch_int8_tall(g, plan, d_status, st);
