@@ -52,10 +52,12 @@ __global__ void k_pool_split(const uint16_t *__restrict__ X, int64_t M, int64_t 
 
 // fp32 [rows][r] -> the compute dtype's terms of it: v = t0 + t1 (+ t2), each the
 // rounding of what the ones before leave (two: 16 bits in bf16, 22 in fp16;
-// three of bf16: 24).  Columns in groups of gw, a group's terms one after
+// three of bf16: 24).  What is left is raised by up each time: 2^11 keeps the
+// second term of fp16 out of the subnormals that would end it at 2^-25 (a T of
+// 2^-10 to 3e-6 of itself).  Columns in groups of gw, a group's terms one after
 // another, zero padding up to W = groups * gw columns: dst [rows][terms * W].
 __global__ void k_split_f32(const float *__restrict__ src, int64_t rows, int r, int W, int gw, int terms,
-                            uint16_t *__restrict__ dst, bool f16) {
+                            float up, uint16_t *__restrict__ dst, bool f16) {
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= rows * W) return;
     const int64_t row = i / W;
@@ -64,7 +66,7 @@ __global__ void k_split_f32(const float *__restrict__ src, int64_t rows, int r, 
     for (int t = 0; t < terms; ++t) {
         const uint16_t h = enc16(v, f16);
         dst[row * terms * W + (int64_t)(j / gw) * terms * gw + t * gw + j % gw] = h;
-        v -= dec16(h, f16);
+        v = (v - dec16(h, f16)) * up;
     }
 }
 
@@ -179,11 +181,11 @@ int launch_pool_split(const uint16_t *X, int64_t M, int64_t Din, int g, int64_t 
     return QLORA_OK;
 }
 
-int launch_split_f32(const float *src, int64_t rows, int r, int W, int gw, int terms, uint16_t *dst, cudaStream_t st,
-                     bool f16) {
+int launch_split_f32(const float *src, int64_t rows, int r, int W, int gw, int terms, float up, uint16_t *dst,
+                     cudaStream_t st, bool f16) {
     const int64_t n = rows * W;
     if (n == 0) return QLORA_OK;
-    k_split_f32<<<blocks_for(n), 256, 0, st>>>(src, rows, r, W, gw, terms, dst, f16);
+    k_split_f32<<<blocks_for(n), 256, 0, st>>>(src, rows, r, W, gw, terms, up, dst, f16);
     QLORA_LAUNCH_CHECK();
     return QLORA_OK;
 }

@@ -33,8 +33,8 @@ int launch_pad_rows(const uint16_t *src, int64_t rows, int r, int rp, int rep, f
                     uint16_t *dst, cudaStream_t st, bool f16);
 int launch_pool_split(const uint16_t *X, int64_t M, int64_t Din, int g, int64_t ld, uint16_t *hi,
                       uint16_t *lo, cudaStream_t st, bool f16);
-int launch_split_f32(const float *src, int64_t rows, int r, int W, int gw, int terms, uint16_t *dst, cudaStream_t st,
-                     bool f16);
+int launch_split_f32(const float *src, int64_t rows, int r, int W, int gw, int terms, float up, uint16_t *dst,
+                     cudaStream_t st, bool f16);
 int launch_reduce(const float *partial, int splits, int64_t P, int64_t Qp, int H, int Qv,
                   float f32_scale, float *out_f32, int64_t fsp, int64_t fsq, float bf_scale,
                   uint16_t *out_bf16, int64_t bsp, uint16_t *out_split, int64_t sp, cudaStream_t st,
@@ -52,6 +52,7 @@ struct SkinnySeg {
 };
 struct SkinnyFold {
     int terms = 1, gw = 0, groups = 0, most = 0;
+    float down = 1.f;
 };
 int skinny_k_tiles(const SkinnySeg *segs, int nseg);
 void skinny_splits(int64_t P, int64_t Q, int nk, const SkinnyFold &f, int *splits, int *per);
@@ -254,11 +255,12 @@ Prod prod_dB(const Dims &d, const uint16_t *dY, const uint16_t *Tsplit) {
     pr.Q = 2 * d.rp;
     return pr;
 }
-// The same from an 8-bit checkpoint: the terms of T (three of bf16, two of
-// fp16) in groups of up to 64 columns, their products added in the kernel.
+// The same from an 8-bit checkpoint: the terms of T (three of bf16, two of fp16,
+// the second 2^11 up) in groups of up to 64 columns, their products added in the kernel.
 Prod prod_dB8(const Dims &d, const uint16_t *dY, const uint16_t *Tsplit) {
     Prod pr{};
     pr.fold = fold_columns(d.rp, d.f16 ? 2 : 3);
+    if (d.f16) pr.fold.down = 0x1p-11f;
     const int W = pr.fold.groups * pr.fold.gw, cols = pr.fold.terms * W;
     pr.seg[0] = SkinnySeg{dY, d.Dout, 0, Tsplit, cols, 0, cols, d.M};
     pr.nseg = 1;
@@ -672,8 +674,9 @@ static int backward_impl(const uint16_t *X, const int8_rows_t *X8, const uint16_
         }
         const Prod pr = X8 ? prod_dB8(d, dY, w.Tsplit) : prod_dB(d, dY, w.Tsplit);
         if (rc == QLORA_OK)
-            rc = X8 ? launch_split_f32(T32, M, r, (int)pr.Q, pr.fold.gw, pr.fold.terms, w.Tsplit, ast, d.f16)
-                    : launch_split_f32(T32, M, r, d.rp, d.rp, 2, w.Tsplit, ast, d.f16);
+            rc = X8 ? launch_split_f32(T32, M, r, (int)pr.Q, pr.fold.gw, pr.fold.terms, 1.f / pr.fold.down, w.Tsplit, ast,
+                                       d.f16)
+                    : launch_split_f32(T32, M, r, d.rp, d.rp, 2, 1.f, w.Tsplit, ast, d.f16);
         ProdPlan pl;
         if (rc == QLORA_OK) rc = run_prod(pr, w.dBpart, d_status, ast, &pl, d.f16);
         if (rc == QLORA_OK)

@@ -38,8 +38,10 @@ struct SkinnySeg {
 // gw > 0 (16 .. 64): the columns of B come in groups of terms * gw, the terms of
 // gw output columns one after another, and C holds their sums ([P][groups * gw]).
 // most: k-tiles one accumulator takes (gw > 0), or a split has (gw == 0, 0: no bound).
+// down: what a term counts of the one before it.
 struct SkinnyFold {
     int terms = 1, gw = 0, groups = 0, most = 0;
+    float down = 1.f;
 };
 
 namespace {
@@ -60,6 +62,7 @@ struct SkinnyParams {
     int64_t P;
     int N;                 // UMMA N = columns per CTA tile
     int terms, gw, most;   // as SkinnyFold
+    float down;
     int a_kmajor, b_kmajor;  // bit s: segment s's operand is K-major
     int nk0, nk1, per;     // k-tiles per segment, k-tiles per split
     int stages, stage_bytes;
@@ -226,11 +229,13 @@ k_umma_skinny(const __grid_constant__ CUtensorMap tA0, const __grid_constant__ C
 #pragma unroll
             for (int c = 0; c < 64; c += 16) {
                 if (c >= p.gw) break;
+                float weight = 1.f;
                 for (int t = 0; t < p.terms; ++t) {
                     uint32_t v[16];
                     tmem_ld16(at + t * p.gw + c, v);
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) sum[c + i] += __uint_as_float(v[i]);
+                    for (int i = 0; i < 16; ++i) sum[c + i] = __fmaf_rn(weight, __uint_as_float(v[i]), sum[c + i]);
+                    weight *= p.down;
                 }
             }
             tc_fence_before();
@@ -332,6 +337,7 @@ int launch_umma_skinny(const SkinnySeg *segs, int nseg, int64_t P, int64_t Q, in
     prm.terms = f.terms;
     prm.gw = f.gw;
     prm.most = f.most;
+    prm.down = f.down;
     prm.stages = skinny_stages(N);
     prm.stage_bytes = skinny_stage_bytes(N);
     const int smem = skinny_smem_bytes(N);

@@ -418,6 +418,25 @@ def test_checkpoint_backward(qlib, M, K, N, r, g, dtype):
     check_db(db2, Th, 0.51 * A.double().abs().amax(0) / 8355711 * pabs.sum(1, keepdim=True) + 2.0 ** -22 * Th.abs())
 
 
+@pytest.mark.parametrize("scale", [1.0, 2.0 ** -10, 2.0 ** -20])
+def test_checkpoint_small_activations(qlib, scale):
+    """T far below fp16's normal range (2^-14), where its second 16-bit term would be lost: dB to 2e-6
+    in the 2-norm.  T's two terms leave 2^-23 of each value; sums in the tensor cores' accumulator lose
+    7e-7 of their magnitudes at most, three times the 2-norm of a sum of M = 300 random signs' terms,
+    rarely in one direction.  The second term is kept 2^11 up, so its own subnormals end at 2^-24 / 2^11:
+    half of that a value of T at most, over the sum ||E^T dy|| <= ||E|| ||dy||, ||E|| <= sqrt(M r) 2^-36
+    (4e-7 here, which counts at the smallest scale only; without the 2^11 the error there is 3e-5)."""
+    M, K, N, r = 300, 256, 264, 8
+    w, x, A, B, dy = layer_case(qlib, M, K, N, r, 1, "fp16")
+    A = (A.float() * scale).half()
+    x8 = qlib.int8_quantize(x)
+    T = (x8.codes.double() * x8.scales.double()[:, None] @ A.double()).float()
+    _, _, db = qlib.backward(x8, dy, w, A, B, 16.0, 1, T=T, need_dx=False, need_dA=False)
+    want = 16.0 / r * T.double().t() @ dy.double()
+    floor = 16.0 / r * (M * r) ** 0.5 * 2.0 ** -36 * dy.double().norm()
+    assert (db.double() - want).norm() <= 2e-6 * want.norm() + floor
+
+
 def test_checkpoint_gradient_against_differences(qlib):
     """The loss <dY, y(x^, A, B)> is linear in A and in B: central differences of the fp64 layer."""
     M, K, N, r, g = 20, 128, 64, 4, 1
