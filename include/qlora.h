@@ -334,7 +334,8 @@ int int8_matmul_backward(const uint16_t *dY, int32_t dtype, int64_t M, const int
  *         by every layer that reads the same x.
  * The other arguments and results are qlora_backward's, dX among them.
  * Errors: as qlora_backward; EINVAL when X8 is not [M, Din]; EUNSUPPORTED for
- * M or Din > 131072.  Workspace: qlora_backward_int8_workspace_size(),
+ * M or Din > 131072.  A T past fp16's range makes its row of dB NaN in fp16, as
+ * in qlora_backward.  Workspace: qlora_backward_int8_workspace_size(),
  * 16-byte aligned. */
 size_t qlora_backward_int8_workspace_size(int64_t M, const nf4_weight_t *q, int32_t r, int32_t pool_group);
 int qlora_backward_int8(const int8_rows_t *X8, const uint16_t *dY, int64_t M, const nf4_weight_t *q,
