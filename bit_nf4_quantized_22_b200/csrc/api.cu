@@ -441,18 +441,21 @@ int run_T_int8(const Dims &d, const int8_rows_t &x, const uint16_t *A, int8_t *d
     return launch_int8_product(g, status, st);
 }
 
-// Scratch of int8_matmul_backward: the digit planes of dY times the channel scales, a step a token.
+// Scratch of int8_matmul_backward: the digit planes of dY times the channel scales (four; most tokens
+// have two), a step a token and whether it has all four.
 struct GradWs {
     int8_t *planes;
     float *steps;
+    uint8_t *deep;
     int64_t ld;
 };
 size_t layout_grad8(int64_t M, const int8_rows_t &w, void *base, GradWs *out) {
     Bump b(base);
     GradWs x{};
     x.ld = round_up(w.rows, 128);   // whole lines: a TMA row off them takes two
-    x.planes = b.take<int8_t>(2 * M * x.ld);
+    x.planes = b.take<int8_t>(4 * M * x.ld);
     x.steps = b.take<float>(M);
+    x.deep = b.take<uint8_t>(M);
     if (out) *out = x;
     return b.off;
 }
@@ -780,10 +783,10 @@ int int8_matmul_backward(const uint16_t *dY, int32_t dtype, int64_t M, const int
     layout_grad8(M, *W, workspace, &ws);
     cudaStream_t st = (cudaStream_t)stream;
     RC(launch_int8_row_digits(dY, dtype == QLORA_DTYPE_FP16, M, W->rows, W->scales, ws.planes, ws.ld, ws.steps,
-                              st));
+                              ws.deep, st));
     Int8Product g{};
     g.a = W->codes, g.lda = W->ld, g.a_mn = 1;
-    g.b = ws.planes, g.ldb = ws.ld, g.plane_rows = M, g.planes = 2;
+    g.b = ws.planes, g.ldb = ws.ld, g.plane_rows = M, g.planes = 2, g.deep = ws.deep;
     g.P = W->cols, g.Q = M, g.R = W->rows;
     g.qscale = ws.steps, g.mul = 1.f;
     g.out = dX, g.ldo = W->cols, g.dtype = dtype;

@@ -8,7 +8,8 @@
 // or MN-major (p contiguous); B holds `planes` signed base-256 digits of the
 // other operand (int8_rows.cu), K-major.  The products built on it:
 //   y  = x . W^T        p = output channel, q = token, A = W's codes, 1 plane
-//   dX = dY . W         p = input feature,  q = token, A = W's codes (MN-major), 2 planes
+//   dX = dY . W         p = input feature,  q = token, A = W's codes (MN-major), 2 planes,
+//                       4 for the tokens whose digits need them
 //   T  = u . A          p = token, q = rank column, A = u's codes, 3 planes
 //   dA = u^T . G        p = input feature, q = rank column, A = u's codes (MN-major), 3 planes
 #include <cuda.h>
@@ -127,8 +128,26 @@ struct TallParams {
     int pool;              // q_inner: the 64 rows of each group summed
     int dtype, vec;
     int pdl;               // B and the scales come from the kernel before (programmatic launch)
+    const uint8_t *deep;   // planes == 4: the columns q with all of them; the others have two (the first ones)
+    int64_t tiles_q;       // DEEP: tiles of columns
     uint32_t *status;
 };
+
+// Is any of flags[at .. at + n) set?  All threads of the CTA; the first form for all Q columns.
+__device__ __forceinline__ bool any_deep(const uint8_t *flags, int64_t Q) {
+    uint32_t any = 0;
+    const int64_t whole = Q / 16;
+    for (int64_t i = threadIdx.x; i < whole; i += kTThreads) {
+        const uint4 v = __ldcg(reinterpret_cast<const uint4 *>(flags) + i);
+        any |= v.x | v.y | v.z | v.w;
+    }
+    if (threadIdx.x < Q % 16) any |= __ldcg(flags + whole * 16 + threadIdx.x);
+    return __syncthreads_or((int)any) != 0;
+}
+__device__ __forceinline__ bool any_deep(const uint8_t *flags, int64_t at, int n, int64_t Q) {
+    const int64_t q = at + threadIdx.x;
+    return __syncthreads_or((int)threadIdx.x < n && q < Q ? (int)__ldcg(flags + q) : 0) != 0;   // n <= 64
+}
 
 // CTA (x, y, z): rows [128 x, +128) of A, rows [nt y, +nt) of each plane of B,
 // k-tiles [per z, +per).  Warp 0 loads by TMA into a ring of stages, warp 1
@@ -139,6 +158,12 @@ struct TallParams {
 // For few tokens it is bound by the weight's bytes (16 on 8192 x 28672: 41.8 us,
 // 5.6 TB/s), for some by what an SM takes in (an MMA of M = 128 rows re-reads
 // its A for every tile of columns): 256 on 4096 x 4096 take 13 us, 1024 take 27.
+//
+// DEEP: the second launch of an input gradient, for the tiles with a token of
+// four planes among them.  It leaves at once where there is none; else CTA y takes
+// tiles y, y + gridDim.y, .. and stores those tokens' columns alone.  Its ring
+// and accumulator run on from tile to tile.
+template <bool DEEP>
 __global__ void __launch_bounds__(kTThreads)
 k_int8_tall(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const TallParams p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -153,10 +178,12 @@ k_int8_tall(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(gen_base + S * p.stage_bytes + 160);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(gen_base + S * p.stage_bytes + 192);
     float *qs = reinterpret_cast<float *>(gen_base + S * p.stage_bytes + 256);   // [nt <= 256]
+    float *qdeep = qs + 64;                        // planes == 4, nt <= 64: columns with all of them
 
+    if (DEEP && !any_deep(p.deep, p.Q)) return;    // the same for all CTAs
     const int warp = warp_index(), lane = threadIdx.x & 31;
     const int64_t p0 = (int64_t)blockIdx.x * kTP;
-    const int64_t q0 = (int64_t)blockIdx.y * p.nt;
+    int64_t q0 = (int64_t)blockIdx.y * p.nt;
     const int kbeg = blockIdx.z * p.per;
     const int kend = kbeg + p.per < p.nk ? kbeg + p.per : p.nk;
     const int nloc = kend - kbeg;                  // >= 1 by construction
@@ -164,7 +191,7 @@ k_int8_tall(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     const uint32_t rank = blockIdx.z, splits = gridDim.z;
 
     bool ok = true;
-    const int head = nloc < S ? nloc : S;          // k-tiles that find their stage free
+    const int head = DEEP ? 0 : nloc < S ? nloc : S;   // k-tiles that find their stage free, loaded ahead
     // tile i of this CTA into stage s
     auto load_a = [&](int i, int s) {
         const uint32_t sa = base + s * p.stage_bytes;
@@ -207,16 +234,24 @@ k_int8_tall(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
 
+    // stage and round of the ring: of the loads in warp 0, of the MMAs in warp 1
+    int s = warp == 0 ? head % S : 0;
+    uint32_t round = warp == 0 && head == S ? 1u : 0u;
+    uint32_t tile = 0;                             // tiles before this one
+#pragma unroll 1
+    for (int64_t y = blockIdx.y; !DEEP || y < p.tiles_q; y += gridDim.y) {
+    if (DEEP) {
+        q0 = y * p.nt;
+        if (!any_deep(p.deep, q0, p.nt, p.Q)) continue;   // the same for all CTAs of the cluster
+    }
     if (warp == 0) {
         if (leader) {
-            int s = 0;
-            uint32_t parity = 0;
-            for (int i = head; i < nloc; ++i) {
-                ok = mbar_wait(empty_bar(s), parity, abort_flag);
+            for (int i = head; i < nloc && ok; ++i) {
+                if (!DEEP || round > 0) ok = mbar_wait(empty_bar(s), (round & 1) ^ 1, abort_flag);
                 if (!ok) break;
                 load_a(i, s);
                 load_b(i, s);
-                if (++s == S) s = 0, parity ^= 1;
+                if (++s == S) s = 0, ++round;
             }
             if (!ok) *abort_flag = 1;
         }
@@ -226,17 +261,16 @@ k_int8_tall(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         // advances 32 B.  MN-major: rows of 128 p, 8 t a 1 KB group, a step
         // of 32 t advances 4 KB (one 128-wide atom, so no leading stride).
         const uint64_t astep = p.a_mn ? 256u : 2u;
-        uint32_t s = 0, parity = 0;
-        uint64_t ad = sdesc(base, 16, 1024);
         const uint64_t bdiff = kTABytes >> 4, sdiff = p.stage_bytes >> 4;
-        for (int i = 0; i < nloc; ++i) {
-            ok = __all_sync(0xffffffffu, mbar_wait(full_bar(s), parity, abort_flag));   // the warp stays together
+        uint64_t ad = sdesc(base, 16, 1024) + s * sdiff;
+        for (int i = 0; i < nloc && ok; ++i) {
+            ok = __all_sync(0xffffffffu, mbar_wait(full_bar(s), round & 1, abort_flag));   // the warp stays together
             if (!ok) break;
             tc_fence_after();
             umma_i8_ktile(tmem, ad, ad + bdiff, astep, 2, idesc, i > 0 ? 1u : 0u);
             umma_commit_elect(empty_bar(s));
             ad += sdiff;
-            if (++s == (uint32_t)S) s = 0, parity ^= 1, ad = sdesc(base, 16, 1024);
+            if (++s == S) s = 0, ++round, ad = sdesc(base, 16, 1024);
         }
         if (ok) umma_commit_elect(acc_bar);
         else *abort_flag = 1;
@@ -244,7 +278,10 @@ k_int8_tall(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         if (p.pdl) asm volatile("griddepcontrol.wait;\n" ::: "memory");
         for (int c = threadIdx.x - 64; c < p.nt; c += kTThreads - 64)   // not the read-only path: may be the kernel before's
             qs[c] = q0 + c < p.Q ? __ldcg(p.qscale + q0 + c) * p.mul : 0.f;
-        ok = __all_sync(0xffffffffu, mbar_wait(acc_bar, 0, abort_flag));
+        if (p.planes == 4)
+            for (int c = threadIdx.x - 64; c < p.nt; c += kTThreads - 64)
+                qdeep[c] = q0 + c < p.Q && __ldcg(p.deep + q0 + c) ? 1.f : 0.f;
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(acc_bar, tile & 1, abort_flag));
         if (ok) {
             // TMEM -> the idle ring, as int32 [column][128 rows]
             tc_fence_after();
@@ -265,7 +302,10 @@ k_int8_tall(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     __syncwarp();
     tc_fence_before();
     __syncthreads();
-    if (warp == 0 && lane == 0 && *abort_flag) {
+    if (DEEP && warp == 0 && lane == 0 && *abort_flag) {
+        // a wait gave up: time (tens of milliseconds) for this CTA's copies to land
+        for (uint32_t i = 0; i < 20000; ++i) __nanosleep(1000);
+    } else if (!DEEP && warp == 0 && lane == 0 && *abort_flag) {
         // a wait gave up: let this CTA's copies land before its shared memory is released
         for (int s = 0; s < S && s < nloc; ++s) {
             const int last = ((nloc - 1 - s) / S) * S + s;
@@ -303,7 +343,9 @@ k_int8_tall(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             if (q >= p.Q) break;
             int4 t = column(0, c);
             float v[4] = {(float)t.x, (float)t.y, (float)t.z, (float)t.w};
-            if (p.planes == 2) {
+            const bool four = p.planes == 4 && qdeep[c] != 0.f;
+            if (DEEP && !four) continue;
+            if (p.planes == 2 || (p.planes == 4 && !four)) {
                 // as k_int8_wide does, so that a token's gradient does not depend on its batch
                 t = column(1, c);
                 v[0] = join_digits(v[0], (float)t.x), v[1] = join_digits(v[1], (float)t.y);
@@ -355,7 +397,11 @@ k_int8_tall(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         }
     }
     __syncwarp();
-    cluster_sync();   // no CTA leaves while a peer reads its sums
+    if (DEEP) fence_proxy_async();                 // the ring's next copies come after these reads
+    cluster_sync();   // no CTA leaves, or fills its ring again, while a peer reads its sums
+    if (!DEEP) break;
+    ++tile;
+    }
     if (warp == 1) {
         tc_fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;\n" ::"r"(tmem), "r"(p.tmem_cols));
@@ -808,20 +854,20 @@ struct TallPlan {
     int nt, splits, per;
     double us;
 };
-static TallPlan plan_tall(const Int8Product &g, int nk) {
+static TallPlan plan_tall(const Int8Product &g, int planes, int64_t Q, int nk) {
     const int sms = device_sms();
-    const int cap = 256 / g.planes / 16 * 16;
+    const int cap = 256 / planes / 16 * 16;
     const int64_t pt = (g.P + kTP - 1) / kTP;
     const double lines = g.lda % 128 || g.ldb % 128 ? 1.5 : 1.0;
     TallPlan best{};
     int last = 0;
     for (int at_most = cap; at_most >= 16; at_most -= 16) {
-        const int64_t tq = (g.Q + at_most - 1) / at_most;
-        const int nt = (int)(((g.Q + tq - 1) / tq + 15) / 16 * 16);      // as even as that many tiles can be
+        const int64_t tq = (Q + at_most - 1) / at_most;
+        const int nt = (int)(((Q + tq - 1) / tq + 15) / 16 * 16);      // as even as that many tiles can be
         if (nt == last) continue;
         last = nt;
-        const int N = nt * g.planes, most = N <= 64 ? kTMaxSplits : 6;
-        const int64_t slots = (N <= kTTwoN ? 2 : 1) * (int64_t)sms, tiles = pt * ((g.Q + nt - 1) / nt);
+        const int N = nt * planes, most = N <= 64 ? kTMaxSplits : 6;
+        const int64_t slots = (N <= kTTwoN ? 2 : 1) * (int64_t)sms, tiles = pt * ((Q + nt - 1) / nt);
         for (int s = 1; s <= most && (s == 1 || 2 * s <= nk); ++s) {
             const int per = (nk + s - 1) / s;
             if ((nk + per - 1) / per != s) continue;
@@ -838,12 +884,15 @@ static TallPlan plan_tall(const Int8Product &g, int nk) {
     return best;
 }
 
-static int launch_int8_tall(const Int8Product &g, const TallPlan &plan, uint32_t *d_status, cudaStream_t st) {
+// only_deep: the launch of k_int8_tall<true>, after the product of two planes has run.
+static int launch_int8_tall(const Int8Product &g, int planes, const TallPlan &plan, bool only_deep, uint32_t *d_status,
+                            cudaStream_t st) {
     if (g.P <= 0 || g.Q <= 0) return QLORA_OK;
     TallParams p{};
     p.P = g.P;
     p.Q = g.Q;
-    p.planes = g.planes;
+    p.planes = planes;
+    p.deep = g.deep;
     p.plane_rows = g.plane_rows;
     p.nk = (int)((g.R + kTK - 1) / kTK);
     p.a_mn = g.a_mn;
@@ -867,9 +916,10 @@ static int launch_int8_tall(const Int8Product &g, const TallPlan &plan, uint32_t
     p.dtype = g.dtype;
     const int esize = g.dtype == QLORA_DTYPE_FP32 ? 4 : 2;
     p.vec = g.ldo % 4 == 0 && (reinterpret_cast<uintptr_t>(g.out) & (4 * esize - 1)) == 0;
-    p.pdl = g.pdl;
+    p.pdl = g.pdl && !only_deep;
+    p.tiles_q = tiles_q;
     p.status = d_status;
-    const int64_t brows = g.plane_rows * (g.planes - 1) + g.Q;
+    const int64_t brows = g.plane_rows * (planes - 1) + g.Q;
     CUtensorMap tA, tB;
     bool ok = g.a_mn ? make_map(&tA, g.a, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.P, g.R, g.lda, 128, kTK,
                                 CU_TENSOR_MAP_SWIZZLE_128B)
@@ -881,9 +931,16 @@ static int launch_int8_tall(const Int8Product &g, const TallPlan &plan, uint32_t
     const size_t ring = (size_t)p.stages * p.stage_bytes;
     if (ring < (size_t)N * kTP * 4) return QLORA_EUNSUPPORTED;   // the sums take the ring's place
     const int smem = (int)ring + 1024 + 256 + 1024;
-    if (set_max_smem(reinterpret_cast<const void *>(k_int8_tall), smem) != cudaSuccess) return QLORA_ECUDA;
+    auto *k = only_deep ? k_int8_tall<true> : k_int8_tall<false>;
+    if (set_max_smem(reinterpret_cast<const void *>(k), smem) != cudaSuccess) return QLORA_ECUDA;
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3((unsigned)((g.P + kTP - 1) / kTP), (unsigned)tiles_q, (unsigned)splits);
+    const int64_t tiles_p = (g.P + kTP - 1) / kTP;
+    int64_t rows_y = tiles_q;
+    if (only_deep) {   // about one CTA an SM
+        rows_y = device_sms() / (tiles_p * splits);
+        rows_y = rows_y < 1 ? 1 : rows_y < tiles_q ? rows_y : tiles_q;
+    }
+    cfg.gridDim = dim3((unsigned)tiles_p, (unsigned)rows_y, (unsigned)splits);
     cfg.blockDim = dim3(kTThreads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
@@ -895,8 +952,8 @@ static int launch_int8_tall(const Int8Product &g, const TallPlan &plan, uint32_t
     attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = g.pdl ? 2 : 1;
-    if (cudaLaunchKernelEx(&cfg, k_int8_tall, tA, tB, p) != cudaSuccess) return QLORA_ECUDA;
+    cfg.numAttrs = p.pdl ? 2 : 1;
+    if (cudaLaunchKernelEx(&cfg, k, tA, tB, p) != cudaSuccess) return QLORA_ECUDA;
     QLORA_LAUNCH_CHECK();
     return QLORA_OK;
 }
@@ -960,22 +1017,34 @@ static int launch_int8_wide(const Int8Product &g, uint32_t *d_status, cudaStream
 // rows.  4096 tokens on 1024 x 1024: 14.1 us wide, 16.4 tall; 512 on 11008 x 4096: 29
 // and 45; 5 on 131072 x 128: 34 and 18; 384 on 11008 x 8192: 46 and 41; 4096 on 512 x
 // 4096: 26 and 17, as the model has them in order.
+// With deep tokens (which only the device knows): four planes for all of them in one
+// launch where that costs no more than a second launch, for the deep ones alone, does
+// (it finds none in 3 us).
 int launch_int8_product(const Int8Product &g, uint32_t *d_status, cudaStream_t st) {
     if (g.P <= 0 || g.Q <= 0) return QLORA_OK;
     const int nk = (int)((g.R + kTK - 1) / kTK);
-    const TallPlan plan = plan_tall(g, nk);
+    const TallPlan plan = plan_tall(g, g.planes, g.Q, nk);
+    bool wide = false;
+    double us = plan.us;
     if (!g.q_inner && g.planes <= 2) {
         const int64_t mrows = g.planes == 2 ? 256 : 512, pairs = device_sms() / 2;
         const int64_t tiles = ((g.Q + mrows - 1) / mrows) * ((g.P + 255) / 256);
         const int64_t rounds = (tiles + pairs - 1) / pairs;
         const double tile = 1.0 + 0.575 * nk, rows = g.Q < mrows ? (double)g.Q / mrows : 1.0;
         const double results = 3.5 + 3.5 * rows;
-        const double us = 8.5 + tile + (double)(rounds - 1) * (tile > results ? tile : results);
+        const double wide_us = 8.5 + tile + (double)(rounds - 1) * (tile > results ? tile : results);
         const bool grid = (g.Q + plan.nt - 1) / plan.nt <= 65535;          // the tall kernel's grid
-        if (!grid || us < plan.us)
-            return launch_int8_wide(g, d_status, st);
+        wide = !grid || wide_us < plan.us;
+        if (wide) us = wide_us;
     }
-    return launch_int8_tall(g, plan, d_status, st);
+    if (g.deep) {
+        const TallPlan all = plan_tall(g, 4, g.Q, nk);
+        if (all.us <= us + 3.0 && (g.Q + all.nt - 1) / all.nt <= 65535)
+            return launch_int8_tall(g, 4, all, false, d_status, st);
+    }
+    const int rc = wide ? launch_int8_wide(g, d_status, st) : launch_int8_tall(g, g.planes, plan, false, d_status, st);
+    if (rc || !g.deep) return rc;
+    return launch_int8_tall(g, 4, plan_tall(g, 4, g.Q < 64 ? g.Q : 64, nk), true, d_status, st);
 }
 
 }  // namespace qlora

@@ -13,6 +13,7 @@ struct Int8Product {
     int64_t ldb;           // bytes, a multiple of 16
     int64_t plane_rows;
     int planes;            // 1, 2 or 3
+    const uint8_t *deep;   // planes == 2, or NULL: rows q with a 1 here have four planes of digits
     int64_t P, Q, R;       // extents of p, q and the reduction t (R <= 131072)
     const float *qscale;
     const float *pscale;   // or NULL
@@ -43,7 +44,7 @@ __device__ __forceinline__ float load_any(const void *p, int64_t i, int dtype) {
 int launch_int8_quantize(const void *X, int dtype, int64_t ldx, const int8_rows_t &q, uint32_t *d_status,
                          cudaStream_t st);
 int launch_int8_row_digits(const uint16_t *Y, bool f16, int64_t rows, int64_t cols, const float *cscale,
-                           int8_t *planes, int64_t ld, float *steps, cudaStream_t st);
+                           int8_t *planes, int64_t ld, float *steps, uint8_t *deep, cudaStream_t st);
 int launch_int8_col_digits(const void *S, int dtype, int64_t R, int r, const float *f, int8_t *planes, int64_t ld,
                            int rp, int rep, float *steps, cudaStream_t st);
 int launch_int8_dequantize(const int8_rows_t &q, int dtype, void *out, cudaStream_t st);

@@ -10,6 +10,7 @@
 // Where an operand is not 8-bit data already, it is written in fixed point and
 // cut into signed base-256 digits, each an int8 plane of its own:
 //   q = 256 d1 + d0  (16 bits, |q| <= 32639)      rows of dY * channel scale
+//   .. in 32 bits, four digits (|q| <= 2^30)       those that 16 bits would take too much from
 //   q = 65536 d2 + 256 d1 + d0 (|q| <= 8355711)   columns of A, of scale * G
 // so that the integer tensor cores give the product of the full operand, as
 // the digits' products added with their weights.
@@ -86,9 +87,22 @@ k_int8_quantize(const void *X, int64_t ldx, int64_t rows, int cols, int8_t *code
 }
 
 // Rows of D = dY * scale[column] (RN32) in 16-bit fixed point, q = RN(D / step),
-// step = a / 32639, as two digit planes.  A rounding is off by half a step,
-// a / 65278, so a row by at most sqrt(cols) / 65278 of its norm whatever its
-// values (about 4e-5 for normal ones): below the 16-bit output's own rounding.
+// step = a / 32639, as two digit planes; a row that this would take too much from
+// in 32 bits, step the power of two with a / step in [2^29, 2^30), as four
+// (`deep`: its planes then hold those digits instead).
+//
+// What 16 bits take from a row is known once its digits are: with h half a step of
+// the result's type (bf16 2^-8, fp16 2^-11) and ||D|| from the upper digits,
+//   the roundings' noise, sqrt(cols / 12) step              <= h / 4 ||D||
+//   the values under 8 steps, a quarter of a step each      <= h / 4 ||D||
+//   the roundings' sum, which weights with a mean multiply  <= h / 2 ||D||
+// Normal rows pass (4096 to 131072 columns: noise 3e-5 to 5e-5 of their norm), a
+// loss's softmax - onehot does not: thousands of values under half a step, all of
+// one sign, would be lost. The three are sums of integers, so a row's choice is its own
+// whatever kernel, thread or batch makes it.  32 bits keep every value to
+// max 2^-30: 131072 of them to 2^-13 of the largest, and D's own fp32 where a
+// value is within 2^-6 of it.  Rows below 2^-111, whose 16-bit step would be subnormal
+// (it would lose up to all of its own bits), are cut in 32 bits too.
 //
 // The scales of one vector's columns (from L1 the second time).
 template <bool FULL>
@@ -127,30 +141,127 @@ __device__ __forceinline__ RowDigits row_digits(uint32_t am) {
     r.step = r.fin ? __fdiv_rn(a, 32639.f) / r.up : __uint_as_float(0x7fffffffu);
     return r;
 }
+// What 16 bits take from a row: the upper digits' squares, 128 times the roundings'
+// sum (mod 2^32, as bit patterns of magic numbers), the values under 8 steps.
+struct DigitLoss {
+    uint32_t squares, sum, small;
+};
+constexpr uint32_t kDigitZero = 0x4b408080u;   // kMagic + 32896.f: q = 0
+// Each value adds (kMagic + 128 x)'s bits less 128 times those of q.
+constexpr uint32_t kLossBase = 0x4b400000u - 128u * kDigitZero;
+
+__device__ __forceinline__ void digit_loss(float d, float t, float inv128, DigitLoss &l) {
+    // |128 x| <= 4177792.5 < 2^22: the magic addition rounds it to an integer too
+    l.sum += __float_as_uint(__fmaf_rn(d, inv128, kMagic)) - 128u * __float_as_uint(t);
+    l.small += __float_as_uint(t) - (kDigitZero - 7u) <= 14u ? 1u : 0u;
+}
 // |d up inv| <= 32639 (1 + 2^-23), so the magic addition rounds it to an integer
 // q in +-32639.  With 32768 + 128 in the magic number, the sum's 16 low bits are
 // 256 (d1 + 128) + (d0 + 128): both digits with their top bit flipped, each in
 // a byte of its own.
-__device__ __forceinline__ void put_digits(float (&d)[kVec], const RowDigits &r, int8_t *hi, int8_t *lo) {
+__device__ __forceinline__ void put_digits(float (&d)[kVec], const RowDigits &r, int8_t *hi, int8_t *lo, DigitLoss &l) {
     uint32_t q[kVec / 2];
     if (r.up != 1.f) {
 #pragma unroll
         for (int e = 0; e < kVec; ++e) d[e] = __fmul_rn(d[e], r.up);
     }
+    const float inv128 = r.inv * 128.f;
 #pragma unroll
-    for (int e = 0; e < kVec; ++e) d[e] = __fmaf_rn(d[e], r.inv, kMagic + 32896.f);
+    for (int e = 0; e < kVec; ++e) {
+        const float t = __fmaf_rn(d[e], r.inv, kMagic + 32896.f);
+        digit_loss(d[e], t, inv128, l);
+        d[e] = t;
+    }
     const uint32_t keep = r.fin ? 0xffffffffu : 0u;
 #pragma unroll
     for (int i = 0; i < kVec / 2; ++i)
         q[i] = (__byte_perm(__float_as_uint(d[2 * i]), __float_as_uint(d[2 * i + 1]), 0x5410) ^ 0x80808080u) & keep;
-    *reinterpret_cast<uint2 *>(hi) = make_uint2(__byte_perm(q[0], q[1], 0x7531), __byte_perm(q[2], q[3], 0x7531));
+    const uint2 upper = make_uint2(__byte_perm(q[0], q[1], 0x7531), __byte_perm(q[2], q[3], 0x7531));
+    l.squares = __dp4a((int)upper.x, (int)upper.x, (int)l.squares);
+    l.squares = __dp4a((int)upper.y, (int)upper.y, (int)l.squares);
+    *reinterpret_cast<uint2 *>(hi) = upper;
     *reinterpret_cast<uint2 *>(lo) = make_uint2(__byte_perm(q[0], q[1], 0x6420), __byte_perm(q[2], q[3], 0x6420));
 }
-__device__ __forceinline__ void put_digit(float d, const RowDigits &r, int8_t *hi, int8_t *lo) {
-    const uint32_t q = (__float_as_uint(__fmaf_rn(__fmul_rn(d, r.up), r.inv, kMagic + 32896.f)) ^ 0x8080u) &
-                       (r.fin ? 0xffffu : 0u);
-    *hi = (int8_t)(uint8_t)(q >> 8);
+__device__ __forceinline__ void put_digit(float d, const RowDigits &r, int8_t *hi, int8_t *lo, DigitLoss &l) {
+    d = __fmul_rn(d, r.up);
+    const float t = __fmaf_rn(d, r.inv, kMagic + 32896.f);
+    digit_loss(d, t, r.inv * 128.f, l);
+    const uint32_t q = (__float_as_uint(t) ^ 0x8080u) & (r.fin ? 0xffffu : 0u);
+    const int upper = (int8_t)(uint8_t)(q >> 8);
+    l.squares += (uint32_t)(upper * upper);
+    *hi = (int8_t)upper;
     *lo = (int8_t)(uint8_t)(q & 255u);
+}
+
+// Do 16 bits take too much?  squares counts ||D||^2 in steps of 256: with h^2 =
+// 2^-16 (bf16) or 2^-22 the three bounds are 4 cols <= 3 squares (or their 2^-6),
+// small^2 <= squares and sum^2 <= 2^12 squares.
+__device__ __forceinline__ bool loss_matters(uint32_t squares, int sum, uint32_t small, int cols, bool f16) {
+    const uint64_t s = f16 ? squares >> 6 : squares;
+    return 4 * (uint64_t)cols > 3 * s || (uint64_t)small * small > s ||
+           (uint64_t)((int64_t)sum * sum) > s << 12;
+}
+
+__device__ __forceinline__ uint32_t block_sum(uint32_t v, uint32_t *part) {   // part: 32 words, free before and after
+    v = __reduce_add_sync(0xffffffffu, v);
+    __syncthreads();
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    return __reduce_add_sync(0xffffffffu, (threadIdx.x & 31) < blockDim.x >> 5 ? part[threadIdx.x & 31] : 0u);
+}
+
+// The power of two of a deep row's step, and values over it.  2^-149 is the unit
+// of D itself: no smaller step is needed.
+constexpr uint32_t kTinyRow = 0x08000000u;     // 2^-111, as bits
+struct DeepStep {
+    float step, mul0, mul1;
+};
+__device__ __forceinline__ DeepStep deep_step(uint32_t am) {
+    int k = (int)(am >> 23) - 127 - 29;
+    k = k < -149 ? -149 : k;
+    const int a = -k / 2, b = -k - a;    // in two factors: 2^149 is past fp32's range
+    DeepStep s;
+    s.step = __uint_as_float(k >= -126 ? (uint32_t)(k + 127) << 23 : 1u << (k + 149));
+    s.mul0 = __uint_as_float((uint32_t)(a + 127) << 23);
+    s.mul1 = __uint_as_float((uint32_t)(b + 127) << 23);
+    return s;
+}
+
+// A row that the whole CTA finds beyond 16 bits: zeros, which lose nothing, come out of the values under 8
+// steps; if too much is still lost, the row's four planes.  Out of line: ordinary rows do not come here.
+template <int DT>
+__device__ __noinline__ bool deep_row(const char *row, int cols, const float *__restrict__ cscale, uint32_t am,
+                                      uint32_t squares, int sum, uint32_t small, int8_t *planes, int64_t plane,
+                                      uint32_t *part) {
+    const int nv = (cols + kVec - 1) / kVec;
+    uint32_t zeros = 0;
+    for (int v = threadIdx.x; v < nv; v += blockDim.x) {
+        const Raw8<DT> r = load8<DT, false>(row, v, cols);
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) zeros += v * kVec + e < cols && val8(r, e) == 0.f;
+    }
+    zeros = block_sum(zeros, part);
+    if (am >= kTinyRow && !loss_matters(squares, sum, small - zeros, cols - (int)zeros, DT == QLORA_DTYPE_FP16))
+        return false;
+    const DeepStep ds = deep_step(am);
+    for (int v = threadIdx.x; v < nv; v += blockDim.x) {
+        const Raw8<DT> r = load8<DT, false>(row, v, cols);
+        uint32_t d[4][2] = {};
+#pragma unroll
+        for (int e = 0; e < kVec; ++e) {
+            const float x = __fmul_rn(val8(r, e), __ldg(cscale + (v * kVec + e < cols ? v * kVec + e : cols - 1)));
+            int q = __float2int_rn(x * ds.mul0 * ds.mul1);           // |q| <= 2^30
+#pragma unroll
+            for (int p = 3; p >= 0; --p) {
+                const int b = (int)(int8_t)(uint8_t)q;
+                q = (q - b) >> 8;
+                d[p][e / 4] |= (uint32_t)(uint8_t)b << (8 * (e & 3));
+            }
+        }
+#pragma unroll
+        for (int p = 0; p < 4; ++p) store8<false>(planes + p * plane, v * kVec, cols, d[p][0], d[p][1]);
+    }
+    return true;
 }
 
 // ROWS rows a CTA: the scales, read for the maxima and again for the digits, are
@@ -160,9 +271,9 @@ __device__ __forceinline__ void put_digit(float d, const RowDigits &r, int8_t *h
 template <int DT, bool FULL, int STEPS, int ROWS>
 __global__ void __launch_bounds__(STEPS == 4 ? 512 : 1024, STEPS == 4 ? 2 : 1)
 k_int8_row_digits(const void *Y, int64_t rows, int cols, const float *__restrict__ cscale,
-                  int8_t *planes, int64_t ld, float *steps) {
+                  int8_t *planes, int64_t ld, float *steps, uint8_t *deep) {
     asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory");
-    __shared__ uint32_t part[ROWS][32];
+    __shared__ uint32_t part[ROWS][32], sums[ROWS][3][32];
     const int64_t m0 = (int64_t)blockIdx.x * ROWS;
     const int threads = blockDim.x;
     const char *row[ROWS];
@@ -215,6 +326,8 @@ k_int8_row_digits(const void *Y, int64_t rows, int cols, const float *__restrict
         }
     }
     RowDigits r[ROWS];
+    DigitLoss loss[ROWS] = {};
+    uint32_t am[ROWS];
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
         if (!FULL) asm("max.NaN.xorsign.abs.f32 %0, %0, %1;\n" : "+f"(top[i]) : "f"(edge[i]));
@@ -225,13 +338,13 @@ k_int8_row_digits(const void *Y, int64_t rows, int cols, const float *__restrict
 #pragma unroll
     for (int i = 0; i < ROWS; ++i) {
         const uint32_t m = (threadIdx.x & 31) < blockDim.x >> 5 ? part[i][threadIdx.x & 31] : 0u;
-        r[i] = row_digits(__reduce_max_sync(0xffffffffu, m));
-        if (threadIdx.x == 0 && m0 + i < rows) steps[m0 + i] = r[i].step;
+        am[i] = __reduce_max_sync(0xffffffffu, m);
+        r[i] = row_digits(am[i]);
     }
     auto put = [&](const Raw8<DT> &x, int i, int v, const float (&f)[kVec]) {
         if (m0 + i >= rows) return;
         digit_products<DT>(x, f, d);
-        put_digits(d, r[i], planes + (m0 + i) * ld + v * kVec, planes + (rows + m0 + i) * ld + v * kVec);
+        put_digits(d, r[i], planes + (m0 + i) * ld + v * kVec, planes + (rows + m0 + i) * ld + v * kVec, loss[i]);
     };
 #pragma unroll
     for (int j = 0; j < STEPS; ++j) {
@@ -257,7 +370,35 @@ k_int8_row_digits(const void *Y, int64_t rows, int cols, const float *__restrict
 #pragma unroll
         for (int i = 0; i < ROWS; ++i)
             if (m0 + i < rows)
-                put_digit(edge[i], r[i], planes + (m0 + i) * ld + at, planes + (rows + m0 + i) * ld + at);
+                put_digit(edge[i], r[i], planes + (m0 + i) * ld + at, planes + (rows + m0 + i) * ld + at, loss[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < ROWS; ++i) {
+        const uint32_t w[3] = {loss[i].squares, loss[i].sum, loss[i].small};
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+            const uint32_t t = __reduce_add_sync(0xffffffffu, w[k]);
+            if ((threadIdx.x & 31) == 0) sums[i][k][threadIdx.x >> 5] = t;
+        }
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int i = 0; i < ROWS && m0 + i < rows; ++i) {
+        uint32_t w[3];
+#pragma unroll
+        for (int k = 0; k < 3; ++k)
+            w[k] = __reduce_add_sync(0xffffffffu, (threadIdx.x & 31) < blockDim.x >> 5 ? sums[i][k][threadIdx.x & 31] : 0u);
+        const int sum = (int)(w[1] - (uint32_t)cols * kLossBase);
+        const uint32_t a = i == 0 ? am[0] : am[ROWS - 1];
+        // the same for the whole CTA; a zero row and one that is not finite have no digits to lose
+        const bool is_deep = a > 0 && a < 0x7f800000u &&
+                             (a < kTinyRow || loss_matters(w[0], sum, w[2], cols, DT == QLORA_DTYPE_FP16)) &&
+                             deep_row<DT>(i == 0 ? row[0] : row[ROWS - 1], cols, cscale, a, w[0], sum, w[2],
+                                          planes + (m0 + i) * ld, rows * ld, part[0]);
+        if (threadIdx.x == 0) {
+            steps[m0 + i] = is_deep ? deep_step(a).step : i == 0 ? r[0].step : r[ROWS - 1].step;
+            deep[m0 + i] = is_deep;
+        }
     }
 }
 
@@ -461,14 +602,14 @@ int launch_quantize(const void *X, int64_t ldx, const int8_rows_t &q, uint32_t *
 
 template <int DT, bool FULL>
 int launch_row_digits(const uint16_t *Y, int64_t rows, int64_t cols, const float *cscale, int8_t *planes, int64_t ld,
-                      float *steps, cudaStream_t st) {
+                      float *steps, uint8_t *deep, cudaStream_t st) {
     const int n = row_steps(rows, cols, false), per = n == 8 ? 2 : 1;
     auto *k = n == 1   ? k_int8_row_digits<DT, FULL, 1, 1>
               : n == 2 ? k_int8_row_digits<DT, FULL, 2, 1>
                        : k_int8_row_digits<DT, FULL, 4, 2>;
     const int t = n == 8 ? row_cta(cols, 4) : row_cta(cols, n);
     k<<<(unsigned)((rows + per - 1) / per), n == 8 && t > 512 ? 512 : t, 0, st>>>(Y, rows, (int)cols, cscale, planes, ld,
-                                                                                steps);
+                                                                                steps, deep);
     QLORA_LAUNCH_CHECK();
     return QLORA_OK;
 }
@@ -488,12 +629,12 @@ int launch_int8_quantize(const void *X, int dtype, int64_t ldx, const int8_rows_
 }
 
 int launch_int8_row_digits(const uint16_t *Y, bool f16, int64_t rows, int64_t cols, const float *cscale,
-                           int8_t *planes, int64_t ld, float *steps, cudaStream_t st) {
+                           int8_t *planes, int64_t ld, float *steps, uint8_t *deep, cudaStream_t st) {
     const bool full = ((reinterpret_cast<uintptr_t>(Y) | reinterpret_cast<uintptr_t>(cscale)) & 15u) == 0 &&
                       cols % kVec == 0;
     auto *f = f16 ? (full ? launch_row_digits<QLORA_DTYPE_FP16, true> : launch_row_digits<QLORA_DTYPE_FP16, false>)
                   : (full ? launch_row_digits<QLORA_DTYPE_BF16, true> : launch_row_digits<QLORA_DTYPE_BF16, false>);
-    return f(Y, rows, cols, cscale, planes, ld, steps, st);
+    return f(Y, rows, cols, cscale, planes, ld, steps, deep, st);
 }
 
 int launch_int8_col_digits(const void *S, int dtype, int64_t R, int r, const float *f, int8_t *planes, int64_t ld,

@@ -312,10 +312,16 @@ int int8_matmul(const void *X, int32_t x_dtype, int64_t ldx, const int8_rows_t *
 /* int8_matmul_backward -- the gradient of int8_matmul for its tokens, straight
  * through their rounding:  dX = dY . dequant(W),
  *   dX[m][k] = RN_dtype(sum_n dY[m][n] sw[n] cw[n][k]).
- * dY sw is taken in 16-bit fixed point per token (step max / 32639), its two
- * 8-bit digits go through the integer tensor cores and the sums are exact, so
- * the result is within (step / 2) sum_n |cw[n][k]| of the exact one before its
- * rounding to dtype.  A token of dY with a NaN or an infinity gets NaN.  The
+ * dY sw is taken in fixed point per token, its 8-bit digits go through the
+ * integer tensor cores and the sums are exact, so the result is within
+ * (step / 2) sum_n |cw[n][k]| of the exact one before its rounding to dtype.
+ * The fixed point has 16 bits (step max / 32639) for a token that loses little
+ * in them: with h = 2^-8 (bf16) or 2^-11 (fp16), the roundings' noise and the
+ * values under 8 steps at most h / 4 of the token's 2-norm each, the roundings'
+ * sum h / 2.  A token that would lose more (softmax - onehot over many
+ * channels, one value far above the others) has 32 bits (a power of two, at
+ * most max 2^-29), at about three times the cost.  Which of the two depends on
+ * the token and the channel scales alone.  A token of dY with a NaN or an infinity gets NaN.  The
  * frozen weight and the bias get no gradient here.
  *   dY    device [M, N] dense, dtype BF16 or FP16;  dX  device [M, K]
  *   workspace/ws_bytes  at least int8_matmul_backward_workspace_size(M, W),

@@ -1,0 +1,126 @@
+"""8-bit rows where their fixed point and their sums are pressed hardest.
+
+Tolerances: half a step of each output type (bf16 2^-8 of the value at most, fp16 2^-11), plus what
+each comment counts."""
+import pytest
+import torch
+
+from test_gpu_int8 import DT, HALF, rand
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------------------ input gradient
+def head(qlib, N, K, mean, seed=1):
+    """A weight of N channels whose values have a mean, in units of their deviation."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    w = torch.randn(N, K, generator=g, device="cuda") + mean
+    return qlib.int8_quantize(0.02 * w)
+
+
+def loss_rows(M, N, dtype, spread, seed=2):
+    """softmax(logits) - onehot, as the cross entropy leaves it in the logits' gradient."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    p = torch.softmax(spread * torch.randn(M, N, generator=g, device="cuda"), 1)
+    p[torch.arange(M), torch.randint(N, (M,), generator=g, device="cuda")] -= 1
+    return p.to(DT[dtype])
+
+
+def row_errors(dx, dy, w):
+    """2-norm of each row's error over the row's own 2-norm, against 64 bits."""
+    want = (dy.double() * w.scales.double()) @ w.codes.double()
+    return (dx.double() - want).norm(dim=1) / want.norm(dim=1)
+
+
+# The fixed point may take as much as the output's own rounding: half a step of the type each
+# (a quarter of that in noise, half of it in errors of one direction, for weights whose mean is at
+# most their deviation).
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("mean", [0.0, 0.3, 1.0])
+@pytest.mark.parametrize("spread", [0.0, 1.0, 4.0])
+@pytest.mark.parametrize("M,N,K", [(3, 32000, 256), (5, 4096, 512), (200, 32000, 128), (700, 5003, 136), (3, 128256, 64),
+                                   (2, 1000, 64), (70, 131072, 24)])
+def test_input_gradient_of_a_loss(qlib, M, N, K, spread, mean, dtype):
+    if dtype == "fp16" and spread == 0 and N > 32000:
+        pytest.skip("1 / N is an fp16 subnormal there: nothing more than the case of 32000")
+    w = head(qlib, N, K, mean)
+    dy = loss_rows(M, N, dtype, spread)
+    assert row_errors(qlib.int8_matmul_backward(dy, w), dy, w).max() <= 2 * HALF[DT[dtype]]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("M,N,K,large", [(4, 28672, 256, 3000.0), (300, 11008, 512, 1000.0), (40, 4096, 100, 300.0),
+                                         (600, 28672, 64, 3000.0), (9, 4099, 72, 60000.0)])
+def test_input_gradient_of_rows_with_one_large_value(qlib, M, N, K, large, dtype):
+    """Every third row has a value far above the others, where its channel has few codes: what the
+    large value leaves of the others decides the result in most columns."""
+    w = head(qlib, N, K, 0.3)
+    w.codes[7, :K // 2] = 0
+    dy = rand(4, M, N, dtype="fp32")
+    dy[::3, 7] = large
+    dy = dy.to(DT[dtype])
+    dx = qlib.int8_matmul_backward(dy, w)
+    want = (dy.double() * w.scales.double()) @ w.codes.double()
+    err = (dx.double() - want)[:, :K // 2].norm(dim=1) / want[:, :K // 2].norm(dim=1)
+    # these columns hold none of the large value: the fixed point's share of the row's norm, which
+    # that value makes up to `ratio` times theirs, counts against them
+    D = dy.double() * w.scales.double()
+    rest = D.clone()
+    rest[:, 7] = 0
+    ratio = D.norm(dim=1) / rest.norm(dim=1)
+    half = HALF[DT[dtype]]
+    assert (err <= half + half * ratio).all()
+    assert row_errors(dx, dy, w).max() <= 2 * half
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+def test_input_gradient_of_equal_values(qlib, dtype):
+    """Values that all lie the same fraction of a step off: their errors have one sign."""
+    N, K = 1000, 64
+    w = qlib.Int8Rows(torch.randint(1, 100, (N, K), dtype=torch.int8, device="cuda"), torch.ones(N, device="cuda"))
+    dy = torch.full((3, N), -1e-3, device="cuda")
+    dy[0, 5], dy[1, 900], dy[2, 0] = 1.0, 1.0, 1.0
+    dy = dy.to(DT[dtype])
+    assert row_errors(qlib.int8_matmul_backward(dy, w), dy, w).max() <= 2 * HALF[DT[dtype]]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("N,K", [(3000, 264), (4099, 130)])
+def test_peaked_tokens_do_not_depend_on_their_batch(qlib, N, K, dtype):
+    """Peaked, ordinary, sparse, zero and NaN rows next to one another: each row's bits are its own."""
+    M = 2100
+    w = head(qlib, N, K, 0.5)
+    dy = rand(3, M, N, dtype=dtype)
+    dy[::5] = loss_rows(M // 5, N, dtype, 1.0)
+    dy[1::5] *= (torch.rand(M // 5, N, device="cuda", generator=torch.Generator(device="cuda").manual_seed(8)) < 0.1)
+    dy[2] = 0
+    dy[3, 17] = float("nan")
+    dy[700:1400] = rand(6, 700, N, dtype=dtype)     # a long run of ordinary rows
+    dx = qlib.int8_matmul_backward(dy, w)
+    assert torch.isnan(dx[3]).all() and not dx[2].any()
+    keep = torch.ones(M, dtype=torch.bool, device="cuda")
+    keep[2:4] = False
+    assert row_errors(dx[keep], dy[keep], w).max() <= 2 * HALF[DT[dtype]]
+    same = lambda a, b: torch.equal(a.view(torch.int16), b.view(torch.int16))   # noqa: E731
+    for m in (1, 2, 5, 40, 65, 130, 400, 900, 1500):
+        assert same(qlib.int8_matmul_backward(dy[:m], w), dx[:m]), m
+    for lo, hi in ((700, 1400), (1399, 1402), (5, 6), (650, 1405)):
+        assert same(qlib.int8_matmul_backward(dy[lo:hi].contiguous(), w), dx[lo:hi]), (lo, hi)
+
+
+def test_peaked_rows_at_every_offset_and_size(qlib):
+    """Peaked rows that start off 16-byte borders, with tiny and huge levels, guards around the result."""
+    for N, K, lo in ((1003, 40, 1), (2051, 33, 3), (17, 16, 5), (9001, 64, 7)):
+        w = head(qlib, N, K, 0.5)
+        M = 70
+        dy = torch.zeros(M * N + 16, dtype=torch.bfloat16, device="cuda")[lo:lo + M * N].view(M, N)
+        dy.copy_(loss_rows(M, N, "bf16", 2.0))
+        dy[1] *= 2.0 ** -90
+        dy[2] *= 2.0 ** 90
+        dy[3] *= 2.0 ** -118
+        buf = torch.full((M + 2, K), 5.0, dtype=torch.bfloat16, device="cuda")
+        dx = qlib.int8_matmul_backward(dy, w, out=buf[1:M + 1])
+        assert (buf[0] == 5).all() and (buf[M + 1] == 5).all()
+        # row 3's products of dY and the scale lie at 2^-129: fp32's unit there is 2^-149, 2^-20 of them
+        err = row_errors(dx, dy, w)
+        assert err.max() <= 2 * 2.0 ** -8, N
