@@ -389,7 +389,7 @@ int run_adapter_down(const Dims &d, const uint16_t *X, const uint16_t *A, uint16
 }
 
 // ---------------------------------------------------------------- 8-bit rows
-// The integer products sum up to 131072 terms of 127 * 128 in 32 bits.
+// The integer products sum up to 131072 terms of 128 * 128 in 32 bits (sum_float).
 constexpr int64_t kInt8MaxTerms = 131072;
 
 int check_rows8(const int8_rows_t *q) {

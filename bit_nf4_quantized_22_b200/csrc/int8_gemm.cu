@@ -103,9 +103,9 @@ __device__ __forceinline__ void tmem_wait(uint32_t (&v)[N]) {
     for (int o = 0; o < N; o += 16) asm volatile("" : QLORA_TIE16(v, o));
 }
 #undef QLORA_TIE16
-__device__ __forceinline__ int4 ld_cluster_int4(uint32_t addr) {
-    int4 v;
-    asm volatile("ld.shared::cluster.v4.s32 {%0,%1,%2,%3}, [%4];\n"
+__device__ __forceinline__ uint4 ld_cluster_uint4(uint32_t addr) {
+    uint4 v;
+    asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];\n"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "r"(addr));
     return v;
@@ -326,36 +326,36 @@ k_int8_tall(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     {
         // column c of plane d over the splits, 4 rows
         auto column = [&](int d, int c) {
-            int4 t = make_int4(0, 0, 0, 0);
+            uint4 t = make_uint4(0, 0, 0, 0);
             const uint32_t at = base + ((d * p.nt + c) * kTP + 4 * lane) * 4;
-            int4 v[kTMaxSplits];                  // all in flight: a peer's memory is far
+            uint4 v[kTMaxSplits];                 // all in flight: a peer's memory is far
 #pragma unroll
             for (uint32_t z = 0; z < kTMaxSplits; ++z)
-                if (z < splits) v[z] = ld_cluster_int4(mapa_shared(at, z));
+                if (z < splits) v[z] = ld_cluster_uint4(mapa_shared(at, z));
 #pragma unroll
             for (uint32_t z = 0; z < kTMaxSplits; ++z)
-                if (z < splits) t.x += v[z].x, t.y += v[z].y, t.z += v[z].z, t.w += v[z].w;
+                if (z < splits) t.x += v[z].x, t.y += v[z].y, t.z += v[z].z, t.w += v[z].w;   // mod 2^32
             return t;
         };
 #pragma unroll 4
         for (int c = (int)rank + warp * (int)splits; c < p.nt; c += (kTThreads / 32) * (int)splits) {
             const int64_t q = q0 + c;
             if (q >= p.Q) break;
-            int4 t = column(0, c);
-            float v[4] = {(float)t.x, (float)t.y, (float)t.z, (float)t.w};
+            uint4 t = column(0, c);
+            float v[4] = {sum_float(t.x), sum_float(t.y), sum_float(t.z), sum_float(t.w)};
             const bool four = p.planes == 4 && qdeep[c] != 0.f;
             if (DEEP && !four) continue;
             if (p.planes == 2 || (p.planes == 4 && !four)) {
                 // as k_int8_wide does, so that a token's gradient does not depend on its batch
                 t = column(1, c);
-                v[0] = join_digits(v[0], (float)t.x), v[1] = join_digits(v[1], (float)t.y);
-                v[2] = join_digits(v[2], (float)t.z), v[3] = join_digits(v[3], (float)t.w);
+                v[0] = join_digits(v[0], sum_float(t.x)), v[1] = join_digits(v[1], sum_float(t.y));
+                v[2] = join_digits(v[2], sum_float(t.z)), v[3] = join_digits(v[3], sum_float(t.w));
             } else if (p.planes > 2) {
-                int64_t sum[4] = {t.x, t.y, t.z, t.w};
+                int64_t sum[4] = {sum_int64(t.x), sum_int64(t.y), sum_int64(t.z), sum_int64(t.w)};
                 for (int d = 1; d < p.planes; ++d) {
                     t = column(d, c);
-                    sum[0] = sum[0] * 256 + t.x, sum[1] = sum[1] * 256 + t.y;
-                    sum[2] = sum[2] * 256 + t.z, sum[3] = sum[3] * 256 + t.w;
+                    sum[0] = sum[0] * 256 + sum_int64(t.x), sum[1] = sum[1] * 256 + sum_int64(t.y);
+                    sum[2] = sum[2] * 256 + sum_int64(t.z), sum[3] = sum[3] * 256 + sum_int64(t.w);
                 }
                 if (p.pool == 64) {
                     int64_t all = sum[0] + sum[1] + sum[2] + sum[3];
@@ -731,7 +731,7 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                                    __fmaf_rn(__fmul_rn(x.z, r), s4.z, b4.z), __fmaf_rn(__fmul_rn(x.w, r), s4.w, b4.w));
             };
             auto sums4 = [](const uint32_t *v) {
-                return make_float4((float)(int)v[0], (float)(int)v[1], (float)(int)v[2], (float)(int)v[3]);
+                return make_float4(sum_float(v[0]), sum_float(v[1]), sum_float(v[2]), sum_float(v[3]));
             };
             auto put4 = [](uint32_t *to, float4 v, auto dt) {
                 if constexpr (dt == QLORA_DTYPE_FP32) {

@@ -35,6 +35,12 @@ bool int8_gemv_takes(int64_t M, int64_t N, int64_t K);
 int launch_int8_gemv(const void *X, int x_dtype, int64_t ldx, const int8_rows_t &X8, const int8_rows_t &W,
                      const void *bias, void *Y, int dtype, uint32_t *d_status, cudaStream_t st);
 
+// An int32 sum of up to 131072 products of two codes.  They lie in (-2^31, 2^31]:
+// 2^31 itself, of codes that are all -128, wraps to -2^31, which no sum is.  Negated
+// both before and after the conversion it comes out right, and every other sum the same.
+__device__ __forceinline__ float sum_float(uint32_t v) { return -(float)(int)(0u - v); }
+__device__ __forceinline__ int64_t sum_int64(uint32_t v) { return -(int64_t)(int)(0u - v); }
+
 __device__ __forceinline__ float load_any(const void *p, int64_t i, int dtype) {
     if (dtype == QLORA_DTYPE_FP32) return __ldg(static_cast<const float *>(p) + i);
     return dec16(__ldg(static_cast<const uint16_t *>(p) + i), dtype == QLORA_DTYPE_FP16);

@@ -175,7 +175,7 @@ k_int8_gemv(const GemvParams p) {
         const int64_t row = n + (lane / MT) * warps;
         if (lane < RW * MT && m < p.M && row < p.N) {
             const float bs = p.bias ? load_any(p.bias, row, p.dtype) : 0.f;
-            const float v = __fmaf_rn(__fmul_rn((float)mine, sx[m]), __ldg(p.wscale + row), bs);
+            const float v = __fmaf_rn(__fmul_rn(sum_float((uint32_t)mine), sx[m]), __ldg(p.wscale + row), bs);
             const int64_t at = m * p.N + row;
             if (p.dtype == QLORA_DTYPE_FP32) static_cast<float *>(p.y)[at] = v;
             else static_cast<uint16_t *>(p.y)[at] = enc16(v, p.dtype == QLORA_DTYPE_FP16);

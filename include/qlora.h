@@ -261,7 +261,8 @@ int qlora_backward(const uint16_t *X, const uint16_t *dY, int64_t M, const nf4_w
  * bitsandbytes article (CSDN) section 4.1 (absmax INT8: s = 127 / max|x|, q =
  * round(s x)) and 4.2 (the vector-wise product: one scale for each row of the
  * input and each output channel of the weight).  One matrix of 8-bit rows:
- *   codes    [rows][ld] int8, the first cols of a row valid; 16-byte aligned
+ *   codes    [rows][ld] int8, the first cols of a row valid; 16-byte aligned.
+ *            int8_quantize writes -127 .. 127; rows made elsewhere may hold -128
  *   scales   [rows] fp32
  *   ld       bytes from one row to the next: >= cols, a multiple of 16 (of 128
  *            is read fastest)

@@ -5,7 +5,7 @@ each comment counts."""
 import pytest
 import torch
 
-from test_gpu_int8 import DT, HALF, rand
+from test_gpu_int8 import DT, HALF, layer_case, rand
 
 pytestmark = pytest.mark.gpu
 
@@ -124,3 +124,30 @@ def test_peaked_rows_at_every_offset_and_size(qlib):
         # row 3's products of dY and the scale lie at 2^-129: fp32's unit there is 2^-149, 2^-20 of them
         err = row_errors(dx, dy, w)
         assert err.max() <= 2 * 2.0 ** -8, N
+
+
+# ------------------------------------------------------------------------------ the code -128
+@pytest.mark.parametrize("M,N", [(1, 40), (2, 9), (3, 40), (130, 300), (700, 264)])
+def test_largest_sums_of_the_lowest_code(qlib, M, N):
+    """Rows made elsewhere may hold -128: 131072 terms of 2^14 are 2^31, one past a 32-bit integer."""
+    K = 131072
+    x8 = qlib.Int8Rows(torch.full((M, K), -128, dtype=torch.int8, device="cuda"), torch.ones(M, device="cuda"))
+    w8 = qlib.Int8Rows(torch.full((N, K), -128, dtype=torch.int8, device="cuda"), torch.ones(N, device="cuda"))
+    w8.codes[N // 2, 5] = 127
+    y = qlib.int8_matmul(x8, w8, dtype=torch.float32)
+    want = torch.full((M, N), 2.0 ** 31, device="cuda")
+    want[:, N // 2] = 2.0 ** 31 - 128 * 255
+    assert torch.equal(y, want)
+
+
+def test_largest_digit_sums_of_the_lowest_code(qlib):
+    """The same in the digits' products: M = 131072 tokens of codes -128 under equal gradients."""
+    M, K, N, r = 131072, 64, 8, 4
+    w, _, A, B, _ = layer_case(qlib, 1, K, N, r, 1, "bf16")
+    x8 = qlib.Int8Rows(torch.full((M, K), -128, dtype=torch.int8, device="cuda"), torch.ones(M, device="cuda"))
+    dy = rand(7, 1, N).expand(M, N).contiguous()
+    _, da, _ = qlib.backward(x8, dy, w, A, B, 8.0, need_dx=False, need_dB=False)
+    G = dy[:1].double() @ B.double().t()
+    want = (8.0 / r * -128.0 * M * G).expand(K, r)
+    # G's eight fp32 terms, half a 24-bit step, fp32 roundings
+    assert ((da.double() - want).abs() <= 2.0 ** -20 * (dy[:1].double().abs() @ B.double().abs().t()) * 128 * M * 8 / r).all()
