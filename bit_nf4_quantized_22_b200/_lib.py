@@ -21,7 +21,7 @@ EXPORTS = (
     "nf4_dequantize", "qlora_workspace_size", "qlora_forward", "qlora_backward",
     "qlora_launch_count", "qlora_profile_enable", "qlora_profile_reset", "qlora_profile_read",
     "qlora_profile_kinds", "qlora_profile_read_each",
-    "qlora_forward_noalloc", "qlora_merge", "qlora_selftest_wait_timeout", "nf4_dequantize_dtype",
+    "qlora_forward_noalloc", "qlora_merge", "qlora_selftest_wait_timeout", "qlora_selftest_turn_timeout", "nf4_dequantize_dtype",
     "nf4_codebook", "fp4_codebook", "int8_quantize", "int8_dequantize", "int8_matmul",
     "int8_matmul_backward_workspace_size", "int8_matmul_backward",
     "qlora_backward_int8_workspace_size", "qlora_backward_int8",
@@ -113,6 +113,8 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.qlora_forward_noalloc.argtypes = [P, i64, W, P, P, P, i32, ctypes.c_float, i32, P, P, P, P]
     lib.qlora_selftest_wait_timeout.restype = ctypes.c_int
     lib.qlora_selftest_wait_timeout.argtypes = [P, P]
+    lib.qlora_selftest_turn_timeout.restype = ctypes.c_int
+    lib.qlora_selftest_turn_timeout.argtypes = [P, P]
     lib.qlora_merge.restype = ctypes.c_int
     lib.qlora_merge.argtypes = [W, P, P, P, i32, ctypes.c_float, i32, P, P]
     lib.nf4_codebook.restype = ctypes.c_int

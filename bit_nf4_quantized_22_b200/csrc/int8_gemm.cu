@@ -694,7 +694,7 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
         const uint32_t lanes = (uint32_t)(32 * qt) << 16;
         const uint32_t free0 = mapa_shared(acc_free(0), 0);
         int i = 0;
-        for (int t = pair; t < tiles && ok; t += pairs, ++i) {
+        for (int t = pair; t < tiles; t += pairs, ++i) {   // all of them, also once a wait has given up
             int tm, tn;
             tile_at(p, t, tm, tn);
             const int64_t n0 = (int64_t)tn * 256;
@@ -710,9 +710,8 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                 const int64_t m = mrow + 256 * h;
                 rs[h] = m < p.M && (h == 0 || !p.digits) ? __ldcg(p.rscale + m) * p.mul : 0.f;
             }
-            asm volatile("bar.sync 1, 256;\n" ::: "memory");
-            ok = __all_sync(0xffffffffu, mbar_wait_cluster(acc_full, i & 1, abort_flag));
-            if (!ok) break;
+            ok = mbar_wait_turn<1, kWEpiThreads>(ok, acc_full, i & 1, abort_flag);   // cs and cb are there
+            if (!ok) continue;
             tc_fence_after();
             // The next tile's MMAs wait for the accumulators: a warp takes its 128
             // columns of one out at once and frees it before it scales, packs and

@@ -228,6 +228,18 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity,
     return false;
 }
 
+// One turn of THREADS threads that meet at a named barrier and then wait for
+// `bar`.  A warp whose wait has given up (ok false) goes on meeting the others
+// turn after turn without waiting again: they may not have given up, and a
+// barrier that a warp has left never fills.
+template <int BARRIER, int THREADS>
+__device__ __forceinline__ bool mbar_wait_turn(bool ok, uint32_t bar, uint32_t parity, volatile int *abort_flag) {
+    asm volatile("bar.sync %0, %1;\n" ::"n"(BARRIER), "n"(THREADS) : "memory");
+    if (ok) ok = __all_sync(0xffffffffu, mbar_wait_cluster(bar, parity, abort_flag));
+    if (!ok) *abort_flag = 1;
+    return ok;
+}
+
 // TMA tile load into this CTA's shared memory whose completion is counted on
 // an mbarrier of the pair's first CTA (`bar0` is a shared::cluster address).
 __device__ __forceinline__ void tma_load_2d_pair(uint32_t dst, const CUtensorMap *tm, int x, int y,

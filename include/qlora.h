@@ -390,6 +390,11 @@ int qlora_forward_noalloc(const uint16_t *X, int64_t M, const nf4_weight_t *q,
  * usable.  Returns EINVAL for a null status pointer. */
 int qlora_selftest_wait_timeout(uint32_t *d_status, void *stream);
 
+/* qlora_selftest_turn_timeout -- the same for warps that meet at a barrier turn
+ * after turn: one of eight has given up before the first turn, the others do in
+ * the second; all of them end. */
+int qlora_selftest_turn_timeout(uint32_t *d_status, void *stream);
+
 /* ---- Benchmark support (not part of the layer's computation) ----------
  * Kernel launches made by the library since the last qlora_profile_reset(). */
 int64_t qlora_launch_count(void);

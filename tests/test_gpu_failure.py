@@ -35,3 +35,18 @@ def test_bounded_wait_times_out_and_context_survives(orc, qlib):
 def test_selftest_rejects_null_status(qlib):
     lib = qlib.load()
     assert lib.qlora_selftest_wait_timeout(None, None) == QLORA_EINVAL
+
+
+def test_warps_in_turns_end_when_one_gave_up(qlib):
+    """A warp that has given up keeps meeting the others, which have not: the kernel ends and says so."""
+    lib = qlib.load()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert lib.qlora_selftest_turn_timeout(None, None) == QLORA_EINVAL
+    assert lib.qlora_selftest_turn_timeout(ctypes.c_void_p(status.data_ptr()), stream) == QLORA_OK
+    torch.cuda.synchronize()
+    assert int(status.item()) == STATUS_TIMEOUT
+    x8 = qlib.int8_quantize(torch.randn(1100, 200, device="cuda"))
+    y = qlib.int8_matmul(x8, x8, dtype=torch.float32)
+    want = ((x8.codes.double() @ x8.codes.double().t()).float() * x8.scales[:, None]) * x8.scales[None]
+    assert torch.equal(y, want)
