@@ -405,7 +405,11 @@ k_int8_row_digits(const void *Y, int64_t rows, int cols, const float *__restrict
 // Columns of S[t][j] (rows t < R, columns j < r; 16-bit or fp32), optionally
 // times f[t], in 24-bit fixed point with one step per column, as three digit
 // planes transposed to planes[d][j][t] (rows of ld bytes, rp rows a plane).
-// A step is max / 8355711: half of it is 6e-8 of the column's largest value.
+// A step is max / 8355711, and a value its nearest multiple, within half of it (6e-8
+// of the column's largest value): the product by the step's reciprocal, three
+// roundings of up to half a step each near the maximum, is corrected by what it
+// leaves of the value (1.7 steps at worst without).  Columns below 2^-100, whose step would
+// be subnormal and lose bits of its own, take a power of two.
 // rep = 64 writes each row's digits 64 times over (t -> 64 t .. 64 t + 63).
 // A cluster of 8 CTAs shares 8 columns: each finds the maxima of its rows,
 // keeping the values in shared memory (up to kColKeep rows; past them they are
@@ -478,9 +482,11 @@ k_int8_col_digits(const void *S, int64_t R, int r, const float *__restrict__ f, 
     const bool fin = m < 0x7f800000u;
     const float up = m < 0x21800000u ? 0x1p64f : 1.f;
     const float a = __uint_as_float(m) * up;
-    const float inv = fin && a > 0.f ? __fdiv_rn(kColMax, a) : 0.f;
-    if (blockIdx.y == 0 && tg == 0 && j0 + jc < rp)
-        steps[j0 + jc] = fin ? __fdiv_rn(a, kColMax) / up : __uint_as_float(0x7fffffffu);
+    // below 2^-100: the power of two with max / step in [2^21, 2^22), but no less than 2^-149
+    const int tiny = (int)(m >> 23) - 127 - 21 < -149 ? -149 : (int)(m >> 23) - 127 - 21;
+    const float unit = m < 0x0d800000u ? ldexpf(1.f, tiny + 64) : __fdiv_rn(a, kColMax);   // the step, times up
+    const float inv = fin && a > 0.f ? __fdiv_rn(1.f, unit) : 0.f;
+    if (blockIdx.y == 0 && tg == 0 && j0 + jc < rp) steps[j0 + jc] = fin ? unit / up : __uint_as_float(0x7fffffffu);
     const bool again = t1 - t0 > kColKeep;
     for (int64_t tb = t0; tb < t1; tb += kColKeep) {
         if (again) {
@@ -493,8 +499,10 @@ k_int8_col_digits(const void *S, int64_t R, int r, const float *__restrict__ f, 
             uint32_t d[3][2] = {};
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                const float x = inv > 0.f ? fminf(fmaxf(tile[jc][k + e] * up * inv, -kColMax), kColMax) : 0.f;
-                const int q = __float2int_rn(x);
+                const float v = tile[jc][k + e] * up;
+                const float t = inv > 0.f ? rintf(v * inv) : 0.f;
+                const float x = inv > 0.f ? t + rintf(__fmaf_rn(-t, unit, v) * inv) : 0.f;   // integers below 2^24: exact
+                const int q = __float2int_rn(fminf(fmaxf(x, -kColMax), kColMax));
                 const int b0 = (int)(int8_t)(uint8_t)q;
                 const int q1 = (q - b0) >> 8;
                 const int b1 = (int)(int8_t)(uint8_t)q1;

@@ -151,3 +151,25 @@ def test_largest_digit_sums_of_the_lowest_code(qlib):
     want = (8.0 / r * -128.0 * M * G).expand(K, r)
     # G's eight fp32 terms, half a 24-bit step, fp32 roundings
     assert ((da.double() - want).abs() <= 2.0 ** -20 * (dy[:1].double().abs() @ B.double().abs().t()) * 128 * M * 8 / r).all()
+
+
+# ------------------------------------------------------------------------------ the checkpoint
+@pytest.mark.parametrize("level", [0, -70, -105, -118])
+@pytest.mark.parametrize("seed", range(3))
+def test_column_digits_within_half_a_step(qlib, seed, level):
+    """dA of one token is its column's fixed point times codes of 1: within 0.51 of the step max / 8355711
+    and one fp32 rounding (2^-24 of the value, 2^-150), for G = dY exactly (B the identity); of columns
+    below 2^-100 the step is a power of two, at most max / 2^21."""
+    M, K, N, r = 8000, 8192, 8, 8
+    w, _, A, _, _ = layer_case(qlib, 1, K, N, r, 1, "bf16")
+    x8 = qlib.Int8Rows(torch.zeros(M, K, dtype=torch.int8, device="cuda"),
+                       torch.rand(M, generator=torch.Generator().manual_seed(seed)).cuda() + 0.5)
+    x8.scales.mul_(2.0 ** level)
+    k = torch.arange(M, device="cuda")
+    x8.codes[k, k] = 1                                 # feature k reads token k alone
+    dy = rand(seed, M, N)
+    B = torch.eye(N, device="cuda").bfloat16()
+    _, da, _ = qlib.backward(x8, dy, w, A, B, float(r), need_dx=False, need_dB=False)
+    want = dy.float() * x8.scales[:, None]             # the product in fp32, as it is cut
+    step = want.double().abs().amax(0) / (8355711 if level > -100 else 2 ** 21)
+    assert ((da[:M].double() - want.double()).abs() <= 0.51 * step + 2.0 ** -24 * want.double().abs() + 2.0 ** -150).all()
