@@ -455,7 +455,7 @@ size_t layout_grad8(int64_t M, const int8_rows_t &w, void *base, GradWs *out) {
     x.ld = round_up(w.rows, 128);   // whole lines: a TMA row off them takes two
     x.planes = b.take<int8_t>(4 * M * x.ld);
     x.steps = b.take<float>(M);
-    x.deep = b.take<uint8_t>(M);
+    x.deep = b.take<uint8_t>(round_up(M, 256));
     if (out) *out = x;
     return b.off;
 }

@@ -36,6 +36,8 @@ constexpr int kTSmemOne = 220 * 1024;
 
 // 256 * (a rounded upper sum) + the lower sum, in fp32: off by 2^-23 of the larger of the two terms
 __device__ __forceinline__ float join_digits(float upper, float lower) { return __fmaf_rn(upper, 256.f, lower); }
+// The same of the joined upper and lower pair of four digits.
+__device__ __forceinline__ float join_pairs(float upper, float lower) { return __fmaf_rn(upper, 65536.f, lower); }
 
 // kind::i8 instruction descriptor: signed 8-bit A and B, s32 accumulator.
 __host__ __device__ constexpr uint32_t idesc_i8(uint32_t m, uint32_t n, uint32_t a_mn, uint32_t b_mn) {
@@ -162,7 +164,8 @@ __device__ __forceinline__ bool any_deep(const uint8_t *flags, int64_t at, int n
 // DEEP: the second launch of an input gradient, for the tiles with a token of
 // four planes among them.  It leaves at once where there is none; else CTA y takes
 // tiles y, y + gridDim.y, .. and stores those tokens' columns alone.  Its ring
-// and accumulator run on from tile to tile.
+// and accumulator run on from tile to tile (512 x 4096 x 32000, 115 us for two
+// planes: none 2.7 us, one token 37, all 269, most of it the exchange of sums).
 template <bool DEEP>
 __global__ void __launch_bounds__(kTThreads)
 k_int8_tall(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const TallParams p) {
@@ -345,11 +348,20 @@ k_int8_tall(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             float v[4] = {sum_float(t.x), sum_float(t.y), sum_float(t.z), sum_float(t.w)};
             const bool four = p.planes == 4 && qdeep[c] != 0.f;
             if (DEEP && !four) continue;
-            if (p.planes == 2 || (p.planes == 4 && !four)) {
+            if (p.planes == 2 || p.planes == 4) {
                 // as k_int8_wide does, so that a token's gradient does not depend on its batch
-                t = column(1, c);
-                v[0] = join_digits(v[0], sum_float(t.x)), v[1] = join_digits(v[1], sum_float(t.y));
-                v[2] = join_digits(v[2], sum_float(t.z)), v[3] = join_digits(v[3], sum_float(t.w));
+                auto join = [&](float *u, uint4 l) {
+                    u[0] = join_digits(u[0], sum_float(l.x)), u[1] = join_digits(u[1], sum_float(l.y));
+                    u[2] = join_digits(u[2], sum_float(l.z)), u[3] = join_digits(u[3], sum_float(l.w));
+                };
+                join(v, column(1, c));
+                if (four) {
+                    t = column(2, c);
+                    float low[4] = {sum_float(t.x), sum_float(t.y), sum_float(t.z), sum_float(t.w)};
+                    join(low, column(3, c));
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = join_pairs(v[e], low[e]);
+                }
             } else if (p.planes > 2) {
                 int64_t sum[4] = {sum_int64(t.x), sum_int64(t.y), sum_int64(t.z), sum_int64(t.w)};
                 for (int d = 1; d < p.planes; ++d) {
@@ -413,7 +425,10 @@ k_int8_tall(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
 // A persistent kernel of CTA pairs for the products with tokens (y and dX):
 // tcgen05 cta_group::2, M = 256 token rows x N = 256 weight columns per MMA,
 // two accumulators a pair.  With one plane they hold two row blocks of a
-// 512 x 256 tile, with two the digits of one 256 x 256 tile.
+// 512 x 256 tile, with two the digits of one 256 x 256 tile.  DEEP: a tile with a row
+// of four planes among its 256 goes through in two passes, the upper pair of planes
+// and the lower; the upper sums wait in the epilogue's registers (4096 x 4096 x 11008
+// without such a row 225 us, one among them 282, all 469).
 // CTA r of the pair holds rows [128 r, +128) of each block and 128 of the
 // columns.  Warp 0 loads (its ring runs on into the next tile), warp 1 of CTA
 // 0 issues the MMAs, warps 4..11 take the sums out of TMEM, scale and store.
@@ -446,6 +461,7 @@ struct WideParams {
     int64_t ldo;
     int dtype, aligned;        // rows of the output start on 16-byte borders: TMA stores
     int pdl;
+    const uint8_t *deep;       // digits: rows with four planes have a 1 (zeros up to a multiple of 256)
     uint32_t *status;
 };
 
@@ -557,6 +573,16 @@ __device__ __forceinline__ void store_ragged(const WideParams &p, int64_t m0, in
         }
     }
 }
+// Is one of the 256 rows of a tile deep?  Eight flags a lane, loaded a tile ahead.
+__device__ __forceinline__ uint2 deep_flags(const WideParams &p, int t) {
+    if (t >= p.mt * p.nt) return make_uint2(0, 0);
+    int tm, tn;
+    tile_at(p, t, tm, tn);
+    return __ldcg(reinterpret_cast<const uint2 *>(p.deep + (int64_t)tm * 256) + (threadIdx.x & 31));
+}
+__device__ __forceinline__ bool any_flag(uint2 f) { return __any_sync(0xffffffffu, (f.x | f.y) != 0); }
+
+template <bool DEEP>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kWThreads, 1)
 k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
             const __grid_constant__ CUtensorMap tmY, const WideParams p) {
@@ -606,7 +632,8 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
     if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 40;\n");
         if (warp == 0) {
-            if (elect_one()) {
+            {
+                const bool leader = elect_one();
                 auto load_w = [&](int s, int t0, int tn) {
                     const uint32_t fa0 = mapa_shared(full(s), 0);
                     const int c0 = tn * 256 + 128 * (int)rank;
@@ -615,30 +642,44 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                     if (p.b_mn) tma_load_2d_pair(sb, &tmW, c0, t0, fa0);
                     else tma_load_2d_pair(sb, &tmW, t0, c0, fa0);
                 };
-                auto load_x = [&](int s, int t0, int tm) {
+                auto load_x = [&](int s, int t0, int tm, int pass) {
                     const uint32_t fa0 = mapa_shared(full(s), 0);
                     const uint32_t sa = base + s * kWStageBytes;
-                    const int r0 = tm * mrows + 128 * (int)rank;
+                    const int r0 = tm * mrows + 128 * (int)rank + (DEEP ? pass * 2 * (int)p.plane_rows : 0);
                     tma_load_2d_pair(sa, &tmX, t0, r0, fa0);
                     tma_load_2d_pair(sa + kWSlab, &tmX, t0, r0 + (p.digits ? (int)p.plane_rows : 256), fa0);
                 };
                 int it = 0, head = 0;
+                uint2 flags = make_uint2(0, 0);
                 for (int t = pair; t < tiles && ok; t += pairs) {
                     int tm, tn;
                     tile_at(p, t, tm, tn);
                     if (it == 0 && p.pdl) {
                         // the weight does not depend on the kernel before
                         head = p.nk < kWStages ? p.nk : kWStages;
-                        for (int k = 0; k < head; ++k) load_w(k, k * kTK, tn);
+                        if (leader)
+                            for (int k = 0; k < head; ++k) load_w(k, k * kTK, tn);
                         asm volatile("griddepcontrol.wait;\n" ::: "memory");
                     }
-                    for (int k = 0; k < p.nk && ok; ++k, ++it) {
-                        const int s = it % kWStages;
-                        if (it >= kWStages) ok = mbar_wait(empty(s), ((it / kWStages) & 1) ^ 1, abort_flag);
-                        if (!ok) break;
-                        if (it >= head) load_w(s, k * kTK, tn);
-                        load_x(s, k * kTK, tm);
+                    int passes = 1;
+                    if (DEEP) {
+                        if (it == 0) flags = deep_flags(p, t);
+                        passes = any_flag(flags) ? 2 : 1;
+                        flags = deep_flags(p, t + pairs);
                     }
+                    if (leader) {
+                        int i = it;
+                        for (int pass = 0; pass < passes && ok; ++pass)
+                            for (int k = 0; k < p.nk && ok; ++k, ++i) {
+                                const int s = i % kWStages;
+                                if (i >= kWStages) ok = mbar_wait(empty(s), ((i / kWStages) & 1) ^ 1, abort_flag);
+                                if (!ok) break;
+                                if (i >= head) load_w(s, k * kTK, tn);
+                                load_x(s, k * kTK, tm, pass);
+                            }
+                    }
+                    it += passes * p.nk;
+                    ok = __all_sync(0xffffffffu, ok);
                 }
                 if (!ok) *abort_flag = 1;
             }
@@ -652,8 +693,19 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                     umma_i8_pair_ktile(tmem + h * 256, dX + s * kStageD + h * kSlabD, dW + s * kStageD, bstep, idesc, acc);
                 };
                 static_assert((kWStages & (kWStages - 1)) == 0, "stage and parity from the running k-tile's bits");
-                uint32_t it = 0, i = 0;
-                for (int t = pair; t < tiles && ok; t += pairs, ++i) {
+                uint32_t it = 0, i = 0;                // k-tiles and passes before
+                uint2 flags = make_uint2(0, 0);
+                if (DEEP) {
+                    if (p.pdl) asm volatile("griddepcontrol.wait;\n" ::: "memory");
+                    flags = deep_flags(p, pair);
+                }
+                for (int t = pair; t < tiles && ok; t += pairs) {
+                  int passes = 1;
+                  if (DEEP) {
+                    passes = any_flag(flags) ? 2 : 1;
+                    flags = deep_flags(p, t + pairs);
+                  }
+                  for (int pass = 0; pass < passes && ok; ++pass, ++i) {
                     const uint32_t nk = p.nk, lead = nk < kWStages ? nk : kWStages;
                     if (i > 0) ok = __all_sync(0xffffffffu, mbar_wait_cluster(acc_free(0), (i - 1) & 1, abort_flag));
                     for (uint32_t k = 0; k < lead && ok; ++k) {
@@ -682,6 +734,7 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                     }
                     if (ok) umma_commit_pair_elect(acc_full, 0x3);
                     it += nk;
+                  }
                 }
                 if (!ok) *abort_flag = 1;
             }
@@ -694,9 +747,17 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
         const uint32_t lanes = (uint32_t)(32 * qt) << 16;
         const uint32_t free0 = mapa_shared(acc_free(0), 0);
         int i = 0;
+        uint32_t full_turns = 0;                               // passes before
+        uint2 flags = make_uint2(0, 0);
+        if (DEEP) flags = deep_flags(p, pair);
         for (int t = pair; t < tiles; t += pairs, ++i) {   // all of them, also once a wait has given up
             int tm, tn;
             tile_at(p, t, tm, tn);
+            bool two = false;
+            if (DEEP) {
+                two = any_flag(flags);
+                flags = deep_flags(p, t + pairs);
+            }
             const int64_t n0 = (int64_t)tn * 256;
             float *cs = cbuf + (i & 1) * 512, *cb = cs + 256;
             cs[e] = p.cscale && n0 + e < p.N ? __ldg(p.cscale + n0 + e) : 1.f;
@@ -710,8 +771,8 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                 const int64_t m = mrow + 256 * h;
                 rs[h] = m < p.M && (h == 0 || !p.digits) ? __ldcg(p.rscale + m) * p.mul : 0.f;
             }
-            ok = mbar_wait_turn<1, kWEpiThreads>(ok, acc_full, i & 1, abort_flag);   // cs and cb are there
-            if (!ok) continue;
+            ok = mbar_wait_turn<1, kWEpiThreads>(ok, acc_full, full_turns++ & 1, abort_flag);   // cs and cb are there
+            if (!ok && !(DEEP && two)) continue;
             tc_fence_after();
             // The next tile's MMAs wait for the accumulators: a warp takes its 128
             // columns of one out at once and frees it before it scales, packs and
@@ -741,6 +802,51 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                     to[1] = pack2(v.z, v.w, dt == QLORA_DTYPE_FP16);
                 }
             };
+            if constexpr (DEEP) {
+                if (two) {
+                    auto pairs16 = [&](int c, float (&v)[16]) {   // 16 columns of the two accumulators, joined
+                        uint32_t raw[32];
+                        tmem_ld16(tmem + lanes + c, *reinterpret_cast<uint32_t(*)[16]>(raw));
+                        tmem_ld16(tmem + lanes + 256 + c, *reinterpret_cast<uint32_t(*)[16]>(raw + 16));
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) v[j] = join_digits(sum_float(raw[j]), sum_float(raw[16 + j]));
+                    };
+                    float upper[8][16];
+                    if (ok) {
+#pragma unroll
+                        for (int g = 0; g < 8; ++g) pairs16(c0 + 16 * g, upper[g]);
+                        release(0), release(1);
+                    }
+                    ok = mbar_wait_turn<1, kWEpiThreads>(ok, acc_full, full_turns++ & 1, abort_flag);
+                    if (!ok) continue;
+                    tc_fence_after();
+                    const bool mine = mrow < p.M && __ldcg(p.deep + mrow) != 0;
+                    auto finish_two = [&](auto dt) {              // a 16-bit type: 32 columns a block
+                        uint32_t out[64];
+#pragma unroll
+                        for (int g = 0; g < 8; ++g) {
+                            float low[16];
+                            pairs16(c0 + 16 * g, low);
+                            if (g == 7) release(0), release(1);
+#pragma unroll
+                            for (int j = 0; j < 16; j += 4) {
+                                const float *u = upper[g] + j, *l = low + j;
+                                const float4 x = mine ? make_float4(join_pairs(u[0], l[0]), join_pairs(u[1], l[1]),
+                                                                    join_pairs(u[2], l[2]), join_pairs(u[3], l[3]))
+                                                      : make_float4(u[0], u[1], u[2], u[3]);
+                                put4(out + 8 * g + j / 2, scaled(c0 + 16 * g + j, x, rs[0]), dt);
+                            }
+                            const int64_t n = n0 + c0 + 32 * (g / 2);
+                            if (p.aligned && g % 2 == 1 && n < p.N && mblk < p.M)
+                                store_tile(&tmY, (int)(n * 2), (int)mblk, out + 8 * (g - 1), turn);
+                        }
+                        if (!p.aligned) store_ragged<false>(p, mblk, n0 + c0, out, turn_words);
+                    };
+                    if (p.dtype == QLORA_DTYPE_BF16) finish_two(std::integral_constant<int, QLORA_DTYPE_BF16>{});
+                    else finish_two(std::integral_constant<int, QLORA_DTYPE_FP16>{});
+                    continue;
+                }
+            }
             auto finish = [&](auto dt) {
                 constexpr bool f32 = dt == QLORA_DTYPE_FP32;
                 constexpr int per = f32 ? 1 : 2, cols = 16 * per, count = 128 / cols;   // a block's columns
@@ -812,7 +918,7 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
             };
             if (p.dtype == QLORA_DTYPE_BF16) finish(std::integral_constant<int, QLORA_DTYPE_BF16>{});
             else if (p.dtype == QLORA_DTYPE_FP16) finish(std::integral_constant<int, QLORA_DTYPE_FP16>{});
-            else finish(std::integral_constant<int, QLORA_DTYPE_FP32>{});
+            else if (!DEEP) finish(std::integral_constant<int, QLORA_DTYPE_FP32>{});   // gradients are 16-bit
         }
         if (lane == 0) bulk_wait_all();              // no memory of this CTA is read behind its end
         if (!ok) *abort_flag = 1;
@@ -978,8 +1084,9 @@ static int launch_int8_wide(const Int8Product &g, uint32_t *d_status, cudaStream
     const uintptr_t at = reinterpret_cast<uintptr_t>(g.out) | (uintptr_t)(g.ldo * (g.dtype == QLORA_DTYPE_FP32 ? 4 : 2));
     p.aligned = at % 16 == 0 && p.N < (1 << 29);          // a TMA coordinate in bytes
     p.pdl = g.pdl;
+    p.deep = g.deep;
     p.status = d_status;
-    const int64_t xrows = g.plane_rows * (g.planes - 1) + g.Q;
+    const int64_t xrows = g.plane_rows * (g.deep ? 3 : g.planes - 1) + g.Q;
     CUtensorMap tX, tW;
     bool ok = make_map(&tX, g.b, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, g.R, xrows, g.ldb, kTK, 128,
                        CU_TENSOR_MAP_SWIZZLE_128B);
@@ -993,7 +1100,8 @@ static int launch_int8_wide(const Int8Product &g, uint32_t *d_status, cudaStream
         ok = ok && make_map(&tY, g.out, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.N * size, p.M, g.ldo * size, 64, 32,
                             CU_TENSOR_MAP_SWIZZLE_64B);
     if (!ok) return QLORA_EUNSUPPORTED;
-    if (set_max_smem(reinterpret_cast<const void *>(k_int8_wide), kWSmemBytes) != cudaSuccess) return QLORA_ECUDA;
+    auto *k = g.deep ? k_int8_wide<true> : k_int8_wide<false>;
+    if (set_max_smem(reinterpret_cast<const void *>(k), kWSmemBytes) != cudaSuccess) return QLORA_ECUDA;
     const int64_t tiles = (int64_t)p.mt * p.nt, pairs = device_sms() / 2;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(2 * (tiles < pairs ? tiles : pairs)));
@@ -1005,7 +1113,7 @@ static int launch_int8_wide(const Int8Product &g, uint32_t *d_status, cudaStream
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = g.pdl ? 1 : 0;
-    if (cudaLaunchKernelEx(&cfg, k_int8_wide, tX, tW, tY, p) != cudaSuccess) return QLORA_ECUDA;
+    if (cudaLaunchKernelEx(&cfg, k, tX, tW, tY, p) != cudaSuccess) return QLORA_ECUDA;
     QLORA_LAUNCH_CHECK();
     return QLORA_OK;
 }
@@ -1016,9 +1124,9 @@ static int launch_int8_wide(const Int8Product &g, uint32_t *d_status, cudaStream
 // rows.  4096 tokens on 1024 x 1024: 14.1 us wide, 16.4 tall; 512 on 11008 x 4096: 29
 // and 45; 5 on 131072 x 128: 34 and 18; 384 on 11008 x 8192: 46 and 41; 4096 on 512 x
 // 4096: 26 and 17, as the model has them in order.
-// With deep tokens (which only the device knows): four planes for all of them in one
-// launch where that costs no more than a second launch, for the deep ones alone, does
-// (it finds none in 3 us).
+// With deep tokens (which only the device knows) the wide kernel takes the tiles that hold
+// one in two passes; few tokens have four planes for all of them in one launch of the tall one where
+// that costs no more than two planes and a second launch, for the deep ones alone (it finds none in 3 us).
 int launch_int8_product(const Int8Product &g, uint32_t *d_status, cudaStream_t st) {
     if (g.P <= 0 || g.Q <= 0) return QLORA_OK;
     const int nk = (int)((g.R + kTK - 1) / kTK);
@@ -1038,10 +1146,11 @@ int launch_int8_product(const Int8Product &g, uint32_t *d_status, cudaStream_t s
     }
     if (g.deep) {
         const TallPlan all = plan_tall(g, 4, g.Q, nk);
-        if (all.us <= us + 3.0 && (g.Q + all.nt - 1) / all.nt <= 65535)
+        if (all.us <= us + (wide ? 0.0 : 3.0) && (g.Q + all.nt - 1) / all.nt <= 65535)
             return launch_int8_tall(g, 4, all, false, d_status, st);
     }
-    const int rc = wide ? launch_int8_wide(g, d_status, st) : launch_int8_tall(g, g.planes, plan, false, d_status, st);
+    if (wide) return launch_int8_wide(g, d_status, st);
+    const int rc = launch_int8_tall(g, g.planes, plan, false, d_status, st);
     if (rc || !g.deep) return rc;
     return launch_int8_tall(g, 4, plan_tall(g, 4, g.Q < 64 ? g.Q : 64, nk), true, d_status, st);
 }

@@ -400,6 +400,8 @@ k_int8_row_digits(const void *Y, int64_t rows, int cols, const float *__restrict
             deep[m0 + i] = is_deep;
         }
     }
+    if (m0 + ROWS >= rows)    // zeros up to whole tiles of 256 rows
+        for (int64_t m = rows + threadIdx.x; m < (rows + 255) / 256 * 256; m += threads) deep[m] = 0;
 }
 
 // Columns of S[t][j] (rows t < R, columns j < r; 16-bit or fp32), optionally

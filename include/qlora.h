@@ -321,7 +321,7 @@ int int8_matmul(const void *X, int32_t x_dtype, int64_t ldx, const int8_rows_t *
  * values under 8 steps at most h / 4 of the token's 2-norm each, the roundings'
  * sum h / 2.  A token that would lose more (softmax - onehot over many
  * channels, one value far above the others) has 32 bits (a power of two, at
- * most max 2^-29), at about three times the cost.  Which of the two depends on
+ * most max 2^-29), at about twice the cost.  Which of the two depends on
  * the token and the channel scales alone.  A token of dY with a NaN or an infinity gets NaN.  The
  * frozen weight and the bias get no gradient here.
  *   dY    device [M, N] dense, dtype BF16 or FP16;  dX  device [M, K]
