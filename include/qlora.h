@@ -339,7 +339,10 @@ int int8_matmul_backward(const uint16_t *dY, int32_t dtype, int64_t M, const int
  *         G, the codes are read as they are, and the sums over them are exact
  *         integers (G's and A's columns in 24-bit fixed point).  May be shared
  *         by every layer that reads the same x.
- * The other arguments and results are qlora_backward's, dX among them.
+ * The other arguments and results are qlora_backward's.  dX is its dX up to the
+ * summation of G (emptied out of the tensor cores' accumulators more often
+ * here): the same bits while a split of G's sum has up to 12 k-tiles (Dout <=
+ * 768 at any M), else s G may round the other way in its 16 bits.
  * Errors: as qlora_backward; EINVAL when X8 is not [M, Din]; EUNSUPPORTED for
  * M or Din > 131072.  A T past fp16's range makes its row of dB NaN in fp16, as
  * in qlora_backward.  Workspace: qlora_backward_int8_workspace_size(),
