@@ -154,6 +154,68 @@ def test_largest_digit_sums_of_the_lowest_code(qlib):
 
 
 # ------------------------------------------------------------------------------ the checkpoint
+def checkpoint_formulas(x8, dy, A, B, alpha, T=None):
+    """(dA, dB) of an unpooled layer in 64 bits."""
+    s = alpha / A.shape[1]
+    xh = x8.codes.double() * x8.scales.double()[:, None]
+    T = xh @ A.double() if T is None else T.double()
+    G = dy.double() @ B.double().t()
+    return s * xh.t() @ G, s * T.t() @ dy.double()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("M,K,N,r", [(4096, 256, 11008, 16), (4096, 256, 11008, 64), (4096, 192, 11000, 24),
+                                     (4000, 128, 11008, 64), (3136, 64, 24576, 40), (4096, 64, 11008, 85),
+                                     (2048, 64, 28672, 256), (9000, 128, 1024, 24), (20000, 64, 2048, 8),
+                                     (12288, 64, 11008, 16)])
+def test_checkpoint_long_reductions(qlib, M, K, N, r, dtype):
+    """More k-tiles in a split of G and of dB than one accumulator takes (12), exact multiples of it and
+    others; ranks past 64; tokens past what the columns' digits keep.  dA and dB in the 2-norm: an
+    accumulator that rounds toward zero loses 1.3e-8 of the sum in each of 12 x 4 steps (6.3e-7), the sums
+    over turns and splits, up to 40 fp32 roundings in one chain, 2^-24 each at random (sqrt(40) 2^-24 =
+    3.8e-7), T's terms and the fixed point 2^-23 (1.2e-7): 1.2e-6.  An accumulator that is not taken out
+    loses 1.4e-6 (22 k-tiles) to 2.3e-6 (35) in one direction; a stale or lost one, the whole result."""
+    w, x, A, B, dy = layer_case(qlib, M, K, N, r, 1, dtype, seed=M + r)
+    x8 = qlib.int8_quantize(x)
+    T = (x8.codes.double() * x8.scales.double()[:, None] @ A.double()).float()
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    _, da, db = qlib.backward(x8, dy, w, A, B, 16.0, 1, T=T, need_dx=False, status=status)
+    assert int(status.item()) == 0
+    wantA, wantB = checkpoint_formulas(x8, dy, A, B, 16.0, T)
+    assert (da.double() - wantA).norm() <= 1.2e-6 * wantA.norm()
+    assert (db.double() - wantB).norm() <= 1.2e-6 * wantB.norm()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("M,K,r", [(40, 9024, 16), (300, 16448, 40), (17, 28672, 8)])
+def test_checkpoint_recomputes_T_of_long_rows(qlib, M, K, r, dtype):
+    """Unpooled inputs past the 8192 rows of A that its columns' digits keep in shared memory.  In the
+    2-norm: A's columns within half a 24-bit step (6e-8 of their maximum, under 3e-7 of a normal
+    column's values), four fp32 roundings in a chain, dB's and G's short sums (5 k-tiles: 2.6e-7)."""
+    N = 136
+    w, x, A, B, dy = layer_case(qlib, M, K, N, r, 1, dtype, seed=K)
+    x8 = qlib.int8_quantize(x)
+    _, da, db = qlib.backward(x8, dy, w, A, B, 16.0, 1, need_dx=False)
+    wantA, wantB = checkpoint_formulas(x8, dy, A, B, 16.0)
+    assert (da.double() - wantA).norm() <= 1.2e-6 * wantA.norm()
+    assert (db.double() - wantB).norm() <= 1.2e-6 * wantB.norm()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("M,N,r", [(4096, 11008, 16), (512, 4096, 85)])
+def test_checkpoint_dx_of_long_reductions(qlib, M, N, r, dtype):
+    """dX differs from qlora_backward's by G's summation alone: s G rounded the other way for a few of its
+    values (one step, two halves of it) and the result's own rounding the other way."""
+    w, x, A, B, dy = layer_case(qlib, M, 128, N, r, 1, dtype)
+    x8 = qlib.int8_quantize(x)
+    dx0, _, _ = qlib.backward(x, dy, w, A, B, 16.0, need_dA=False, need_dB=False)
+    dx, _, _ = qlib.backward(x8, dy, w, A, B, 16.0, need_dA=False, need_dB=False)
+    half = HALF[DT[dtype]]
+    sG = 16.0 / r * (dy.double() @ B.double().t()).abs()
+    assert ((dx.double() - dx0.double()).abs() <= 2 * half * (sG @ A.double().abs().t()) + 2 * half * dx0.double().abs()).all()
+    assert torch.isfinite(dx).all()
+
+
 @pytest.mark.parametrize("level", [0, -70, -105, -118])
 @pytest.mark.parametrize("seed", range(3))
 def test_column_digits_within_half_a_step(qlib, seed, level):
