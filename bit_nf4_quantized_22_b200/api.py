@@ -539,7 +539,7 @@ class QLoRALinear8BitInputFn(torch.autograd.Function):
 
 class Int8LinearFn(torch.autograd.Function):
     """int8_matmul of a bf16 or fp16 x with a gradient for x (straight through its rounding);
-    none for the frozen weight and bias."""
+    none for the frozen weight and bias: backward refuses a bias that requires one."""
 
     @staticmethod
     def forward(ctx, x, w: Int8Rows, bias=None):
@@ -551,4 +551,6 @@ class Int8LinearFn(torch.autograd.Function):
     @staticmethod
     @once_differentiable
     def backward(ctx, dy):
+        if any(ctx.needs_input_grad[2:]):
+            raise RuntimeError("bias: frozen, it gets no gradient here; pass bias.detach()")
         return int8_matmul_backward(dy.contiguous(), ctx.w), None, None

@@ -235,3 +235,18 @@ def test_column_digits_within_half_a_step(qlib, seed, level):
     want = dy.float() * x8.scales[:, None]             # the product in fp32, as it is cut
     step = want.double().abs().amax(0) / (8355711 if level > -100 else 2 ** 21)
     assert ((da[:M].double() - want.double()).abs() <= 0.51 * step + 2.0 ** -24 * want.double().abs() + 2.0 ** -150).all()
+
+
+# ------------------------------------------------------------------------------ autograd
+def test_bias_that_wants_a_gradient_is_refused(qlib):
+    """The frozen bias gets no gradient: one that asks for it must not go without in silence."""
+    w8 = qlib.int8_quantize(rand(2, 16, 64, dtype="fp32"))
+    x, bias = rand(1, 4, 64).requires_grad_(), rand(3, 16).requires_grad_()
+    with torch.no_grad():
+        y = qlib.Int8LinearFn.apply(x, w8, bias)
+    assert torch.equal(qlib.Int8LinearFn.apply(x, w8, bias.detach()), y)
+    with pytest.raises(RuntimeError, match="bias"):
+        qlib.Int8LinearFn.apply(x, w8, bias).sum().backward()
+    z = qlib.Int8LinearFn.apply(x, w8, bias.detach())
+    z.sum().backward()
+    assert torch.equal(x.grad, qlib.int8_matmul_backward(torch.ones_like(z), w8))
