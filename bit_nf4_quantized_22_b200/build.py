@@ -14,7 +14,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libqlora.so")
 SOURCES = ["api.cu", "codebook.cpp", "quantize.cu", "gemv.cu", "adapter.cu", "umma_gemm.cu", "profile.cu", "noalloc.cu", "umma_skinny.cu", "merge.cu", "selftest.cu", "int8_rows.cu", "int8_gemm.cu", "int8_gemv.cu"]
-HEADERS = ["common.cuh", "tcgen05.cuh", "int8_gemm.cuh", "int8_rows.cuh"]
+HEADERS = ["common.cuh", "tcgen05.cuh", "tcgen05_epilogue.cuh", "int8_gemm.cuh", "int8_rows.cuh"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",

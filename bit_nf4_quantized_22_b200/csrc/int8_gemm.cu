@@ -18,7 +18,7 @@
 #include <type_traits>
 
 #include "int8_gemm.cuh"
-#include "tcgen05.cuh"
+#include "tcgen05_epilogue.cuh"
 
 namespace qlora {
 namespace {

@@ -5,7 +5,7 @@
 // mbarrier nothing arrives on) so that a test can see the status word set
 // and the context still usable afterwards.
 #include "common.cuh"
-#include "tcgen05.cuh"
+#include "tcgen05_epilogue.cuh"
 
 namespace qlora {
 namespace {

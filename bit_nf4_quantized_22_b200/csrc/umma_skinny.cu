@@ -21,7 +21,7 @@
 // of a split operand with it, in registers with rounding to nearest, while the
 // SM's other CTA keeps the tensor core busy.
 #include "common.cuh"
-#include "tcgen05.cuh"
+#include "tcgen05_epilogue.cuh"
 
 namespace qlora {
 
