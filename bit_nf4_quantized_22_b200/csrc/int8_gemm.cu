@@ -166,7 +166,9 @@ __device__ __forceinline__ bool any_deep(const uint8_t *flags, int64_t at, int n
 // tiles y, y + gridDim.y, .. and stores those tokens' columns alone.  Its ring
 // and accumulator run on from tile to tile (512 x 4096 x 32000, 115 us for two
 // planes: none 2.7 us, one token 37, all 269, most of it the exchange of sums).
-template <bool DEEP>
+// FOUR: all tokens with four planes, in one launch. Both are kernels of their own: their
+// columns' registers (188 for 126) would leave one CTA an SM to every product.
+template <bool FOUR, bool DEEP>
 __global__ void __launch_bounds__(kTThreads)
 k_int8_tall(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB, const TallParams p) {
     extern __shared__ __align__(1024) uint8_t smem_raw[];
@@ -281,7 +283,7 @@ k_int8_tall(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
         if (p.pdl) asm volatile("griddepcontrol.wait;\n" ::: "memory");
         for (int c = threadIdx.x - 64; c < p.nt; c += kTThreads - 64)   // not the read-only path: may be the kernel before's
             qs[c] = q0 + c < p.Q ? __ldcg(p.qscale + q0 + c) * p.mul : 0.f;
-        if (p.planes == 4)
+        if (FOUR)
             for (int c = threadIdx.x - 64; c < p.nt; c += kTThreads - 64)
                 qdeep[c] = q0 + c < p.Q && __ldcg(p.deep + q0 + c) ? 1.f : 0.f;
         ok = __all_sync(0xffffffffu, ok && mbar_wait(acc_bar, tile & 1, abort_flag));
@@ -346,9 +348,9 @@ k_int8_tall(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
             if (q >= p.Q) break;
             uint4 t = column(0, c);
             float v[4] = {sum_float(t.x), sum_float(t.y), sum_float(t.z), sum_float(t.w)};
-            const bool four = p.planes == 4 && qdeep[c] != 0.f;
+            const bool four = FOUR && qdeep[c] != 0.f;
             if (DEEP && !four) continue;
-            if (p.planes == 2 || p.planes == 4) {
+            if (FOUR || p.planes == 2) {
                 // as k_int8_wide does, so that a token's gradient does not depend on its batch
                 auto join = [&](float *u, uint4 l) {
                     u[0] = join_digits(u[0], sum_float(l.x)), u[1] = join_digits(u[1], sum_float(l.y));
@@ -747,7 +749,7 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
         const uint32_t lanes = (uint32_t)(32 * qt) << 16;
         const uint32_t free0 = mapa_shared(acc_free(0), 0);
         int i = 0;
-        uint32_t full_turns = 0;                               // passes before
+        uint32_t full_turns = 0;                               // DEEP: passes before
         uint2 flags = make_uint2(0, 0);
         if (DEEP) flags = deep_flags(p, pair);
         for (int t = pair; t < tiles; t += pairs, ++i) {   // all of them, also once a wait has given up
@@ -771,7 +773,7 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                 const int64_t m = mrow + 256 * h;
                 rs[h] = m < p.M && (h == 0 || !p.digits) ? __ldcg(p.rscale + m) * p.mul : 0.f;
             }
-            ok = mbar_wait_turn<1, kWEpiThreads>(ok, acc_full, full_turns++ & 1, abort_flag);   // cs and cb are there
+            ok = mbar_wait_turn<1, kWEpiThreads>(ok, acc_full, (DEEP ? full_turns++ : (uint32_t)i) & 1, abort_flag);   // cs and cb are there
             if (!ok && !(DEEP && two)) continue;
             tc_fence_after();
             // The next tile's MMAs wait for the accumulators: a warp takes its 128
@@ -791,7 +793,8 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                                    __fmaf_rn(__fmul_rn(x.z, r), s4.z, b4.z), __fmaf_rn(__fmul_rn(x.w, r), s4.w, b4.w));
             };
             auto sums4 = [](const uint32_t *v) {
-                return make_float4(sum_float(v[0]), sum_float(v[1]), sum_float(v[2]), sum_float(v[3]));
+                if constexpr (DEEP) return make_float4(sum_float(v[0]), sum_float(v[1]), sum_float(v[2]), sum_float(v[3]));
+                return make_float4((float)(int)v[0], (float)(int)v[1], (float)(int)v[2], (float)(int)v[3]);
             };
             auto put4 = [](uint32_t *to, float4 v, auto dt) {
                 if constexpr (dt == QLORA_DTYPE_FP32) {
@@ -989,7 +992,7 @@ static TallPlan plan_tall(const Int8Product &g, int planes, int64_t Q, int nk) {
     return best;
 }
 
-// only_deep: the launch of k_int8_tall<true>, after the product of two planes has run.
+// only_deep: the launch of its DEEP form, after the product of two planes has run.
 static int launch_int8_tall(const Int8Product &g, int planes, const TallPlan &plan, bool only_deep, uint32_t *d_status,
                             cudaStream_t st) {
     if (g.P <= 0 || g.Q <= 0) return QLORA_OK;
@@ -1036,7 +1039,7 @@ static int launch_int8_tall(const Int8Product &g, int planes, const TallPlan &pl
     const size_t ring = (size_t)p.stages * p.stage_bytes;
     if (ring < (size_t)N * kTP * 4) return QLORA_EUNSUPPORTED;   // the sums take the ring's place
     const int smem = (int)ring + 1024 + 256 + 1024;
-    auto *k = only_deep ? k_int8_tall<true> : k_int8_tall<false>;
+    auto *k = only_deep ? k_int8_tall<true, true> : planes == 4 ? k_int8_tall<true, false> : k_int8_tall<false, false>;
     if (set_max_smem(reinterpret_cast<const void *>(k), smem) != cudaSuccess) return QLORA_ECUDA;
     cudaLaunchConfig_t cfg{};
     const int64_t tiles_p = (g.P + kTP - 1) / kTP;
@@ -1133,7 +1136,9 @@ int launch_int8_product(const Int8Product &g, uint32_t *d_status, cudaStream_t s
     const TallPlan plan = plan_tall(g, g.planes, g.Q, nk);
     bool wide = false;
     double us = plan.us;
-    if (!g.q_inner && g.planes <= 2) {
+    // a product (not a gradient) of 131072 terms stays with the tall kernel: the wide one converts its
+    // sums without sum_float, which costs it registers (7253 x 560 x 12160: 78 us for 77)
+    if (!g.q_inner && g.planes <= 2 && (g.R < 131072 || g.deep)) {
         const int64_t mrows = g.planes == 2 ? 256 : 512, pairs = device_sms() / 2;
         const int64_t tiles = ((g.Q + mrows - 1) / mrows) * ((g.P + 255) / 256);
         const int64_t rounds = (tiles + pairs - 1) / pairs;
