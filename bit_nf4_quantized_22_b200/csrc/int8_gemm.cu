@@ -501,8 +501,9 @@ __device__ __forceinline__ void tile_at(const WideParams &p, int t, int &tm, int
 // A warp's block of 32 rows x 64 bytes of finished values, lane l with 16 words of
 // row l, goes out as a TMA store from `turn` (the warp's own 2 KB, swizzled): it
 // leaves while the next block is converted (926 x 212 x 10448: 15 us, stored by the
-// lanes 20).  18 bytes a cycle and SM leave so: products of short
-// reductions are bound by it (7253 x 560 x 12160: 84 us for 176 MB of results).
+// lanes 20).  Products of short reductions wait for their results (7253 x 560 x
+// 12160: 76 us for 176 MB of them, about 8 bytes a cycle and SM; what holds them
+// at half of what the memory takes is not known).
 __device__ __forceinline__ void store_tile(const CUtensorMap *tm, int x, int y, const uint32_t *w, uint32_t turn) {
     const int lane = threadIdx.x & 31;
     if (lane == 0) bulk_wait_read();                 // the block before is out of `turn`

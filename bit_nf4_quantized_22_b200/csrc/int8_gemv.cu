@@ -213,9 +213,9 @@ int pick_rows(const GemvParams &p, bool fused, cudaStream_t st) {
 }  // namespace
 
 // Against the tall kernel at 16 tokens (one MMA width serves them all): one and
-// two tokens are faster here at every size (4096 x 4096: 6.4 and 7.4 us, there
-// 8.5; 8192 x 28672: 40.8 us, there 42.7), three and four on small weights alone
-// (1024 x 1024: 5.4, there 7.2; 4096 x 11008: 15.6, there 12.5).
+// two tokens are faster here at every size (rows given, cold weights, 4096 x 4096:
+// 5.5 and 6.2 us, there 8.0; 8192 x 28672: 37.9 and 38.6, there 41.7), three and four
+// on small weights alone (1024 x 1024: 3.6, there 4.9; 4096 x 11008: 15.6, there 11.4).
 bool int8_gemv_takes(int64_t M, int64_t N, int64_t K) {
     return M * ((K + 511) / 512 * 512) <= kGemvTokenBytes && (M <= 2 || (M <= 4 && N * K <= (int64_t)8 << 20));
 }

@@ -265,9 +265,10 @@ __device__ __noinline__ bool deep_row(const char *row, int cols, const float *__
 }
 
 // ROWS rows a CTA: the scales, read for the maxima and again for the digits, are
-// most of the traffic inside the SM, and two rows share them (4096 x 11008: 37 us,
-// one row 41).  64 registers, for two CTAs an SM of long rows too (4258 x 14856: 46
-// us, with 78 registers 67).
+// most of the traffic inside the SM, and two rows share them.  64 registers, for two
+// CTAs an SM of long rows too.  4096 x 11008: 51 us, 127 where all rows take four planes;
+// what DigitLoss sums costs 14 of them (37 us without, one row a CTA 41; 4258 x 14856: 66
+// us, 46 without, 67 with 78 registers).
 template <int DT, bool FULL, int STEPS, int ROWS>
 __global__ void __launch_bounds__(STEPS == 4 ? 512 : 1024, STEPS == 4 ? 2 : 1)
 k_int8_row_digits(const void *Y, int64_t rows, int cols, const float *__restrict__ cscale,

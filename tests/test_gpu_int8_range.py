@@ -108,6 +108,36 @@ def test_peaked_tokens_do_not_depend_on_their_batch(qlib, N, K, dtype):
         assert same(qlib.int8_matmul_backward(dy[lo:hi].contiguous(), w), dx[lo:hi]), (lo, hi)
 
 
+@pytest.mark.parametrize("M,N,K", [(30, 2000, 320), (300, 3000, 520), (1100, 3000, 264)])
+def test_peaked_tokens_at_replay(qlib, M, N, K):
+    """One captured call (one launch of four planes, two launches, passes of tiles) on a stream of its own
+    takes its tokens' fixed point from the values at replay, with one workspace for two graphs."""
+    w = head(qlib, N, K, 0.3)
+    plain, peaked = rand(3, M, N), loss_rows(M, N, "bf16", 1.0)
+    mixed = plain.clone()
+    mixed[M // 2] = peaked[0]
+    want = [qlib.int8_matmul_backward(d, w) for d in (plain, peaked, mixed)]
+    need = 4 * M * ((N + 127) // 128 * 128) + 8 * M + 4096
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    dy = plain.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        assert torch.equal(qlib.int8_matmul_backward(dy, w, workspace=ws), want[0])
+    torch.cuda.current_stream().wait_stream(side)
+    graphs, outs = [], []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(qlib.int8_matmul_backward(dy, w, workspace=ws))
+        graphs.append(g)
+    for i, d in enumerate((plain, peaked, mixed, plain, mixed, peaked)):
+        dy.copy_(d)
+        graphs[i & 1].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[i & 1], want[(0, 1, 2, 0, 2, 1)[i]]), i
+
+
 def test_peaked_rows_at_every_offset_and_size(qlib):
     """Peaked rows that start off 16-byte borders, with tiny and huge levels, guards around the result."""
     for N, K, lo in ((1003, 40, 1), (2051, 33, 3), (17, 16, 5), (9001, 64, 7)):
