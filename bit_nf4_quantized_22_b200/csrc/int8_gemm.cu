@@ -245,176 +245,176 @@ k_int8_tall(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUt
     uint32_t tile = 0;                             // tiles before this one
 #pragma unroll 1
     for (int64_t y = blockIdx.y; !DEEP || y < p.tiles_q; y += gridDim.y) {
-    if (DEEP) {
-        q0 = y * p.nt;
-        if (!any_deep(p.deep, q0, p.nt, p.Q)) continue;   // the same for all CTAs of the cluster
-    }
-    if (warp == 0) {
-        if (leader) {
-            for (int i = head; i < nloc && ok; ++i) {
-                if (!DEEP || round > 0) ok = mbar_wait(empty_bar(s), (round & 1) ^ 1, abort_flag);
+        if (DEEP) {
+            q0 = y * p.nt;
+            if (!any_deep(p.deep, q0, p.nt, p.Q)) continue;   // the same for all CTAs of the cluster
+        }
+        if (warp == 0) {
+            if (leader) {
+                for (int i = head; i < nloc && ok; ++i) {
+                    if (!DEEP || round > 0) ok = mbar_wait(empty_bar(s), (round & 1) ^ 1, abort_flag);
+                    if (!ok) break;
+                    load_a(i, s);
+                    load_b(i, s);
+                    if (++s == S) s = 0, ++round;
+                }
+                if (!ok) *abort_flag = 1;
+            }
+        } else if (warp == 1) {
+            const uint32_t idesc = idesc_i8(kTP, (uint32_t)N, p.a_mn ? 1u : 0u, 0u);
+            // K-major: rows of 128 t, 8-row groups 1 KB apart, a step of 32 t
+            // advances 32 B.  MN-major: rows of 128 p, 8 t a 1 KB group, a step
+            // of 32 t advances 4 KB (one 128-wide atom, so no leading stride).
+            const uint64_t astep = p.a_mn ? 256u : 2u;
+            const uint64_t bdiff = kTABytes >> 4, sdiff = p.stage_bytes >> 4;
+            uint64_t ad = sdesc(base, 16, 1024) + s * sdiff;
+            for (int i = 0; i < nloc && ok; ++i) {
+                ok = __all_sync(0xffffffffu, mbar_wait(full_bar(s), round & 1, abort_flag));   // the warp stays together
                 if (!ok) break;
-                load_a(i, s);
-                load_b(i, s);
-                if (++s == S) s = 0, ++round;
+                tc_fence_after();
+                umma_i8_ktile(tmem, ad, ad + bdiff, astep, 2, idesc, i > 0 ? 1u : 0u);
+                umma_commit_elect(empty_bar(s));
+                ad += sdiff;
+                if (++s == S) s = 0, ++round, ad = sdesc(base, 16, 1024);
             }
-            if (!ok) *abort_flag = 1;
-        }
-    } else if (warp == 1) {
-        const uint32_t idesc = idesc_i8(kTP, (uint32_t)N, p.a_mn ? 1u : 0u, 0u);
-        // K-major: rows of 128 t, 8-row groups 1 KB apart, a step of 32 t
-        // advances 32 B.  MN-major: rows of 128 p, 8 t a 1 KB group, a step
-        // of 32 t advances 4 KB (one 128-wide atom, so no leading stride).
-        const uint64_t astep = p.a_mn ? 256u : 2u;
-        const uint64_t bdiff = kTABytes >> 4, sdiff = p.stage_bytes >> 4;
-        uint64_t ad = sdesc(base, 16, 1024) + s * sdiff;
-        for (int i = 0; i < nloc && ok; ++i) {
-            ok = __all_sync(0xffffffffu, mbar_wait(full_bar(s), round & 1, abort_flag));   // the warp stays together
-            if (!ok) break;
-            tc_fence_after();
-            umma_i8_ktile(tmem, ad, ad + bdiff, astep, 2, idesc, i > 0 ? 1u : 0u);
-            umma_commit_elect(empty_bar(s));
-            ad += sdiff;
-            if (++s == S) s = 0, ++round, ad = sdesc(base, 16, 1024);
-        }
-        if (ok) umma_commit_elect(acc_bar);
-        else *abort_flag = 1;
-    } else {
-        if (p.pdl) asm volatile("griddepcontrol.wait;\n" ::: "memory");
-        for (int c = threadIdx.x - 64; c < p.nt; c += kTThreads - 64)   // not the read-only path: may be the kernel before's
-            qs[c] = q0 + c < p.Q ? __ldcg(p.qscale + q0 + c) * p.mul : 0.f;
-        if (FOUR)
-            for (int c = threadIdx.x - 64; c < p.nt; c += kTThreads - 64)
-                qdeep[c] = q0 + c < p.Q && __ldcg(p.deep + q0 + c) ? 1.f : 0.f;
-        ok = __all_sync(0xffffffffu, ok && mbar_wait(acc_bar, tile & 1, abort_flag));
-        if (ok) {
-            // TMEM -> the idle ring, as int32 [column][128 rows]
-            tc_fence_after();
-            const int qt = warp & 3;
-            for (int c = 0; c < N; c += 16) {
-                uint32_t v[16];
-                tmem_ld16(tmem + ((uint32_t)(32 * qt) << 16) + c, v);
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-                    *reinterpret_cast<uint32_t *>(gen_base + ((c + i) * kTP + 32 * qt + lane) * 4) = v[i];
-            }
+            if (ok) umma_commit_elect(acc_bar);
+            else *abort_flag = 1;
         } else {
-            *abort_flag = 1;
-        }
-    }
-
-    if (!ok && p.status) atomicOr(p.status, QLORA_STATUS_TIMEOUT);
-    __syncwarp();
-    tc_fence_before();
-    __syncthreads();
-    if (DEEP && warp == 0 && lane == 0 && *abort_flag) {
-        // a wait gave up: time (tens of milliseconds) for this CTA's copies to land
-        for (uint32_t i = 0; i < 20000; ++i) __nanosleep(1000);
-    } else if (!DEEP && warp == 0 && lane == 0 && *abort_flag) {
-        // a wait gave up: let this CTA's copies land before its shared memory is released
-        for (int s = 0; s < S && s < nloc; ++s) {
-            const int last = ((nloc - 1 - s) / S) * S + s;
-            for (uint32_t i = 0; i < kWaitLimit; ++i)
-                if (mbar_try_wait(full_bar(s), (last / S) & 1)) break;
-        }
-    }
-    __syncwarp();
-    const int64_t prow = p0 + 4 * lane;
-    float ps[4], bs[4];
+            if (p.pdl) asm volatile("griddepcontrol.wait;\n" ::: "memory");
+            for (int c = threadIdx.x - 64; c < p.nt; c += kTThreads - 64)   // not the read-only path: may be the kernel before's
+                qs[c] = q0 + c < p.Q ? __ldcg(p.qscale + q0 + c) * p.mul : 0.f;
+            if (FOUR)
+                for (int c = threadIdx.x - 64; c < p.nt; c += kTThreads - 64)
+                    qdeep[c] = q0 + c < p.Q && __ldcg(p.deep + q0 + c) ? 1.f : 0.f;
+            ok = __all_sync(0xffffffffu, ok && mbar_wait(acc_bar, tile & 1, abort_flag));
+            if (ok) {
+                // TMEM -> the idle ring, as int32 [column][128 rows]
+                tc_fence_after();
+                const int qt = warp & 3;
+                for (int c = 0; c < N; c += 16) {
+                    uint32_t v[16];
+                    tmem_ld16(tmem + ((uint32_t)(32 * qt) << 16) + c, v);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const bool in = prow + e < p.P;
-        ps[e] = in && p.pscale ? __ldg(p.pscale + prow + e) : 1.f;
-        bs[e] = in && p.bias ? load_any(p.bias, prow + e, p.dtype) : 0.f;
-    }
-    cluster_sync();   // the cluster's sums are in shared memory
-    {
-        // column c of plane d over the splits, 4 rows
-        auto column = [&](int d, int c) {
-            uint4 t = make_uint4(0, 0, 0, 0);
-            const uint32_t at = base + ((d * p.nt + c) * kTP + 4 * lane) * 4;
-            uint4 v[kTMaxSplits];                 // all in flight: a peer's memory is far
-#pragma unroll
-            for (uint32_t z = 0; z < kTMaxSplits; ++z)
-                if (z < splits) v[z] = ld_cluster_uint4(mapa_shared(at, z));
-#pragma unroll
-            for (uint32_t z = 0; z < kTMaxSplits; ++z)
-                if (z < splits) t.x += v[z].x, t.y += v[z].y, t.z += v[z].z, t.w += v[z].w;   // mod 2^32
-            return t;
-        };
-#pragma unroll 4
-        for (int c = (int)rank + warp * (int)splits; c < p.nt; c += (kTThreads / 32) * (int)splits) {
-            const int64_t q = q0 + c;
-            if (q >= p.Q) break;
-            uint4 t = column(0, c);
-            float v[4] = {sum_float(t.x), sum_float(t.y), sum_float(t.z), sum_float(t.w)};
-            const bool four = FOUR && qdeep[c] != 0.f;
-            if (DEEP && !four) continue;
-            if (FOUR || p.planes == 2) {
-                // as k_int8_wide does, so that a token's gradient does not depend on its batch
-                auto join = [&](float *u, uint4 l) {
-                    u[0] = join_digits(u[0], sum_float(l.x)), u[1] = join_digits(u[1], sum_float(l.y));
-                    u[2] = join_digits(u[2], sum_float(l.z)), u[3] = join_digits(u[3], sum_float(l.w));
-                };
-                join(v, column(1, c));
-                if (four) {
-                    t = column(2, c);
-                    float low[4] = {sum_float(t.x), sum_float(t.y), sum_float(t.z), sum_float(t.w)};
-                    join(low, column(3, c));
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) v[e] = join_pairs(v[e], low[e]);
-                }
-            } else if (p.planes > 2) {
-                int64_t sum[4] = {sum_int64(t.x), sum_int64(t.y), sum_int64(t.z), sum_int64(t.w)};
-                for (int d = 1; d < p.planes; ++d) {
-                    t = column(d, c);
-                    sum[0] = sum[0] * 256 + sum_int64(t.x), sum[1] = sum[1] * 256 + sum_int64(t.y);
-                    sum[2] = sum[2] * 256 + sum_int64(t.z), sum[3] = sum[3] * 256 + sum_int64(t.w);
-                }
-                if (p.pool == 64) {
-                    int64_t all = sum[0] + sum[1] + sum[2] + sum[3];
-#pragma unroll
-                    for (int x = 8; x > 0; x /= 2) all += __shfl_xor_sync(0xffffffffu, all, x);
-                    if ((lane & 15) == 0 && prow < p.P)
-                        static_cast<float *>(p.out)[prow / 64 * p.ldo + q] = __fmul_rn(__ll2float_rn(all), qs[c]);
-                    continue;
-                }
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = __ll2float_rn(sum[e]);
-            }
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = __fmaf_rn(__fmul_rn(v[e], qs[c]), ps[e], bs[e]);
-            if (p.q_inner) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if (prow + e < p.P) static_cast<float *>(p.out)[(prow + e) * p.ldo + q] = v[e];
-            } else if (p.dtype == QLORA_DTYPE_FP32) {
-                float *o = static_cast<float *>(p.out) + q * p.ldo + prow;
-                if (p.vec && prow + 4 <= p.P) {
-                    *reinterpret_cast<float4 *>(o) = make_float4(v[0], v[1], v[2], v[3]);
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (prow + e < p.P) o[e] = v[e];
+                    for (int i = 0; i < 16; ++i)
+                        *reinterpret_cast<uint32_t *>(gen_base + ((c + i) * kTP + 32 * qt + lane) * 4) = v[i];
                 }
             } else {
-                const bool f16 = p.dtype == QLORA_DTYPE_FP16;
-                uint16_t *o = static_cast<uint16_t *>(p.out) + q * p.ldo + prow;
-                if (p.vec && prow + 4 <= p.P) {
-                    *reinterpret_cast<uint2 *>(o) = make_uint2(pack2(v[0], v[1], f16), pack2(v[2], v[3], f16));
-                } else {
+                *abort_flag = 1;
+            }
+        }
+
+        if (!ok && p.status) atomicOr(p.status, QLORA_STATUS_TIMEOUT);
+        __syncwarp();
+        tc_fence_before();
+        __syncthreads();
+        if (DEEP && warp == 0 && lane == 0 && *abort_flag) {
+            // a wait gave up: time (tens of milliseconds) for this CTA's copies to land
+            for (uint32_t i = 0; i < 20000; ++i) __nanosleep(1000);
+        } else if (!DEEP && warp == 0 && lane == 0 && *abort_flag) {
+            // a wait gave up: let this CTA's copies land before its shared memory is released
+            for (int s = 0; s < S && s < nloc; ++s) {
+                const int last = ((nloc - 1 - s) / S) * S + s;
+                for (uint32_t i = 0; i < kWaitLimit; ++i)
+                    if (mbar_try_wait(full_bar(s), (last / S) & 1)) break;
+            }
+        }
+        __syncwarp();
+        const int64_t prow = p0 + 4 * lane;
+        float ps[4], bs[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const bool in = prow + e < p.P;
+            ps[e] = in && p.pscale ? __ldg(p.pscale + prow + e) : 1.f;
+            bs[e] = in && p.bias ? load_any(p.bias, prow + e, p.dtype) : 0.f;
+        }
+        cluster_sync();   // the cluster's sums are in shared memory
+        {
+            // column c of plane d over the splits, 4 rows
+            auto column = [&](int d, int c) {
+                uint4 t = make_uint4(0, 0, 0, 0);
+                const uint32_t at = base + ((d * p.nt + c) * kTP + 4 * lane) * 4;
+                uint4 v[kTMaxSplits];                 // all in flight: a peer's memory is far
+#pragma unroll
+                for (uint32_t z = 0; z < kTMaxSplits; ++z)
+                    if (z < splits) v[z] = ld_cluster_uint4(mapa_shared(at, z));
+#pragma unroll
+                for (uint32_t z = 0; z < kTMaxSplits; ++z)
+                    if (z < splits) t.x += v[z].x, t.y += v[z].y, t.z += v[z].z, t.w += v[z].w;   // mod 2^32
+                return t;
+            };
+#pragma unroll 4
+            for (int c = (int)rank + warp * (int)splits; c < p.nt; c += (kTThreads / 32) * (int)splits) {
+                const int64_t q = q0 + c;
+                if (q >= p.Q) break;
+                uint4 t = column(0, c);
+                float v[4] = {sum_float(t.x), sum_float(t.y), sum_float(t.z), sum_float(t.w)};
+                const bool four = FOUR && qdeep[c] != 0.f;
+                if (DEEP && !four) continue;
+                if (FOUR || p.planes == 2) {
+                    // as k_int8_wide does, so that a token's gradient does not depend on its batch
+                    auto join = [&](float *u, uint4 l) {
+                        u[0] = join_digits(u[0], sum_float(l.x)), u[1] = join_digits(u[1], sum_float(l.y));
+                        u[2] = join_digits(u[2], sum_float(l.z)), u[3] = join_digits(u[3], sum_float(l.w));
+                    };
+                    join(v, column(1, c));
+                    if (four) {
+                        t = column(2, c);
+                        float low[4] = {sum_float(t.x), sum_float(t.y), sum_float(t.z), sum_float(t.w)};
+                        join(low, column(3, c));
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) v[e] = join_pairs(v[e], low[e]);
+                    }
+                } else if (p.planes > 2) {
+                    int64_t sum[4] = {sum_int64(t.x), sum_int64(t.y), sum_int64(t.z), sum_int64(t.w)};
+                    for (int d = 1; d < p.planes; ++d) {
+                        t = column(d, c);
+                        sum[0] = sum[0] * 256 + sum_int64(t.x), sum[1] = sum[1] * 256 + sum_int64(t.y);
+                        sum[2] = sum[2] * 256 + sum_int64(t.z), sum[3] = sum[3] * 256 + sum_int64(t.w);
+                    }
+                    if (p.pool == 64) {
+                        int64_t all = sum[0] + sum[1] + sum[2] + sum[3];
+#pragma unroll
+                        for (int x = 8; x > 0; x /= 2) all += __shfl_xor_sync(0xffffffffu, all, x);
+                        if ((lane & 15) == 0 && prow < p.P)
+                            static_cast<float *>(p.out)[prow / 64 * p.ldo + q] = __fmul_rn(__ll2float_rn(all), qs[c]);
+                        continue;
+                    }
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) v[e] = __ll2float_rn(sum[e]);
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] = __fmaf_rn(__fmul_rn(v[e], qs[c]), ps[e], bs[e]);
+                if (p.q_inner) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        if (prow + e < p.P) o[e] = enc16(v[e], f16);
+                        if (prow + e < p.P) static_cast<float *>(p.out)[(prow + e) * p.ldo + q] = v[e];
+                } else if (p.dtype == QLORA_DTYPE_FP32) {
+                    float *o = static_cast<float *>(p.out) + q * p.ldo + prow;
+                    if (p.vec && prow + 4 <= p.P) {
+                        *reinterpret_cast<float4 *>(o) = make_float4(v[0], v[1], v[2], v[3]);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (prow + e < p.P) o[e] = v[e];
+                    }
+                } else {
+                    const bool f16 = p.dtype == QLORA_DTYPE_FP16;
+                    uint16_t *o = static_cast<uint16_t *>(p.out) + q * p.ldo + prow;
+                    if (p.vec && prow + 4 <= p.P) {
+                        *reinterpret_cast<uint2 *>(o) = make_uint2(pack2(v[0], v[1], f16), pack2(v[2], v[3], f16));
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            if (prow + e < p.P) o[e] = enc16(v[e], f16);
+                    }
                 }
             }
         }
-    }
-    __syncwarp();
-    if (DEEP) fence_proxy_async();                 // the ring's next copies come after these reads
-    cluster_sync();   // no CTA leaves, or fills its ring again, while a peer reads its sums
-    if (!DEEP) break;
-    ++tile;
+        __syncwarp();
+        if (DEEP) fence_proxy_async();                 // the ring's next copies come after these reads
+        cluster_sync();   // no CTA leaves, or fills its ring again, while a peer reads its sums
+        if (!DEEP) break;
+        ++tile;
     }
     if (warp == 1) {
         tc_fence_after();
@@ -703,41 +703,41 @@ k_int8_wide(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUt
                     flags = deep_flags(p, pair);
                 }
                 for (int t = pair; t < tiles && ok; t += pairs) {
-                  int passes = 1;
-                  if (DEEP) {
-                    passes = any_flag(flags) ? 2 : 1;
-                    flags = deep_flags(p, t + pairs);
-                  }
-                  for (int pass = 0; pass < passes && ok; ++pass, ++i) {
-                    const uint32_t nk = p.nk, lead = nk < kWStages ? nk : kWStages;
-                    if (i > 0) ok = __all_sync(0xffffffffu, mbar_wait_cluster(acc_free(0), (i - 1) & 1, abort_flag));
-                    for (uint32_t k = 0; k < lead && ok; ++k) {
-                        const uint32_t s = (it + k) % kWStages;
-                        ok = __all_sync(0xffffffffu, mbar_wait_cluster(full(s), ((it + k) / kWStages) & 1, abort_flag));
+                    int passes = 1;
+                    if (DEEP) {
+                        passes = any_flag(flags) ? 2 : 1;
+                        flags = deep_flags(p, t + pairs);
+                    }
+                    for (int pass = 0; pass < passes && ok; ++pass, ++i) {
+                        const uint32_t nk = p.nk, lead = nk < kWStages ? nk : kWStages;
+                        if (i > 0) ok = __all_sync(0xffffffffu, mbar_wait_cluster(acc_free(0), (i - 1) & 1, abort_flag));
+                        for (uint32_t k = 0; k < lead && ok; ++k) {
+                            const uint32_t s = (it + k) % kWStages;
+                            ok = __all_sync(0xffffffffu, mbar_wait_cluster(full(s), ((it + k) / kWStages) & 1, abort_flag));
+                            if (!ok) break;
+                            tc_fence_after();
+                            mma(s, 0, k > 0 ? 1u : 0u);
+                        }
+                        if (ok && i > 0) ok = __all_sync(0xffffffffu, mbar_wait_cluster(acc_free(1), (i - 1) & 1, abort_flag));
                         if (!ok) break;
                         tc_fence_after();
-                        mma(s, 0, k > 0 ? 1u : 0u);
+                        for (uint32_t k = 0; k < lead; ++k) {
+                            const uint32_t s = (it + k) % kWStages;
+                            mma(s, 1, k > 0 ? 1u : 0u);
+                            umma_commit_pair_elect(empty(s), 0x3);
+                        }
+                        for (uint32_t k = lead; k < nk; ++k) {
+                            const uint32_t s = (it + k) % kWStages;
+                            ok = __all_sync(0xffffffffu, mbar_wait_cluster(full(s), ((it + k) / kWStages) & 1, abort_flag));
+                            if (!ok) break;
+                            tc_fence_after();
+                            mma(s, 0, 1u);
+                            mma(s, 1, 1u);
+                            umma_commit_pair_elect(empty(s), 0x3);
+                        }
+                        if (ok) umma_commit_pair_elect(acc_full, 0x3);
+                        it += nk;
                     }
-                    if (ok && i > 0) ok = __all_sync(0xffffffffu, mbar_wait_cluster(acc_free(1), (i - 1) & 1, abort_flag));
-                    if (!ok) break;
-                    tc_fence_after();
-                    for (uint32_t k = 0; k < lead; ++k) {
-                        const uint32_t s = (it + k) % kWStages;
-                        mma(s, 1, k > 0 ? 1u : 0u);
-                        umma_commit_pair_elect(empty(s), 0x3);
-                    }
-                    for (uint32_t k = lead; k < nk; ++k) {
-                        const uint32_t s = (it + k) % kWStages;
-                        ok = __all_sync(0xffffffffu, mbar_wait_cluster(full(s), ((it + k) / kWStages) & 1, abort_flag));
-                        if (!ok) break;
-                        tc_fence_after();
-                        mma(s, 0, 1u);
-                        mma(s, 1, 1u);
-                        umma_commit_pair_elect(empty(s), 0x3);
-                    }
-                    if (ok) umma_commit_pair_elect(acc_full, 0x3);
-                    it += nk;
-                  }
                 }
                 if (!ok) *abort_flag = 1;
             }
